@@ -403,6 +403,124 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
                                  const float *q, const void *k_cache, const void *v_cache,
                                  const int32_t *ctx_len, float *out, void *stream);
 
+/*
+ * Packed rows over a caller-owned paged cache: the three steps of an attention block for a
+ * batch in which every sequence brings its own number of new tokens -- append their keys
+ * and values (with the position rotation), attend to the cache, or attend to a whole prompt
+ * that is not cached.  (kasahare 0.4.0 / simple-llm, "Architecture": RoPE(q, k, pos), then
+ * attn = softmax(q . k^T / sqrt(d_head)) . v with GQA; "Inside nanochat Part 4:
+ * Understanding Inference", Continuous Batching: sequences of different lengths share a
+ * batch.)  They need no context: weights, cache and lengths are the caller's.
+ *
+ * The rows (tokens) of all sequences lie one behind the other.  Row i of sequence s is packed
+ * row row_start[s] + i and stands at position p = ctx_len[s] + i; rows [row_start[s],
+ * row_start[s + 1]) are the sequence's (none: the sequence has no new token).  Rows before
+ * row_start[0] and from row_start[nseq] on belong to no sequence: nothing of theirs is read
+ * into a result and nothing is written for them.
+ *
+ * The lengths are device memory and are read when the work runs, so a captured graph can be
+ * replayed with new lengths, page tables and data in the same buffers.  The kernels check
+ * them: `status` (device int32[1], set to 0 by the caller at first) collects bits,
+ *   SLM_ROWS_TIMEOUT  a bounded wait inside the kernel ran out: the results are invalid;
+ *   SLM_ROWS_PAGE     a page id outside [0, n_pages) was needed: an append writes nothing for
+ *                     that row; an attention reads page 0 in its place, so the results of
+ *                     that sequence are meaningless;
+ *   SLM_ROWS_LENGTH   row_start does not ascend within [0, rows], a ctx_len is negative, or a
+ *                     position lies outside the page table (or the rotation table): an append
+ *                     writes nothing for such a row; an attention gives meaningless results
+ *                     for that sequence.
+ * No call reads or writes outside its buffers because of a length or a page id.
+ *
+ * Requirements of all three: nseq in [1, 1024]; n_heads % n_kv_heads == 0; head_dim a multiple
+ * of 8 in [8, 256]; q, k, v, out and the cache 16-byte aligned; row strides (*_ld, in elements,
+ * from one packed row to the next) of at least heads * head_dim and a multiple of 16 bytes, so
+ * q, k and v may be column ranges of one projection's output; heads of a row are adjacent.
+ * rows = 0 is allowed and does nothing.  Every pointer but the structs themselves is device
+ * memory of the current device (checked).  The calls are asynchronous on `stream`, allocate
+ * nothing and may be captured.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED, SLM_ECUDA; the text is
+ * in slm_last_error(NULL).
+ */
+typedef struct {
+    void *k, *v;                /* device [n_pages][n_kv_heads][page_size][head_dim] of kv_dtype   */
+    const int32_t *page_table;  /* device int32 [nseq][table_ld]: page of positions
+                                   [i * page_size, (i + 1) * page_size) of sequence s; entries past
+                                   a sequence's last position are not read                         */
+    int32_t n_pages, page_size; /* page_size: a power of two in [16, 2^20]                         */
+    int32_t table_ld;           /* entries per sequence                                            */
+    int32_t n_kv_heads, head_dim, kv_dtype; /* SLM_F32 or SLM_BF16                                 */
+} slm_kv_cache;
+
+typedef struct {
+    const int32_t *row_start;   /* device int32 [nseq + 1], ascending                              */
+    const int32_t *ctx_len;     /* device int32 [nseq]: positions cached before the new rows; NULL:
+                                   none                                                            */
+    int32_t nseq, rows;         /* rows: packed rows that the buffers hold (>= row_start[nseq])    */
+} slm_rows;
+
+enum { SLM_ROWS_TIMEOUT = 1, SLM_ROWS_PAGE = 2, SLM_ROWS_LENGTH = 4 };
+
+/*
+ * slm_kv_append -- write the keys and values of the packed rows into the cache, position
+ * ctx_len[s] + i of sequence s, rotating keys (and queries) on the way.
+ *   dtype: SLM_F32 or SLM_BF16, the type of k, v [rows][n_kv_heads][head_dim] and q
+ *     [rows][n_heads][head_dim].  The cache may have the other type: the rotation is done in
+ *     fp32 and every value is rounded once, to nearest even, as it is stored.
+ *   rope: device fp32 [rope_len][head_dim / 2][2] = (cos, sin) of position and pair, pairs
+ *     (j, j + head_dim / 2) as everywhere in this library; NULL: nothing is rotated (k, v and q
+ *     are copied), and rope_len is ignored.
+ *   q, q_out: both NULL (n_heads is ignored), or the rows' queries and where they go rotated,
+ *     [rows][n_heads][head_dim] of the cache's type, which is what slm_attention_paged takes.
+ *     q_out may be q itself when the types and strides are equal; other overlaps of inputs and
+ *     outputs are not allowed.
+ *   Two rows must not go to the same cache position (a page that two sequences share may not
+ *   be written through either).
+ */
+int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
+                  const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_heads, const void *q,
+                  int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status, void *stream);
+
+/*
+ * slm_attention_rows_workspace_bytes -- bytes of workspace for slm_attention_paged and
+ * slm_attention_prompt at this shape on the current device, whatever the lengths are; 0 for
+ * arguments that they refuse, or without a device.
+ */
+size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t nseq, int32_t n_heads,
+                                          int32_t n_kv_heads, int32_t head_dim);
+
+/*
+ * slm_attention_paged -- attention of the packed rows over the paged cache, which already holds
+ * their own keys and values (slm_kv_append): for every row at position p of sequence s and query
+ * head h, with kv head g = h / (n_heads / n_kv_heads),
+ *     out[row][h] = sum_t softmax_t(q[row][h] . k[s][g][t] / sqrt(head_dim)) v[s][g][t],  t = 0..p.
+ * One new row per sequence is a decode step; many are a chunk of a prompt; a batch may mix both.
+ *   q, out: [rows][n_heads][head_dim] of the cache's type.  q as given (already rotated).
+ *   n_heads / n_kv_heads at most 64 (32 for head_dim > 128), else SLM_EUNSUPPORTED.
+ *   workspace: device memory, 256-byte aligned, of slm_attention_rows_workspace_bytes(kv_dtype,
+ *     rows, nseq, ...) bytes.  It needs no initialisation and carries nothing from call to call;
+ *     the call owns it until its work has finished, so calls that may overlap (two streams, two
+ *     graphs replayed at once) need one each.
+ *   Scores, the softmax and its sums are fp32.  The same call with the same inputs gives the
+ *   same bits.
+ *   Keys and values that no row of a call sees (cache slots past a sequence's last position,
+ *   other sequences' pages) may hold anything, infinities and NaN included.  Non-finite values
+ *   at a position that some rows see and earlier rows of the same sequence do not may reach those
+ *   earlier rows.
+ */
+int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q, int64_t q_ld,
+                        void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
+                        void *stream);
+
+/*
+ * slm_attention_prompt -- causal attention over whole prompts: as slm_attention_paged, with the
+ * keys and values of the same packed rows in the place of a cache (ctx_len must be NULL).
+ *   dtype: SLM_F32 or SLM_BF16, the type of q, out [rows][n_heads][head_dim] and k, v
+ *     [rows][n_kv_heads][head_dim].
+ */
+int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                         const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
+                         void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif

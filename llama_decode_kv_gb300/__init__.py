@@ -42,8 +42,21 @@ class slm_config(ctypes.Structure):
                 ("kv_page_size", ctypes.c_int32), ("kv_pages", ctypes.c_int32)]
 
 
+class slm_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "page_size", "table_ld", "n_kv_heads", "head_dim", "kv_dtype")]
+
+
+class slm_rows(ctypes.Structure):
+    _fields_ = [("row_start", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p), ("nseq", ctypes.c_int32),
+                ("rows", ctypes.c_int32)]
+
+
+SLM_ROWS_TIMEOUT, SLM_ROWS_PAGE, SLM_ROWS_LENGTH = 1, 2, 4
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _SIGS = {
     "slm_create": (ctypes.c_int, [ctypes.POINTER(slm_config), _P, ctypes.c_size_t, ctypes.POINTER(_P)]),
     "slm_prefill": (ctypes.c_int, [_P, _I32, _P, _I32, _P, _P, _P]),
@@ -73,6 +86,11 @@ _SIGS = {
     "slm_attention_noalloc_max_bytes": (ctypes.c_size_t, []),
     "slm_attention_decode_noalloc": (ctypes.c_int, [_I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
                                                     _P, _P, _P]),
+    "slm_kv_append": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, _I32, _I32, _P, _I64, _P, _I64, _P, _P]),
+    "slm_attention_rows_workspace_bytes": (ctypes.c_size_t, [_I32] * 6),
+    "slm_attention_paged": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "slm_attention_prompt": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                            ctypes.c_size_t, _P, _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -134,6 +152,118 @@ def attention_decode_noalloc(q, k_cache, v_cache, ctx_len, out, kv_dtype: int, s
     lens = (ctypes.c_int32 * B)(*[int(x) for x in ctx_len])
     return slm_attention_decode_noalloc(B, H, KV, hd, cap, kv_dtype, _ptr(q), _ptr(k_cache),
                                         _ptr(v_cache), lens, _ptr(out), _stream_ptr(stream))
+
+
+def _dtype_code(t) -> int:
+    """SLM_F32 / SLM_BF16 of a torch dtype."""
+    name = str(t)
+    if name == "torch.float32":
+        return SLM_F32
+    if name == "torch.bfloat16":
+        return SLM_BF16
+    raise ValueError(f"{name}: the packed-row calls take float32 and bfloat16")
+
+
+def _heads(x, name: str, heads: int, head_dim: int, rows: int, dtype):
+    """Row stride (elements) of a [rows][heads][head_dim] tensor whose heads are adjacent."""
+    if x.dtype != dtype or tuple(x.shape) != (rows, heads, head_dim):
+        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected {(rows, heads, head_dim)} {dtype}")
+    ld, h, d = x.stride()
+    if rows and ((d != 1 and head_dim > 1) or (h != head_dim and heads > 1)):
+        raise ValueError(f"{name}: the heads of a row must be adjacent (strides {x.stride()})")
+    return ld if rows > 1 else heads * head_dim
+
+
+def _ints(x, name: str, *shape):
+    if str(x.dtype) != "torch.int32" or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected contiguous int32 {shape}")
+    return x.data_ptr()
+
+
+def _packed(row_start, ctx_len, rows: int) -> slm_rows:
+    nseq = row_start.shape[0] - 1
+    return slm_rows(_ints(row_start, "row_start", nseq + 1),
+                    None if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
+
+
+def _cache(k_cache, v_cache, page_table, nseq: int) -> slm_kv_cache:
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must be [pages][kv heads][page size][head_dim] of one shape and type")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
+    pages, kv, page, hd = k_cache.shape
+    ld = page_table.shape[-1]
+    return slm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), _ints(page_table, "page_table", nseq, ld), pages, page,
+                        ld, kv, hd, _dtype_code(k_cache.dtype))
+
+
+def _rows_check(rc: int, what: str):
+    if rc != 0:
+        raise SlmError(rc, what, slm_last_error(None).decode())
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, rope=None, q=None, q_out=None,
+              stream=None) -> None:
+    """slm_kv_append over torch tensors of the current device: write the packed rows k, v
+    [rows][kv heads][head_dim] into the paged cache [pages][kv heads][page size][head_dim] at
+    positions ctx_len[s] + i (ctx_len None: from 0), rotated by rope [positions][head_dim / 2][2]
+    when given; q [rows][heads][head_dim] is rotated into q_out (the cache's type).  Row strides
+    are free.  status: int32[1] collecting SLM_ROWS_* bits.  Raises SlmError / ValueError."""
+    rows, kv, hd = k.shape
+    r = _packed(row_start, ctx_len, rows)
+    c = _cache(k_cache, v_cache, page_table, r.nseq)
+    dt = _dtype_code(k.dtype)
+    if c.n_kv_heads != kv or c.head_dim != hd:
+        raise ValueError(f"k holds {kv} heads of {hd}, the cache {c.n_kv_heads} of {c.head_dim}")
+    k_ld, v_ld = _heads(k, "k", kv, hd, rows, k.dtype), _heads(v, "v", kv, hd, rows, k.dtype)
+    n_rope, heads, q_ld, o_ld = 0, 0, 0, 0
+    if rope is not None:
+        if str(rope.dtype) != "torch.float32" or tuple(rope.shape[1:]) != (hd // 2, 2) or not rope.is_contiguous():
+            raise ValueError(f"rope: {tuple(rope.shape)} {rope.dtype}, expected contiguous float32 [n][{hd // 2}][2]")
+        n_rope = rope.shape[0]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        heads = q.shape[1]
+        q_ld, o_ld = _heads(q, "q", heads, hd, rows, k.dtype), _heads(q_out, "q_out", heads, hd, rows, k_cache.dtype)
+    _rows_check(slm_kv_append(ctypes.byref(c), ctypes.byref(r), dt, _ptr(k), k_ld, _ptr(v), v_ld, _ptr(rope), n_rope,
+                              heads, _ptr(q), q_ld, _ptr(q_out), o_ld, _ints(status, "status", 1), _stream_ptr(stream)),
+                "slm_kv_append")
+
+
+def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """slm_attention_rows_workspace_bytes; dtype is a torch dtype."""
+    return int(slm_attention_rows_workspace_bytes(_dtype_code(dtype), rows, nseq, n_heads, n_kv_heads, head_dim))
+
+
+def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream=None) -> None:
+    """slm_attention_paged over torch tensors of the current device: out[row][h] = attention of
+    the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
+    already holds the rows' own keys and values).  workspace: uint8 tensor of
+    attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
+    rows, heads, hd = q.shape
+    r = _packed(row_start, ctx_len, rows)
+    c = _cache(k_cache, v_cache, page_table, r.nseq)
+    if c.head_dim != hd:
+        raise ValueError(f"q has heads of {hd}, the cache of {c.head_dim}")
+    q_ld, o_ld = _heads(q, "q", heads, hd, rows, k_cache.dtype), _heads(out, "out", heads, hd, rows, k_cache.dtype)
+    _rows_check(slm_attention_paged(ctypes.byref(c), ctypes.byref(r), heads, _ptr(q), q_ld, _ptr(out), o_ld,
+                                    _ptr(workspace), workspace.nbytes, _ints(status, "status", 1), _stream_ptr(stream)),
+                "slm_attention_paged")
+
+
+def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) -> None:
+    """slm_attention_prompt over torch tensors of the current device: causal attention of the
+    packed prompts q [rows][heads][head_dim], k, v [rows][kv heads][head_dim] into out.
+    Raises SlmError / ValueError."""
+    rows, heads, hd = q.shape
+    kv = k.shape[1]
+    r = _packed(row_start, None, rows)
+    q_ld, o_ld = _heads(q, "q", heads, hd, rows, q.dtype), _heads(out, "out", heads, hd, rows, q.dtype)
+    k_ld, v_ld = _heads(k, "k", kv, hd, rows, q.dtype), _heads(v, "v", kv, hd, rows, q.dtype)
+    _rows_check(slm_attention_prompt(ctypes.byref(r), _dtype_code(q.dtype), heads, kv, hd, _ptr(q), q_ld, _ptr(k), k_ld,
+                                     _ptr(v), v_ld, _ptr(out), o_ld, _ptr(workspace), workspace.nbytes,
+                                     _ints(status, "status", 1), _stream_ptr(stream)), "slm_attention_prompt")
 
 
 def sample(logits, temperature: float, top_k: int, top_p: float, uniforms, next_ids, stream=None) -> int:

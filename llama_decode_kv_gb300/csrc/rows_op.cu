@@ -1,0 +1,313 @@
+// rows_op.cu -- the packed-row operators behind the C ABI (include/slm.h): slm_kv_append,
+// slm_attention_paged, slm_attention_prompt.  Checks of arguments and the choice of kernels;
+// nothing here reads the lengths, which live on the device.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "rows.cuh"
+
+namespace slm {
+
+// SMs of the current device (looked up once per device); < 0: no device, and the status code.
+static int current_sms(int &dev) {
+    static std::atomic<int> known[64];
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return attn_fail(SLM_ECUDA, "no CUDA device");
+    }
+    if (dev >= 0 && dev < 64 && known[dev].load() > 0) return known[dev].load();
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return attn_fail(SLM_ECUDA, "no CUDA device");
+    }
+    if (dev >= 0 && dev < 64) known[dev].store(sms);
+    return sms;
+}
+
+struct PtrCheck {
+    const void *p;
+    const char *name;
+};
+
+// Device (or managed) memory of the current device, all of them.
+static int check_pointers(int dev, const PtrCheck *list, int n) {
+    for (int i = 0; i < n; i++) {
+        if (!list[i].p) continue;
+        cudaPointerAttributes a{};
+        if (cudaPointerGetAttributes(&a, list[i].p) != cudaSuccess) {
+            cudaGetLastError();
+            return attn_fail(SLM_EINVAL, "%s is not device memory", list[i].name);
+        }
+        if (a.type == cudaMemoryTypeManaged) continue;
+        if (a.type != cudaMemoryTypeDevice) return attn_fail(SLM_EINVAL, "%s is not device memory", list[i].name);
+        if (a.device != dev)
+            return attn_fail(SLM_EINVAL, "%s is memory of device %d, the current device is %d", list[i].name, a.device, dev);
+    }
+    return SLM_OK;
+}
+
+static int elem_size(int dtype) { return dtype == SLM_F32 ? 4 : 2; }
+
+static int check_dtype(int dtype, const char *name) {
+    if (dtype != SLM_F32 && dtype != SLM_BF16) return attn_fail(SLM_EINVAL, "%s %d is neither SLM_F32 nor SLM_BF16", name, dtype);
+    return SLM_OK;
+}
+
+static int check_heads(int H, int KV, int hd) {
+    if (H < 1 || KV < 1 || H % KV) return attn_fail(SLM_EINVAL, "n_heads %d must be a positive multiple of n_kv_heads %d", H, KV);
+    if (hd < 8 || hd % 8 || hd > 256) return attn_fail(SLM_EINVAL, "head_dim %d must be a multiple of 8 in [8, 256]", hd);
+    return SLM_OK;
+}
+
+static int check_rows(const slm_rows *r) {
+    if (!r) return attn_fail(SLM_EINVAL, "rows is NULL");
+    if (r->nseq < 1 || r->nseq > kRowsMaxSeqs) return attn_fail(SLM_EINVAL, "nseq %d outside [1, %d]", r->nseq, kRowsMaxSeqs);
+    if (r->rows < 0) return attn_fail(SLM_EINVAL, "rows %d < 0", r->rows);
+    if (!r->row_start) return attn_fail(SLM_EINVAL, "row_start is NULL");
+    if ((uintptr_t)r->row_start % 4 || (uintptr_t)r->ctx_len % 4) return attn_fail(SLM_EINVAL, "row_start and ctx_len must be 4-byte aligned");
+    return SLM_OK;
+}
+
+static int check_cache(const slm_kv_cache *c) {
+    if (!c) return attn_fail(SLM_EINVAL, "cache is NULL");
+    if (check_dtype(c->kv_dtype, "kv_dtype")) return SLM_EINVAL;
+    if (c->n_kv_heads < 1) return attn_fail(SLM_EINVAL, "n_kv_heads %d < 1", c->n_kv_heads);
+    if (c->head_dim < 8 || c->head_dim % 8 || c->head_dim > 256)
+        return attn_fail(SLM_EINVAL, "head_dim %d must be a multiple of 8 in [8, 256]", c->head_dim);
+    if (c->page_size < 16 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)))
+        return attn_fail(SLM_EINVAL, "page_size %d must be a power of two in [16, 2^20]", c->page_size);
+    if (c->n_pages < 1 || c->table_ld < 1) return attn_fail(SLM_EINVAL, "n_pages %d and table_ld %d must be positive", c->n_pages, c->table_ld);
+    if (!c->k || !c->v || !c->page_table) return attn_fail(SLM_EINVAL, "k, v and page_table of the cache must be non-NULL");
+    if (((uintptr_t)c->k | (uintptr_t)c->v) & 15) return attn_fail(SLM_EINVAL, "the cache's k and v must be 16-byte aligned");
+    if ((uintptr_t)c->page_table % 4) return attn_fail(SLM_EINVAL, "page_table must be 4-byte aligned");
+    return SLM_OK;
+}
+
+// Packed rows of `heads` heads: base and row stride (elements) on 16-byte boundaries.
+static int check_packed(const void *p, long long ld, int heads, int hd, int dtype, int rows, const char *name) {
+    if (!p) return attn_fail(SLM_EINVAL, "%s is NULL", name);
+    if ((uintptr_t)p & 15) return attn_fail(SLM_EINVAL, "%s must be 16-byte aligned", name);
+    if (rows > 1 && (ld < (long long)heads * hd || ld > (1LL << 32)))
+        return attn_fail(SLM_EINVAL, "%s: row stride %lld outside [%lld, 2^32]", name, ld, (long long)heads * hd);
+    if (rows > 1 && (ld * elem_size(dtype)) % 16) return attn_fail(SLM_EINVAL, "%s: a row stride must be a multiple of 16 bytes", name);
+    return SLM_OK;
+}
+
+static int check_status(const int32_t *status) {
+    if (!status || (uintptr_t)status % 4) return attn_fail(SLM_EINVAL, "status must be a 4-byte aligned device int32");
+    return SLM_OK;
+}
+
+static int log2i(int v) {
+    int s = 0;
+    while ((1 << s) < v) s++;
+    return s;
+}
+
+// Positions are int32 in the kernels.
+static long long cache_cap(const slm_kv_cache *c) {
+    return std::min<long long>((long long)c->table_ld * c->page_size, 0x7fffff00LL);
+}
+
+// Tiling and workspace of an attention call.
+struct RowsTiling {
+    RowsGeom geom;
+    int P, slot_rows;
+    size_t ws;
+};
+
+static RowsTiling rows_tiling(int sms, int rows, int nseq, int H, int KV, int hd) {
+    RowsTiling t{};
+    const int G = H / KV;
+    const int R = rows_simt_tile(rows, nseq, G, hd);
+    t.geom = {KV, R / G, 64};
+    t.P = rows_simt_ctas(sms, hd, R, nseq);
+    t.slot_rows = (int)std::min<long long>((long long)t.geom.PT * G, (long long)std::max(rows, 1) * G);
+    t.ws = rows_ws_bytes(t.P, t.slot_rows, hd);
+    return t;
+}
+
+static int check_group(int H, int KV, int hd) {
+    const int most = hd <= 128 ? kRowsMaxGroup : kRowsMaxGroup / 2;
+    if (H / KV > most) return attn_fail(SLM_EUNSUPPORTED, "%d query heads per kv head: at most %d at head_dim %d", H / KV, most, hd);
+    return SLM_OK;
+}
+
+// The part that both attention calls share: workspace, kernel, join.
+static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long longest, void *ws, size_t ws_bytes,
+                         cudaStream_t s) {
+    if (!ws || (uintptr_t)ws % 256) return attn_fail(SLM_EINVAL, "workspace must be non-NULL and 256-byte aligned");
+    if (ws_bytes < t.ws) return attn_fail(SLM_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, t.ws);
+    a.ws = (uint8_t *)ws;
+    a.P = t.P;
+    a.slot_rows = t.slot_rows;
+    a.geom = t.geom;
+    a.G = a.H / a.KV;
+    a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)a.hd));
+    const bool bf16 = dtype == SLM_BF16;
+    cudaError_t e = rows_simt_launch(a, bf16, s);
+    // an item of one block is never shared by two CTAs
+    if (e == cudaSuccess && longest > t.geom.BLK) e = rows_join_launch(a, bf16, s);
+    if (e != cudaSuccess) return attn_fail(SLM_ECUDA, "attention launch: %s", cudaGetErrorString(e));
+    return SLM_OK;
+}
+
+}  // namespace slm
+
+using namespace slm;
+
+extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
+                             const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_heads,
+                             const void *q, int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status,
+                             void *stream) {
+    int rc;
+    if ((rc = check_cache(cache)) || (rc = check_rows(rows)) || (rc = check_dtype(dtype, "dtype"))) return rc;
+    const int KV = cache->n_kv_heads, hd = cache->head_dim;
+    if ((rc = check_packed(k, k_ld, KV, hd, dtype, rows->rows, "k")) ||
+        (rc = check_packed(v, v_ld, KV, hd, dtype, rows->rows, "v")) || (rc = check_status(status)))
+        return rc;
+    if (q || q_out) {
+        if ((rc = check_heads(n_heads, KV, hd)) || (rc = check_packed(q, q_ld, n_heads, hd, dtype, rows->rows, "q")) ||
+            (rc = check_packed(q_out, q_out_ld, n_heads, hd, cache->kv_dtype, rows->rows, "q_out")))
+            return rc;
+        if (q == q_out && (dtype != cache->kv_dtype || (rows->rows > 1 && q_ld != q_out_ld)))
+            return attn_fail(SLM_EINVAL, "q can be rotated in place only in the cache's type, with one row stride");
+    }
+    if (rope && ((uintptr_t)rope % 16 || rope_len < 1))
+        return attn_fail(SLM_EINVAL, "rope must be 16-byte aligned and hold at least one position");
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (sms < 0) return sms;
+    const PtrCheck ptrs[] = {{cache->k, "the cache's k"}, {cache->v, "the cache's v"}, {cache->page_table, "page_table"},
+                             {rows->row_start, "row_start"}, {rows->ctx_len, "ctx_len"}, {k, "k"}, {v, "v"},
+                             {rope, "rope"}, {q, "q"}, {q_out, "q_out"}, {status, "status"}};
+    if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
+    if (rows->rows == 0) return SLM_OK;
+    AppendArgs a{};
+    a.row_start = rows->row_start;
+    a.ctx_len = rows->ctx_len;
+    a.nseq = rows->nseq;
+    a.rows = rows->rows;
+    a.H = q ? n_heads : 0;
+    a.KV = KV;
+    a.hd = hd;
+    a.cap = cache_cap(cache);
+    a.q = (const uint8_t *)q;
+    a.k = (const uint8_t *)k;
+    a.v = (const uint8_t *)v;
+    a.q_out = (uint8_t *)q_out;
+    a.kc = (uint8_t *)cache->k;
+    a.vc = (uint8_t *)cache->v;
+    a.q_ld = q_ld;
+    a.k_ld = k_ld;
+    a.v_ld = v_ld;
+    a.q_out_ld = q_out_ld;
+    a.rope = rope;
+    a.rope_len = rope_len;
+    a.table = cache->page_table;
+    a.table_ld = cache->table_ld;
+    a.n_pages = cache->n_pages;
+    a.page_shift = log2i(cache->page_size);
+    a.status = status;
+    const cudaError_t e = rows_append_launch(a, dtype == SLM_BF16, cache->kv_dtype == SLM_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return attn_fail(SLM_ECUDA, "append launch: %s", cudaGetErrorString(e));
+    return SLM_OK;
+}
+
+extern "C" size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t nseq, int32_t n_heads,
+                                                     int32_t n_kv_heads, int32_t head_dim) {
+    if (rows < 0 || nseq < 1 || nseq > kRowsMaxSeqs || check_dtype(dtype, "dtype") || check_heads(n_heads, n_kv_heads, head_dim) ||
+        check_group(n_heads, n_kv_heads, head_dim))
+        return 0;
+    int dev = 0;
+    const int sms = current_sms(dev);
+    return sms < 0 ? 0 : rows_tiling(sms, rows, nseq, n_heads, n_kv_heads, head_dim).ws;
+}
+
+extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q,
+                                   int64_t q_ld, void *out, int64_t out_ld, void *workspace, size_t workspace_bytes,
+                                   int32_t *status, void *stream) {
+    int rc;
+    if ((rc = check_cache(cache)) || (rc = check_rows(rows))) return rc;
+    const int KV = cache->n_kv_heads, hd = cache->head_dim, dtype = cache->kv_dtype;
+    if ((rc = check_heads(n_heads, KV, hd)) || (rc = check_group(n_heads, KV, hd)) ||
+        (rc = check_packed(q, q_ld, n_heads, hd, dtype, rows->rows, "q")) ||
+        (rc = check_packed(out, out_ld, n_heads, hd, dtype, rows->rows, "out")) || (rc = check_status(status)))
+        return rc;
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (sms < 0) return sms;
+    const PtrCheck ptrs[] = {{cache->k, "the cache's k"}, {cache->v, "the cache's v"}, {cache->page_table, "page_table"},
+                             {rows->row_start, "row_start"}, {rows->ctx_len, "ctx_len"}, {q, "q"}, {out, "out"},
+                             {workspace, "workspace"}, {status, "status"}};
+    if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
+    if (rows->rows == 0) return SLM_OK;
+    RowsArgs a{};
+    a.row_start = rows->row_start;
+    a.ctx_len = rows->ctx_len;
+    a.nseq = rows->nseq;
+    a.rows = rows->rows;
+    a.H = n_heads;
+    a.KV = KV;
+    a.hd = hd;
+    a.cap = cache_cap(cache);
+    a.q = (const uint8_t *)q;
+    a.out = (uint8_t *)out;
+    a.q_ld = q_ld;
+    a.out_ld = out_ld;
+    a.kv.k = (const uint8_t *)cache->k;
+    a.kv.v = (const uint8_t *)cache->v;
+    a.kv.table = cache->page_table;
+    a.kv.table_ld = cache->table_ld;
+    a.kv.n_pages = cache->n_pages;
+    a.kv.page_shift = log2i(cache->page_size);
+    a.status = status;
+    return run_attention(a, rows_tiling(sms, rows->rows, rows->nseq, n_heads, KV, hd), dtype, a.cap, workspace,
+                         workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, int32_t n_kv_heads,
+                                    int32_t head_dim, const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                                    const void *v, int64_t v_ld, void *out, int64_t out_ld, void *workspace,
+                                    size_t workspace_bytes, int32_t *status, void *stream) {
+    int rc;
+    if ((rc = check_rows(rows)) || (rc = check_dtype(dtype, "dtype")) || (rc = check_heads(n_heads, n_kv_heads, head_dim)) ||
+        (rc = check_group(n_heads, n_kv_heads, head_dim)))
+        return rc;
+    if (rows->ctx_len) return attn_fail(SLM_EINVAL, "ctx_len must be NULL: a whole prompt has no cached positions");
+    if ((rc = check_packed(q, q_ld, n_heads, head_dim, dtype, rows->rows, "q")) ||
+        (rc = check_packed(k, k_ld, n_kv_heads, head_dim, dtype, rows->rows, "k")) ||
+        (rc = check_packed(v, v_ld, n_kv_heads, head_dim, dtype, rows->rows, "v")) ||
+        (rc = check_packed(out, out_ld, n_heads, head_dim, dtype, rows->rows, "out")) || (rc = check_status(status)))
+        return rc;
+    int dev = 0;
+    const int sms = current_sms(dev);
+    if (sms < 0) return sms;
+    const PtrCheck ptrs[] = {{rows->row_start, "row_start"}, {q, "q"}, {k, "k"}, {v, "v"}, {out, "out"},
+                             {workspace, "workspace"}, {status, "status"}};
+    if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
+    if (rows->rows == 0) return SLM_OK;
+    RowsArgs a{};
+    a.row_start = rows->row_start;
+    a.nseq = rows->nseq;
+    a.rows = rows->rows;
+    a.H = n_heads;
+    a.KV = n_kv_heads;
+    a.hd = head_dim;
+    a.cap = rows->rows;
+    a.q = (const uint8_t *)q;
+    a.out = (uint8_t *)out;
+    a.q_ld = q_ld;
+    a.out_ld = out_ld;
+    a.kv.k = (const uint8_t *)k;
+    a.kv.v = (const uint8_t *)v;
+    a.kv.k_ld = k_ld;
+    a.kv.v_ld = v_ld;
+    a.status = status;
+    return run_attention(a, rows_tiling(sms, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows,
+                         workspace, workspace_bytes, (cudaStream_t)stream);
+}

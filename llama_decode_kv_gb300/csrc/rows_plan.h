@@ -1,0 +1,200 @@
+// rows_plan.h -- how the attention of packed rows is cut into work (host and device, no
+// CUDA calls, so that the host tests walk the same code).
+//
+// Sequence s of a batch has n new rows (tokens) after ctx cached positions.  Its work for
+// one kv head is cut into items of up to PT tokens (all G query heads of the group
+// together); an item walks the blocks of BLK positions [0, ctx + its last token], so item t
+// has nb(t) = ceil((ctx + min((t + 1) PT, n)) / BLK) blocks and counts nb(t) + kItemCost
+// units (the unit on top stands for its queries and its epilogue).  All items of a batch,
+// in the order (sequence, kv head, item), form one line of `total` units, which is cut into
+// P equal ranges, one per CTA: every CTA gets the same work whatever the lengths are, and
+// an item that a cut divides is joined afterwards from the partial states of its pieces.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SLM_HD __host__ __device__ __forceinline__
+#else
+#define SLM_HD inline
+#endif
+
+namespace slm {
+
+constexpr int kRowsMaxSeqs = 1024;  // sequences per call (their lengths sit in shared memory)
+constexpr int kRowsMaxGroup = 64;   // query heads per kv head
+constexpr int kItemCost = 1;
+
+// A sequence's rows after its lengths were checked: first packed row, rows, cached positions.
+struct SeqRows {
+    int row0, n, ctx;
+};
+
+// Check one sequence against the packed buffer (rows) and what the cache can hold (cap
+// positions; the lengths are device data, so nothing was checked before).  false: a length
+// was out of bounds and has been cut to fit.
+SLM_HD bool seq_rows(int begin, int end, int ctx, int rows, long long cap, SeqRows &o) {
+    bool ok = true;
+    int a = begin, b = end;
+    if (a < 0 || a > rows) {
+        a = a < 0 ? 0 : rows;
+        ok = false;
+    }
+    if (b < a || b > rows) {
+        b = b < a ? a : rows;
+        ok = false;
+    }
+    int n = b - a;
+    if (n > 0 && (ctx < 0 || (long long)ctx + n > cap)) {
+        ok = false;
+        ctx = 0;
+        if (n > cap) n = (int)cap;
+    }
+    o.row0 = a;
+    o.n = n;
+    o.ctx = n > 0 ? ctx : 0;
+    return ok;
+}
+
+// sum over i in [0, n) of floor((a i + b) / m), by exchanging the roles of a and m (the
+// lattice points under a line, counted by rows and by columns in turn).
+SLM_HD unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned long long b) {
+    unsigned long long s = 0;
+    while (n > 0) {
+        s += (unsigned long long)(a / m) * ((unsigned long long)n * (n - 1) / 2);
+        a %= m;
+        s += (unsigned long long)n * (b / m);
+        b %= m;
+        const unsigned long long top = (unsigned long long)a * n + b;
+        if (top < m) break;
+        n = (unsigned)(top / m);
+        b = top % m;
+        const unsigned t = m;
+        m = a;
+        a = t;
+    }
+    return s;
+}
+
+struct RowsGeom {
+    int KV;      // kv heads
+    int PT;      // tokens per item
+    int BLK;     // positions per block
+};
+
+SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
+
+SLM_HD int item_blocks(const RowsGeom &g, int ctx, int n, int t) {
+    const long long end = (long long)(t + 1) * g.PT;
+    const int last = end < n ? (int)end : n;
+    return (int)(((long long)ctx + last + g.BLK - 1) / g.BLK);
+}
+
+// Units of the items [0, t) of one kv head of a sequence.
+SLM_HD long long head_units(const RowsGeom &g, int ctx, int n, int t) {
+    if (t <= 0) return 0;
+    const int T = item_count(g, n), full = t < T ? t : T - 1;
+    long long s = (long long)floor_sum((unsigned)full, (unsigned)g.BLK, (unsigned)g.PT,
+                                       (unsigned long long)ctx + g.PT + g.BLK - 1);
+    if (t >= T) s += item_blocks(g, ctx, n, T - 1);
+    return s + (long long)kItemCost * (t < T ? t : T);
+}
+
+// First unit of CTA c of P on a line of `total` units.
+SLM_HD long long range_start(long long total, int P, int c) { return total * c / P; }
+
+// The CTA whose range holds unit x.
+SLM_HD int range_of(long long total, int P, long long x) {
+    int c = (int)((x * P) / total);
+    while (c + 1 < P && range_start(total, P, c + 1) <= x) c++;
+    while (c > 0 && range_start(total, P, c) > x) c--;
+    return c;
+}
+
+// One piece of one item: blocks [kb0, kb1) of its nb.
+struct RowsPiece {
+    int s, g, t, nb, kb0, kb1;
+    long long base;  // the item's first unit
+};
+
+// Walks the pieces of the units [x, end).  seq: the checked sequences; wstart[s]: units of
+// the sequences before s (wstart[nseq] = total).
+struct RowsWalk {
+    long long x, end, base;
+    int s, g, t, T, nb;
+
+    SLM_HD void open(const SeqRows *seq, const RowsGeom &G) {
+        T = item_count(G, seq[s].n);
+        nb = item_blocks(G, seq[s].ctx, seq[s].n, t);
+    }
+
+    SLM_HD void begin(const SeqRows *seq, const long long *wstart, int nseq, const RowsGeom &G, long long from,
+                      long long to) {
+        x = from;
+        end = to;
+        if (x >= end) return;
+        int lo = 0, hi = nseq - 1;  // the last s with wstart[s] <= x (empty sequences have no units)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (wstart[mid] <= x)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        s = lo;
+        const long long per = (wstart[s + 1] - wstart[s]) / G.KV;
+        long long rem = x - wstart[s];
+        g = (int)(rem / per);
+        rem -= (long long)g * per;
+        int a = 0, b = item_count(G, seq[s].n) - 1;  // the last t with head_units(t) <= rem
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (head_units(G, seq[s].ctx, seq[s].n, mid) <= rem)
+                a = mid;
+            else
+                b = mid - 1;
+        }
+        t = a;
+        base = wstart[s] + (long long)g * per + head_units(G, seq[s].ctx, seq[s].n, t);
+        open(seq, G);
+    }
+
+    // The next piece with at least one block; false at the end of the range.
+    SLM_HD bool next(const SeqRows *seq, int nseq, const RowsGeom &G, RowsPiece &p) {
+        while (x < end) {
+            const long long first = base + kItemCost, stop = base + kItemCost + nb;
+            const long long hi = end < stop ? end : stop;
+            p.s = s;
+            p.g = g;
+            p.t = t;
+            p.nb = nb;
+            p.base = base;
+            p.kb0 = x > first ? (int)(x - first) : 0;
+            p.kb1 = hi > first ? (int)(hi - first) : 0;
+            x = hi;
+            if (x >= stop) {  // on to the next item
+                base = stop;
+                if (++t == T) {
+                    t = 0;
+                    if (++g == G.KV) {
+                        g = 0;
+                        s++;
+                        while (s < nseq && seq[s].n == 0) s++;
+                    }
+                }
+                if (s < nseq)
+                    open(seq, G);
+                else
+                    end = x;
+            }
+            if (p.kb1 > p.kb0) return true;
+        }
+        return false;
+    }
+};
+
+// A CTA has at most two pieces that are not whole items: one that starts inside an item
+// (its first) and one that starts an item and does not finish it (its last).
+SLM_HD int piece_slot(int cta, const RowsPiece &p) { return 2 * cta + (p.kb0 > 0 ? 0 : 1); }
+
+}  // namespace slm
