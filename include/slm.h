@@ -499,8 +499,9 @@ size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t n
  *     rows, nseq, ...) bytes.  It needs no initialisation and carries nothing from call to call;
  *     the call owns it until its work has finished, so calls that may overlap (two streams, two
  *     graphs replayed at once) need one each.
- *   Scores, the softmax and its sums are fp32.  The same call with the same inputs gives the
- *   same bits.
+ *   Scores, the softmax and its sums are fp32; bf16 heads of up to 128 run on the tensor cores,
+ *   where the softmax weights are rounded to bf16 before they multiply v; every other shape is
+ *   fp32 throughout.  The same call with the same inputs gives the same bits.
  *   Keys and values that no row of a call sees (cache slots past a sequence's last position,
  *   other sequences' pages) may hold anything, infinities and NaN included.  Non-finite values
  *   at a position that some rows see and earlier rows of the same sequence do not may reach those

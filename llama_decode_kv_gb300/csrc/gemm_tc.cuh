@@ -42,6 +42,12 @@ cudaError_t make_bf16_map(CUtensorMap *map, const void *base, int rows, int cols
 // boxes of 64 columns x box_rows rows x 1, 128-byte swizzle.
 cudaError_t make_bf16_tiled_map(CUtensorMap *map, const void *base, int tiles, int rows, int tile_k, int box_rows);
 
+// Tensor map of a bf16 array of `rank` dimensions, innermost (contiguous) first: dims in
+// elements, strides in bytes of dimensions 1 .. rank - 1, box in elements with 64 columns of the
+// innermost dimension (128-byte swizzle).  Out-of-range elements read as zero.
+cudaError_t make_bf16_map_nd(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                             const uint32_t *box);
+
 // Enqueue C = A . B^T with the given epilogue.  K must be a multiple of 64.
 cudaError_t gemm_bf16_tn(const GemmArgs &args, cudaStream_t stream);
 

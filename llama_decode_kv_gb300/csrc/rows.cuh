@@ -120,6 +120,9 @@ int rows_simt_tile(int rows, int nseq, int G, int hd);  // query rows (token, he
 int rows_simt_ctas(int sms, int hd, int R, int nseq);
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 
+// Tensor-core attention: bf16, head_dim up to 128; items of two tiles of 128 / G tokens.
+cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s);
+
 struct AppendArgs {
     const int *row_start, *ctx_len;
     int nseq, rows;

@@ -1,0 +1,620 @@
+// rows_attention_tc.cu -- attention of packed bf16 rows on the 5th-generation tensor cores,
+// heads of up to 128, over a paged cache or packed prompts.
+//
+// out = sum_{t <= p} softmax_t(q . k_t / sqrt(hd)) v_t for every row (token, query head).
+// The G query heads of a kv head and TT = 128 / G tokens make a tile of up to 128 rows (row =
+// token * G + head), so keys and values are read once for the whole group, and a decode step is
+// the same kernel with one tile that is mostly empty.  An item is two such tiles, one behind
+// the other, over the same keys: while the softmax of one runs, the tensor core works for the
+// other.  Items are cut into equal ranges of 128-position blocks (rows_plan.h), one persistent
+// CTA per SM; pieces of items leave as partial states for rows_join_kernel.
+//
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
+//                   causal mask where the block needs one, the running maximum, P = 2^(S - m) as
+//                   bf16 back into tensor memory, the sum in fp32; at the end O / l to global
+//                   memory.  O stays where it is: it is rescaled (by the same threads) only when
+//                   a row's maximum grew by more than 2^8, so P stays below 2^8 and the final
+//                   division takes the stale maximum out again.
+//   warp 8          tcgen05.mma issuer: S = Q K^T (both operands in shared memory, K-major),
+//                   O += P V (P from tensor memory, V as it lies in memory: head_dim contiguous,
+//                   which is the MN-major operand).  Also zeroes the rows of the last block's V
+//                   that no row sees, since 0 * NaN is NaN.
+//   warp 9          TMA producer: the tile's queries as one box {64, G, TT} per 64 columns, keys
+//                   and values as boxes of up to 128 positions, one per page where pages are
+//                   shorter, into a ring of 128-byte-swizzled [128][64] panels.  Head widths
+//                   that are no multiple of 64 are filled up with zeros by the copy.
+//
+// Rounding: q, k, v as given; S, maxima, sums and O in fp32; P to bf16 (2^-9 relative, at most
+// half a step), the result to bf16.
+//
+// Every wait is bounded; the first to run out stops all roles, and tensor memory is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "device_common.cuh"
+#include "gemm_tc.cuh"
+#include "rows.cuh"
+
+namespace slm {
+
+constexpr int kTcThreads = 320;
+constexpr int kTcBlk = 128;                 // positions per block
+constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]
+constexpr int kTcCols = 512;                // tensor memory columns
+constexpr float kTcSlack = 8.0f;            // log2 growth of a maximum that O is not rescaled for
+
+struct RowsTcArgs {
+    CUtensorMap q, k, v;
+    RowsArgs a;
+    int TT;      // tokens per tile
+    int box;     // positions per key / value box
+    int stages;  // ring depth
+};
+
+struct TcBars {
+    uint64_t kv_full[16], kv_empty[16];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], drain;
+    uint32_t tmem;
+    int stop;
+};
+
+// ------------------------------------------------------------------ PTX wrappers
+
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory operand descriptors, 128-byte swizzle, rows of 128 bytes in groups of 8 (1024
+// bytes apart).  K-major (Q, K): the groups run along M / N.  MN-major (V): the groups run along
+// K, and panels of 64 columns are kPanel apart.
+__device__ __forceinline__ uint64_t operand_desc(const void *p, uint32_t lead) {
+    const uint32_t a = smem_addr(p);
+    return (uint64_t)((a & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// kind::f16, fp32 accumulator, bf16 operands; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, int b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+#define SLM_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define SLM_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+
+// Columns of this thread's lane.  The wait stands in the same statement, so that nothing that
+// uses the registers can move before it.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : SLM_R8(r, 0), SLM_R8(r, 8), SLM_R8(r, 16), SLM_R8(r, 24)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld128(uint32_t addr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : SLM_R8(r, 0), SLM_R8(r, 8), SLM_R8(r, 16), SLM_R8(r, 24), SLM_R8(r, 32), SLM_R8(r, 40), SLM_R8(r, 48),
+          SLM_R8(r, 56), SLM_R8(r, 64), SLM_R8(r, 72), SLM_R8(r, 80), SLM_R8(r, 88), SLM_R8(r, 96), SLM_R8(r, 104),
+          SLM_R8(r, 112), SLM_R8(r, 120)
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        SLM_I8(r, 0), SLM_I8(r, 8), SLM_I8(r, 16), SLM_I8(r, 24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        SLM_I8(r, 0), SLM_I8(r, 8)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bounded wait for the phase of the given parity; the first wait of the CTA to run out raises
+// stop, and every later wait gives up at once.
+__device__ __noinline__ bool tc_wait_slow(uint64_t *bar, uint32_t parity, int *status, volatile int *stop) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*stop) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            atomicOr(status, SLM_ROWS_TIMEOUT);
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *stop) {
+    return mbar_try_wait(bar, parity) || tc_wait_slow(bar, parity, status, stop);
+}
+
+// The blocks of a piece that tile i takes part in, and its tokens.
+struct TileView {
+    int n, tok0, ntok;  // blocks from p.kb0 on; first token in the sequence; tokens
+};
+__device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece &p, int TT, int PT, int i) {
+    TileView v;
+    v.tok0 = p.t * PT + i * TT;
+    v.ntok = max(0, min(TT, sr.n - v.tok0));
+    const int nb = v.ntok > 0 ? (sr.ctx + v.tok0 + v.ntok + kTcBlk - 1) / kTcBlk : 0;
+    v.n = max(0, min(p.kb1, nb) - p.kb0);
+    return v;
+}
+
+__host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages) {
+    return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int HDP, bool PAGED>
+__global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
+    constexpr int NP = HDP / 64;  // 64-column panels of a [128][head_dim] operand
+    constexpr uint32_t kO = 256, kP = HDP == 64 ? 384 : 0;  // P has columns of its own, or S's
+    const RowsArgs &A = T.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sq = base;                             // [2 tiles][NP][128][64]
+    uint8_t *ring = base + 2 * NP * kPanel;         // [stages][NP][128][64]
+    TcBars *B = (TcBars *)(ring + (size_t)T.stages * NP * kPanel);
+    long long *wstart = (long long *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);
+    SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
+    volatile int *stop = &B->stop;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int TT = T.TT, PT = A.geom.PT, G = A.G;
+
+    if (tid == 0) {
+        for (int s = 0; s < T.stages; s++) {
+            mbar_init(&B->kv_full[s], 1);
+            mbar_init(&B->kv_empty[s], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&B->q_full[i], 1);
+            mbar_init(&B->q_empty[i], 1);
+            mbar_init(&B->s_full[i], 1);
+            mbar_init(&B->p_ready[i], 4);
+            mbar_init(&B->o_full[i], 1);
+        }
+        mbar_init(&B->drain, 1);
+        B->stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&B->tmem)),
+                     "r"(kTcCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    rows_layout(A, seq, wstart, tid, kTcThreads);  // ends with a __syncthreads()
+    tc_after();
+    const uint32_t tmem = B->tmem;
+    const long long total = wstart[A.nseq];
+    RowsWalk w;
+    w.begin(seq, wstart, A.nseq, A.geom, range_start(total, A.P, blockIdx.x), range_start(total, A.P, blockIdx.x + 1));
+    RowsPiece p;
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- softmax, a thread per row
+        const int i = warp >> 2, r = tid & 127;                 // tile, row
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + 128 * i, tP = kP ? tmem + lanes + kP + 64 * i : tS, tO = tmem + lanes + kO + HDP * i;
+        const int tok = r / G, head = r - tok * G;
+        const float c = A.scale_log2;
+        uint32_t sp = 0, op = 0;  // phases of s_full, o_full
+        bool joined = false;
+        while (w.next(seq, A.nseq, A.geom, p)) {
+            const SeqRows sr = seq[p.s];
+            const TileView v = tile_view(sr, p, TT, PT, i);
+            const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
+            const bool valid = tok < v.ntok && r < TT * G;
+            const bool busy = __any_sync(0xffffffffu, valid);    // else only the hand-offs
+            const int seen = sr.ctx + v.tok0 + tok + 1;          // positions the row sees
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            if (!whole && p.kb0 == 0) {
+                joined = true;
+                if (tid == 0) write_join(A, blockIdx.x, seq, total, &p);
+            }
+            for (int j = 0; j < v.n; j++) {
+                if (!(ok = tc_wait(&B->s_full[i], sp, A.status, stop))) break;
+                sp ^= 1;
+                if (busy) {
+                    tc_after();
+                    __syncwarp();
+                    uint32_t s[128];
+                    tmem_ld128(tS, s);
+                    const int lim = seen - (p.kb0 + j) * kTcBlk;  // keys of the block that the row sees
+                    if (__any_sync(0xffffffffu, lim < kTcBlk)) {
+#pragma unroll
+                        for (int k = 0; k < 128; k++)
+                            if (k >= lim) s[k] = 0xff800000u;  // -infinity
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 128; k += 4)
+#pragma unroll
+                        for (int q = 0; q < 4; q++) mx[q] = fmaxf(mx[q], __uint_as_float(s[k + q]));
+                    const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (j == 0) {
+                        m = mb;
+                    } else {
+                        const bool grow = m == -INFINITY ? mb > m : (mb - m) * c > kTcSlack;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? fast_exp2((m - mb) * c) : 1.0f;
+                            if (grow) m = mb;
+                            l *= f;
+#pragma unroll 1
+                            for (int d = 0; d < HDP; d += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + d, o);
+#pragma unroll
+                                for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st32(tO + d, o);
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k0 = 0; k0 < 128; k0 += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float a = fast_exp2(fmaf(__uint_as_float(s[k0 + k]), c, -mc));
+                            const float b = fast_exp2(fmaf(__uint_as_float(s[k0 + k + 1]), c, -mc));
+                            sum[k & 2] += a;
+                            sum[(k & 2) + 1] += b;
+                            pk[k / 2] = pack_bf16x2(a, b);
+                        }
+                        tmem_st16(tP + k0 / 2, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
+                    tc_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->p_ready[i]);
+            }
+            if (!ok) break;
+            if (v.n > 0) {
+                if (!tc_wait(&B->o_full[i], op, A.status, stop)) break;
+                op ^= 1;
+            }
+            if (!busy) continue;
+            tc_after();
+            __syncwarp();
+            if (whole) {
+                const float inv = 1.0f / l;
+                uint16_t *dst = (uint16_t *)A.out + (size_t)(sr.row0 + v.tok0 + tok) * A.out_ld + (size_t)(p.g * G + head) * A.hd;
+#pragma unroll 1
+                for (int d = 0; d < HDP; d += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + d, o);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            h[q] = pack_bf16x2(__uint_as_float(o[k + 2 * q]) * inv, __uint_as_float(o[k + 2 * q + 1]) * inv);
+                        if (valid && d + k < A.hd) *(uint4 *)(dst + d + k) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                float *part = slot_ptr(A, piece_slot(blockIdx.x, p));
+                const int row = i * TT * G + r;
+                if (v.n > 0) {
+#pragma unroll 1
+                    for (int d = 0; d < HDP; d += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + d, o);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            if (valid && d + k < A.hd) *(uint4 *)(part + (size_t)row * A.hd + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        __syncwarp();
+                    }
+                }
+                if (valid) {  // the maximum in the log2 domain, as the join takes it
+                    float *pm = part + (size_t)A.slot_rows * A.hd + row;
+                    pm[0] = m == -INFINITY ? m : m * c;
+                    pm[A.slot_rows] = l;
+                }
+            }
+            tc_before();
+        }
+        if (!joined && tid == 0) write_join(A, blockIdx.x, seq, total, nullptr);
+    } else if (warp == 8) {
+        // ---------------------------------------------------------------- tensor core
+        constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
+        const int ksteps = (A.hd + 15) / 16;
+        uint32_t st = 0, ph = 0;        // the ring stage that comes next, its phase
+        uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+        bool ok = true;
+        auto next_stage = [&](uint32_t &s) {
+            if (++s == (uint32_t)T.stages) {
+                s = 0;
+                ph ^= 1;
+            }
+        };
+        auto issue_s = [&](int i, uint32_t ks) {  // S_i = Q_i K^T
+            const uint8_t *a = sq + (size_t)i * NP * kPanel, *b = ring + (size_t)ks * NP * kPanel;
+            for (int k = 0; k < ksteps; k++) {
+                const int off = (k >> 2) * kPanel + (k & 3) * 32;
+                mma_ss(tmem + 128 * i, operand_desc(a + off, 16), operand_desc(b + off, 16), idS, k != 0);
+            }
+        };
+        auto issue_o = [&](int i, uint32_t vs, bool first) {  // O_i (+)= P_i V
+            const uint8_t *b = ring + (size_t)vs * NP * kPanel;
+#pragma unroll
+            for (int k = 0; k < kTcBlk / 16; k++)
+                mma_ts(tmem + kO + HDP * i, tmem + (kP ? kP + 64 * i : 128 * i) + 8 * k, operand_desc(b + k * 2048, kPanel),
+                       idO, !(first && k == 0));
+        };
+        while (ok && w.next(seq, A.nseq, A.geom, p)) {
+            const SeqRows sr = seq[p.s];
+            const int n = p.kb1 - p.kb0;
+            const int nt[2] = {tile_view(sr, p, TT, PT, 0).n, tile_view(sr, p, TT, PT, 1).n};
+            const int L = sr.ctx + min(p.t * PT + PT, sr.n);  // positions the item sees
+            const int tail = p.kb1 == p.nb ? L - (p.nb - 1) * kTcBlk : kTcBlk;  // of the last block
+            uint32_t ks = st;
+            if (!(ok = tc_wait(&B->kv_full[ks], ph, A.status, stop))) break;
+            next_stage(st);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                if (nt[i] == 0) continue;
+                if (!(ok = tc_wait(&B->q_full[i], qph[i], A.status, stop))) break;
+                qph[i] ^= 1;
+                tc_after();
+                if (lane == 0) {
+                    issue_s(i, ks);
+                    tc_commit(&B->s_full[i]);
+                    if (nt[i] == 1) tc_commit(&B->q_empty[i]);
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) tc_commit(&B->kv_empty[ks]);
+            for (int j = 0; j < n && ok; j++) {
+                const uint32_t vs = st;
+                if (!(ok = tc_wait(&B->kv_full[vs], ph, A.status, stop))) break;
+                next_stage(st);
+                if (j == n - 1 && tail < kTcBlk) {
+                    // V rows that nobody sees: whole 128-byte rows, so the swizzle does not matter
+                    for (int e = lane; e < NP * (kTcBlk - tail) * 8; e += 32) {
+                        const int pn = e / ((kTcBlk - tail) * 8), x = e - pn * (kTcBlk - tail) * 8;
+                        *(uint4 *)(ring + ((size_t)vs * NP + pn) * kPanel + tail * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                const bool more = j + 1 < n;
+                if (more) ks = st;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (j < nt[i]) {
+                        if (!(ok = tc_wait(&B->p_ready[i], pph[i], A.status, stop))) break;
+                        pph[i] ^= 1;
+                        tc_after();
+                        if (lane == 0) {
+                            issue_o(i, vs, j == 0);
+                            if (j == nt[i] - 1) tc_commit(&B->o_full[i]);
+                        }
+                    }
+                    if (i == 1 && lane == 0) tc_commit(&B->kv_empty[vs]);
+                    if (i == 0 && more) {
+                        if (!(ok = tc_wait(&B->kv_full[ks], ph, A.status, stop))) break;
+                        next_stage(st);
+                        tc_after();
+                    }
+                    if (j + 1 < nt[i] && lane == 0) {
+                        issue_s(i, ks);
+                        tc_commit(&B->s_full[i]);
+                        if (j + 2 == nt[i]) tc_commit(&B->q_empty[i]);
+                    }
+                }
+                if (!ok) break;
+                if (more && lane == 0) tc_commit(&B->kv_empty[ks]);
+            }
+        }
+        if (!ok) {  // what was issued still runs: wait for it, bounded
+            if (lane == 0) {
+                tc_commit(&B->drain);
+                const unsigned long long t0 = global_ns();
+                while (!mbar_try_wait(&B->drain, 0) && global_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------------------------------- TMA producer
+        uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
+        uint32_t qn[2] = {0, 0};              // query tiles loaded so far
+        bool ok = true;
+        const int shift = A.kv.page_shift, box = T.box;
+        const int per = kTcBlk / box;         // boxes of a block
+        while (ok && w.next(seq, A.nseq, A.geom, p)) {
+            const SeqRows sr = seq[p.s];
+            const int L = sr.ctx + min(p.t * PT + PT, sr.n);
+            // the page (lane: box) of a block; a bad id becomes page 0
+            auto page_of = [&](int kb) {
+                const int pos = kb * kTcBlk + lane * box;
+                if (!PAGED || lane >= per || pos >= L || kb >= p.kb1) return -1;
+                int pg = __ldg(A.kv.table + (size_t)p.s * A.kv.table_ld + (pos >> shift));
+                if (pg < 0 || pg >= A.kv.n_pages) {
+                    atomicOr(A.status, SLM_ROWS_PAGE);
+                    pg = 0;
+                }
+                return pg;
+            };
+            int page = page_of(p.kb0);
+            for (int kb = p.kb0; kb < p.kb1 && ok; kb++) {
+                const int after = page_of(kb + 1);
+                const int pos0 = kb * kTcBlk;
+                const int nbox = PAGED ? min(per, (L - pos0 + box - 1) / box) : 1;
+                for (int is_v = 0; is_v < 2; is_v++) {
+                    if (issued >= (uint32_t)T.stages && !(ok = tc_wait(&B->kv_empty[st], ph ^ 1, A.status, stop))) break;
+                    uint64_t *bar = &B->kv_full[st];
+                    uint8_t *dst = ring + (size_t)st * NP * kPanel;
+                    const CUtensorMap *map = is_v ? &T.v : &T.k;
+                    if (lane == 0) mbar_expect_tx(bar, (uint32_t)(nbox * box * 128 * NP));
+                    __syncwarp();
+                    if (lane < nbox)
+#pragma unroll
+                        for (int pn = 0; pn < NP; pn++) {
+                            if (PAGED)
+                                tma_4d(dst + pn * kPanel + lane * box * 128, map, pn * 64, (pos0 + lane * box) & ((1 << shift) - 1),
+                                       p.g, page, bar);
+                            else
+                                tma_3d(dst + pn * kPanel, map, pn * 64, p.g, sr.row0 + pos0, bar);
+                        }
+                    issued++;
+                    if (++st == (uint32_t)T.stages) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                    if (kb == p.kb0 && is_v == 0) {  // the queries, behind the first keys
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const TileView v = tile_view(sr, p, TT, PT, i);
+                            if (v.n == 0) continue;
+                            if (qn[i] > 0 && !(ok = tc_wait(&B->q_empty[i], (qn[i] - 1) & 1, A.status, stop))) break;
+                            qn[i]++;
+                            if (lane == 0) {
+                                mbar_expect_tx(&B->q_full[i], (uint32_t)(NP * TT * G * 128));
+#pragma unroll
+                                for (int pn = 0; pn < NP; pn++)
+                                    tma_3d(sq + (size_t)(i * NP + pn) * kPanel, &T.q, pn * 64, p.g * G, sr.row0 + v.tok0,
+                                           &B->q_full[i]);
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                }
+                page = after;
+            }
+        }
+        if (*stop) {  // copies in flight end before the shared memory goes: wait for them, bounded
+            const unsigned long long t0 = global_ns();
+            const uint32_t back = min(issued, (uint32_t)T.stages);
+            for (uint32_t b = 1; b <= back; b++) {
+                const uint32_t q = issued - b;
+                while (!mbar_try_wait(&B->kv_full[q % T.stages], (q / T.stages) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+            for (int i = 0; i < 2; i++)
+                while (qn[i] > 0 && !mbar_try_wait(&B->q_full[i], (qn[i] - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+                }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+static int tc_stages(int hd, int nseq) {
+    // as many ring stages as fit beside the batch's lengths (1,024 sequences: 20 KB)
+    const int HDP = hd <= 64 ? 64 : 128;
+    int n = HDP == 64 ? 10 : 5;
+    while (tc_fixed_bytes(HDP, n) + (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 > kSmemLimit) n--;
+    return n;
+}
+
+template <int HDP, bool PAGED> static cudaError_t launch_tc(const RowsTcArgs &t, cudaStream_t s) {
+    const size_t smem = tc_fixed_bytes(HDP, t.stages) + (size_t)t.a.nseq * sizeof(SeqRows) + (size_t)(t.a.nseq + 1) * 8;
+    cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<HDP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    rows_tc_kernel<HDP, PAGED><<<t.a.P, kTcThreads, smem, s>>>(t);
+    return cudaGetLastError();
+}
+
+cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {
+    RowsTcArgs t{};
+    t.a = a;
+    t.TT = a.geom.PT / 2;
+    t.stages = tc_stages(a.hd, a.nseq);
+    const bool paged = a.kv.table != nullptr;
+    const uint64_t hb = (uint64_t)a.hd * 2;  // bytes of a head
+    const uint64_t qd[] = {(uint64_t)a.hd, (uint64_t)a.H, (uint64_t)a.rows}, qs[] = {hb, (uint64_t)a.q_ld * 2};
+    const uint32_t qb[] = {64, (uint32_t)a.G, (uint32_t)t.TT};
+    cudaError_t e = make_bf16_map_nd(&t.q, a.q, 3, qd, qs, qb);
+    if (paged) {
+        const uint64_t page = 1ull << a.kv.page_shift;
+        t.box = page < kTcBlk ? (int)page : kTcBlk;
+        const uint64_t d[] = {(uint64_t)a.hd, page, (uint64_t)a.KV, (uint64_t)a.kv.n_pages};
+        const uint64_t st[] = {hb, hb * page, hb * page * a.KV};
+        const uint32_t b[] = {64, (uint32_t)t.box, 1, 1};
+        if (e == cudaSuccess) e = make_bf16_map_nd(&t.k, a.kv.k, 4, d, st, b);
+        if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 4, d, st, b);
+    } else {
+        t.box = kTcBlk;
+        const uint64_t d[] = {(uint64_t)a.hd, (uint64_t)a.KV, (uint64_t)a.rows};
+        const uint64_t ks[] = {hb, (uint64_t)a.kv.k_ld * 2}, vs[] = {hb, (uint64_t)a.kv.v_ld * 2};
+        const uint32_t b[] = {64, 1, (uint32_t)t.box};
+        if (e == cudaSuccess) e = make_bf16_map_nd(&t.k, a.kv.k, 3, d, ks, b);
+        if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 3, d, vs, b);
+    }
+    if (e != cudaSuccess) return e;
+    if (a.hd <= 64) return paged ? launch_tc<64, true>(t, s) : launch_tc<64, false>(t, s);
+    return paged ? launch_tc<128, true>(t, s) : launch_tc<128, false>(t, s);
+}
+
+}  // namespace slm

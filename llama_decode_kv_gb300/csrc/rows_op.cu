@@ -120,12 +120,20 @@ struct RowsTiling {
     size_t ws;
 };
 
-static RowsTiling rows_tiling(int sms, int rows, int nseq, int H, int KV, int hd) {
+// bf16 heads of up to 128 run on the tensor cores, one CTA per SM.
+static bool on_tensor_cores(int dtype, int hd) { return dtype == SLM_BF16 && hd <= 128; }
+
+static RowsTiling rows_tiling(int sms, int dtype, int rows, int nseq, int H, int KV, int hd) {
     RowsTiling t{};
     const int G = H / KV;
-    const int R = rows_simt_tile(rows, nseq, G, hd);
-    t.geom = {KV, R / G, 64};
-    t.P = rows_simt_ctas(sms, hd, R, nseq);
+    if (on_tensor_cores(dtype, hd)) {
+        t.geom = {KV, 2 * (128 / G), 128};
+        t.P = sms;
+    } else {
+        const int R = rows_simt_tile(rows, nseq, G, hd);
+        t.geom = {KV, R / G, 64};
+        t.P = rows_simt_ctas(sms, hd, R, nseq);
+    }
     t.slot_rows = (int)std::min<long long>((long long)t.geom.PT * G, (long long)std::max(rows, 1) * G);
     t.ws = rows_ws_bytes(t.P, t.slot_rows, hd);
     return t;
@@ -149,7 +157,11 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     a.G = a.H / a.KV;
     a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)a.hd));
     const bool bf16 = dtype == SLM_BF16;
-    cudaError_t e = rows_simt_launch(a, bf16, s);
+    if (a.rows == 1) {  // one row: its stride has no meaning
+        a.q_ld = a.out_ld = (long long)a.H * a.hd;
+        a.kv.k_ld = a.kv.v_ld = (long long)a.KV * a.hd;
+    }
+    cudaError_t e = on_tensor_cores(dtype, a.hd) ? rows_tc_launch(a, s) : rows_simt_launch(a, bf16, s);
     // an item of one block is never shared by two CTAs
     if (e == cudaSuccess && longest > t.geom.BLK) e = rows_join_launch(a, bf16, s);
     if (e != cudaSuccess) return attn_fail(SLM_ECUDA, "attention launch: %s", cudaGetErrorString(e));
@@ -225,7 +237,7 @@ extern "C" size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows
         return 0;
     int dev = 0;
     const int sms = current_sms(dev);
-    return sms < 0 ? 0 : rows_tiling(sms, rows, nseq, n_heads, n_kv_heads, head_dim).ws;
+    return sms < 0 ? 0 : rows_tiling(sms, dtype, rows, nseq, n_heads, n_kv_heads, head_dim).ws;
 }
 
 extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q,
@@ -266,7 +278,7 @@ extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *ro
     a.kv.n_pages = cache->n_pages;
     a.kv.page_shift = log2i(cache->page_size);
     a.status = status;
-    return run_attention(a, rows_tiling(sms, rows->rows, rows->nseq, n_heads, KV, hd), dtype, a.cap, workspace,
+    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, KV, hd), dtype, a.cap, workspace,
                          workspace_bytes, (cudaStream_t)stream);
 }
 
@@ -308,6 +320,6 @@ extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t
     a.kv.k_ld = k_ld;
     a.kv.v_ld = v_ld;
     a.status = status;
-    return run_attention(a, rows_tiling(sms, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows,
+    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows,
                          workspace, workspace_bytes, (cudaStream_t)stream);
 }
