@@ -38,9 +38,8 @@ struct RowsArgs {
 // Workspace: one RowsJoin per CTA, then 2 P slots of slot_rows unnormalised output rows
 // (fp32), their running maxima (log2 domain) and their sums.
 struct RowsJoin {
-    long long total, base;  // units in all; the item's first unit
-    int valid, nb;
-    int row0, tokens, head0, pad;
+    int pieces;               // of the item that this CTA starts and another one finishes; 0: none
+    int row0, tokens, head0;  // the item's first packed row, its tokens, its first query head
 };
 
 __host__ __device__ inline size_t join_bytes(int P) { return ((size_t)P * sizeof(RowsJoin) + 255) / 256 * 256; }
@@ -85,16 +84,13 @@ __device__ __forceinline__ void rows_layout(const RowsArgs &A, SeqRows *seq, lon
 }
 
 // What the joining kernel needs to know about the item that this CTA starts and another
-// finishes (p null: none).
-__device__ __forceinline__ void write_join(const RowsArgs &A, int cta, const SeqRows *seq, long long total,
+// finishes (p null: none).  unit: units of a range.
+__device__ __forceinline__ void write_join(const RowsArgs &A, int cta, const SeqRows *seq, long long unit,
                                            const RowsPiece *p) {
     RowsJoin j{};
-    j.valid = p != nullptr;
     if (p) {
         const SeqRows r = seq[p->s];
-        j.total = total;
-        j.base = p->base;
-        j.nb = p->nb;
+        j.pieces = (int)udiv(p->base + kItemCost + p->nb - 1, unit) - cta + 1;
         j.row0 = r.row0 + p->t * A.geom.PT;
         j.tokens = min(A.geom.PT, r.n - p->t * A.geom.PT);
         j.head0 = p->g * A.G;

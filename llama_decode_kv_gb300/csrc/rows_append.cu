@@ -97,6 +97,8 @@ __device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int
 template <typename TI, typename TC, int VEC>
 __global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __grid_constant__ AppendArgs A, int rpc) {
     __shared__ AppendRow rows[8];
+    pdl_wait();
+    pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = blockIdx.x * rpc, nr = min(rpc, A.rows - r0);
     if (warp < nr) {
@@ -151,11 +153,8 @@ static cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     const int rpc = a.rows >= 2048 ? 4 : 1;
     const int gy = rpc > 1 ? 1 : (units + kAppendThreads - 1) / kAppendThreads;
     const dim3 grid((a.rows + rpc - 1) / rpc, gy);
-    if (vec == 8)
-        rows_append_kernel<TI, TC, 8><<<grid, kAppendThreads, 0, s>>>(a, rpc);
-    else
-        rows_append_kernel<TI, TC, 4><<<grid, kAppendThreads, 0, s>>>(a, rpc);
-    return cudaGetLastError();
+    return launch_pdl(vec == 8 ? rows_append_kernel<TI, TC, 8> : rows_append_kernel<TI, TC, 4>, grid, dim3(kAppendThreads), 0, s,
+                      a, rpc);
 }
 
 cudaError_t rows_append_launch(const AppendArgs &a, bool in_bf16, bool cache_bf16, cudaStream_t s) {

@@ -15,6 +15,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "rows.cuh"
 
@@ -72,10 +74,12 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
     const int tx = tid & 15, kq = (tid >> 4) % KQ, ty = (tid >> 4) / KQ;
     const T *Q = (const T *)A.q;
 
+    pdl_wait();
+    pdl_trigger();
     rows_layout(A, seq, wstart, tid, kSimtThreads);
-    const long long total = wstart[A.nseq];
+    const long long unit = range_units(wstart[A.nseq], A.P);
     RowsWalk w;
-    w.begin(seq, wstart, A.nseq, A.geom, range_start(total, A.P, blockIdx.x), range_start(total, A.P, blockIdx.x + 1));
+    w.begin(seq, wstart, A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1));
     RowsPiece p;
     bool joined = false;
     while (w.next(seq, A.nseq, A.geom, p)) {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
         const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
         if (!whole && p.kb0 == 0) {
             joined = true;
-            if (tid == 0) write_join(A, blockIdx.x, seq, total, &p);
+            if (tid == 0) write_join(A, blockIdx.x, seq, unit, &p);
         }
         if (whole) {
             if (kq == 0)
@@ -290,102 +294,117 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
             }
         }
     }
-    if (!joined && tid == 0) write_join(A, blockIdx.x, seq, total, nullptr);
+    if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
 }
 
 // ---- joining
 //
 // Piece i of an item has, per row, the maximum m_i, the sum l_i and the unnormalised O_i:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i.
-// CTA x looks after the item that attention CTA x starts and another one finishes (RowsJoin);
-// its pieces are slot 2x + 1 and slot 2c of every CTA c behind x up to the one that holds the
-// item's last unit.  A warp takes a row and goes over the pieces in order, so the result does
-// not depend on timing; with 12 pieces or more (one long context over the whole GPU, few rows)
-// the eight warps of a CTA share a row's pieces instead and add up in shared memory.
+// Block x looks after the item that attention CTA x starts and another one finishes (RowsJoin);
+// its pieces are slot 2x + 1 and the slots 2c of the CTAs behind x.  A thread takes four columns
+// of a row and goes over the pieces in order, so the result does not depend on timing.  With
+// kJoinShared pieces or more (a long context over the whole GPU, few rows) the eight warps of a
+// block share the pieces of a row instead and add up in shared memory.
+constexpr int kJoinShared = 12;
+
+template <typename T> __device__ __forceinline__ void store4(T *p, float4 v, float f);
+template <> __device__ __forceinline__ void store4<float>(float *p, float4 v, float f) {
+    *(float4 *)p = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v, float f) {
+    *(uint2 *)p = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+}
+
+__device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
+    a.x = fmaf(f, b.x, a.x);
+    a.y = fmaf(f, b.y, a.y);
+    a.z = fmaf(f, b.z, a.z);
+    a.w = fmaf(f, b.w, a.w);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs A) {
     pdl_wait();
+    pdl_trigger();
     const RowsJoin J = ((const RowsJoin *)A.ws)[blockIdx.x];
-    if (!J.valid) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.x;
-    const int c1 = range_of(J.total, A.P, J.base + kItemCost + J.nb - 1);
-    const int nr = J.tokens * A.G, n = c1 - c0 + 1;
+    if (J.pieces == 0) return;
+    const int n = J.pieces, nr = J.tokens * A.G, cols = A.hd / 4, c0 = blockIdx.x;
     const size_t sf = slot_floats(A.slot_rows, A.hd);
     const float *slots = (const float *)(A.ws + join_bytes(A.P));
-    const bool shared = n >= 12;
-    __shared__ float red[8][256 + 2];
-    // piece i of the item: its slot, or null when the CTA's range is empty
-    auto piece = [&](int i) -> const float * {
-        const int c = c0 + i;
-        if (i == 0) return slots + (size_t)(2 * c + 1) * sf;
-        return range_start(J.total, A.P, c + 1) > range_start(J.total, A.P, c) ? slots + (size_t)(2 * c) * sf : nullptr;
-    };
-    const int step = shared ? 1 : 8;
-    for (int r = blockIdx.y * step + (shared ? 0 : warp); r < nr; r += gridDim.y * step) {
-        const int i0 = shared ? warp : 0, is = shared ? 8 : 1;
-        // the maximum over this warp's pieces, lanes in parallel
-        float m = -INFINITY;
-        for (int i = i0 + is * lane; i < n; i += is * 32) {
-            const float *s = piece(i);
-            if (s) m = fmaxf(m, s[(size_t)A.slot_rows * A.hd + r]);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.f, acc[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) acc[k] = 0.f;
-#pragma unroll 4
-        for (int i = i0; i < n; i += is) {
-            const float *s = piece(i);
-            if (!s) continue;
-            const float mi = s[(size_t)A.slot_rows * A.hd + r];
-            if (mi == -INFINITY) continue;  // the row saw nothing of this piece; its O was not written
-            const float f = exp2f(mi - m);
-            l += f * s[(size_t)A.slot_rows * (A.hd + 1) + r];
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int d = lane + 32 * k;
-                if (d < A.hd) acc[k] = fmaf(f, s[(size_t)r * A.hd + d], acc[k]);
-            }
-        }
-        if (shared) {
-            __syncthreads();  // the last row's sums have been read
-            if (lane == 0) {
-                red[warp][256] = m;
-                red[warp][257] = l;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; k++) red[warp][lane + 32 * k] = acc[k];
-            __syncthreads();
-            if (warp) continue;
-            m = -INFINITY;
-            for (int w = 0; w < 8; w++) m = fmaxf(m, red[w][256]);
-            l = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; k++) acc[k] = 0.f;
-            for (int w = 0; w < 8; w++) {
-                if (red[w][256] == -INFINITY) continue;
-                const float f = exp2f(red[w][256] - m);
-                l += f * red[w][257];
-#pragma unroll
-                for (int k = 0; k < 8; k++) acc[k] = fmaf(f, red[w][lane + 32 * k], acc[k]);
-            }
-        }
+    const float *stats = slots + (size_t)A.slot_rows * A.hd;  // maxima, then sums, of slot 0
+    auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * sf; };
+    auto dest = [&](int r) {
         const int tok = r / A.G;
-        T *dst = (T *)A.out + (size_t)(J.row0 + tok) * A.out_ld + (size_t)(J.head0 + r - tok * A.G) * A.hd;
-        const float inv = 1.0f / l;
+        return (T *)A.out + (size_t)(J.row0 + tok) * A.out_ld + (size_t)(J.head0 + r - tok * A.G) * A.hd;
+    };
+    if (n < kJoinShared) {
+        for (int e = blockIdx.y * 256 + threadIdx.x; e < nr * cols; e += gridDim.y * 256) {
+            const int r = e / cols, d = (e - r * cols) * 4;
+            float m[kJoinShared], M = -INFINITY, l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int d = lane + 32 * k;
-            if (d < A.hd) dst[d] = from_float<T>(acc[k] * inv);
+            for (int i = 0; i < kJoinShared; i++) {
+                m[i] = i < n ? stats[slot(i) + r] : -INFINITY;
+                M = fmaxf(M, m[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinShared; i++) {
+                if (m[i] == -INFINITY) continue;  // no piece, or the row saw nothing of it: O was not written
+                const float f = exp2f(m[i] - M);
+                l = fmaf(f, stats[slot(i) + A.slot_rows + r], l);
+                add4(acc, f, *(const float4 *)(slots + slot(i) + (size_t)r * A.hd + d));
+            }
+            store4<T>(dest(r) + d, acc, 1.0f / l);
+        }
+        return;
+    }
+    __shared__ __align__(16) float red[8][256];
+    __shared__ float rm[8], rl[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = blockIdx.y; r < nr; r += gridDim.y) {
+        float M = -INFINITY, l = 0.f;
+        for (int i = warp + 8 * lane; i < n; i += 256) M = fmaxf(M, stats[slot(i) + r]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+        for (int i = warp; i < n; i += 8) {
+            const float mi = stats[slot(i) + r];
+            if (mi == -INFINITY) continue;
+            const float f = exp2f(mi - M);
+            l = fmaf(f, stats[slot(i) + A.slot_rows + r], l);
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+                if (lane + 32 * k < cols) add4(acc[k], f, *(const float4 *)(slots + slot(i) + (size_t)r * A.hd + 4 * (lane + 32 * k)));
+        }
+        __syncthreads();  // the last row's sums have been read
+        if (lane == 0) {
+            rm[warp] = M;
+            rl[warp] = l;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) *(float4 *)(red[warp] + 4 * (lane + 32 * k)) = acc[k];
+        __syncthreads();
+        if (threadIdx.x < cols) {
+            float Ma = -INFINITY, la = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < 8; w++) Ma = fmaxf(Ma, rm[w]);
+            for (int w = 0; w < 8; w++) {
+                if (rm[w] == -INFINITY) continue;
+                const float f = exp2f(rm[w] - Ma);
+                la = fmaf(f, rl[w], la);
+                add4(a, f, *(const float4 *)(red[w] + 4 * threadIdx.x));
+            }
+            store4<T>(dest(r) + 4 * threadIdx.x, a, 1.0f / la);
         }
     }
 }
 
 cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
     if (a.P < 2) return cudaSuccess;
-    // an item's rows are spread over up to 8 CTAs
-    const int gy = a.slot_rows >= 64 ? 8 : (a.slot_rows + 7) / 8;
+    // an item's rows are spread over up to 16 blocks
+    const int gy = (int)std::min<long long>(16, ((long long)a.slot_rows * (a.hd / 4) + 255) / 256);
     const dim3 grid(a.P - 1, gy);
     return bf16 ? launch_pdl(rows_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a)
                 : launch_pdl(rows_join_kernel<float>, grid, dim3(256), 0, s, a);
@@ -417,8 +436,7 @@ template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsA
     const size_t smem = simt_smem<HDP, R>(a.nseq);
     cudaError_t e = cudaFuncSetAttribute(rows_simt_kernel<T, HDP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    rows_simt_kernel<T, HDP, R><<<a.P, kSimtThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(rows_simt_kernel<T, HDP, R>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
 }
 
 template <typename T> static cudaError_t launch_simt_hd(const RowsArgs &a, cudaStream_t s) {

@@ -55,7 +55,7 @@ struct RowsTcArgs {
 
 struct TcBars {
     uint64_t kv_full[16], kv_empty[16];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
     uint32_t tmem;
     int stop;
 };
@@ -83,11 +83,12 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 
 // Shared-memory operand descriptors, 128-byte swizzle, rows of 128 bytes in groups of 8 (1024
 // bytes apart).  K-major (Q, K): the groups run along M / N.  MN-major (V): the groups run along
-// K, and panels of 64 columns are kPanel apart.
-__device__ __forceinline__ uint64_t operand_desc(const void *p, uint32_t lead) {
-    const uint32_t a = smem_addr(p);
-    return (uint64_t)((a & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// K, and panels of 64 columns are kPanel apart.  The upper word is the same for all: the group
+// stride, version 1, the swizzle.  The lower word is the address and the panel stride (`lead`), in
+// units of 16 bytes; offsets are added to it.
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(const void *p, uint32_t lead) {
+    return (smem_addr(p) >> 4) | (lead >> 4) << 16;
 }
 
 // kind::f16, fp32 accumulator, bf16 operands; b_mn: B is MN-major.
@@ -96,19 +97,19 @@ __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, int b_mn) {
            ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, "
+        "%5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
 
@@ -120,8 +121,8 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 #define SLM_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define SLM_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
 
-// Columns of this thread's lane.  The wait stands in the same statement, so that nothing that
-// uses the registers can move before it.
+// Columns of this thread's lane.  The wait stands in the same statement: the registers are not
+// valid before it, and between two statements the compiler may copy them and give them to others.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -131,20 +132,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld128(uint32_t addr, uint32_t *r) {
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t *r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
         "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
-        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
-        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
-        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
-        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : SLM_R8(r, 0), SLM_R8(r, 8), SLM_R8(r, 16), SLM_R8(r, 24), SLM_R8(r, 32), SLM_R8(r, 40), SLM_R8(r, 48),
-          SLM_R8(r, 56), SLM_R8(r, 64), SLM_R8(r, 72), SLM_R8(r, 80), SLM_R8(r, 88), SLM_R8(r, 96), SLM_R8(r, 104),
-          SLM_R8(r, 112), SLM_R8(r, 120)
+          SLM_R8(r, 56)
         : "r"(addr)
         : "memory");
 }
@@ -164,22 +160,83 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Bounded wait for the phase of the given parity; the first wait of the CTA to run out raises
-// stop, and every later wait gives up at once.
-__device__ __noinline__ bool tc_wait_slow(uint64_t *bar, uint32_t parity, int *status, volatile int *stop) {
-    const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (*stop) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
-            atomicOr(status, SLM_ROWS_TIMEOUT);
-            *stop = 1;
-            return false;
+// fp32 pairs in one register pair: one instruction for two results.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ void mask64(uint32_t (&s)[64], int lim) {
+#pragma unroll
+    for (int k = 0; k < 64; k++)
+        if (k >= lim) s[k] = 0xff800000u;  // -infinity
+}
+
+__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 0; k < 64; k += 8)
+#pragma unroll
+        for (int q = 0; q < 4; q++) m[q] = max3(m[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// P = 2^(S c - m c) of 64 keys: added to the sums, and as bf16 pairs to tensor memory.
+__device__ __forceinline__ void weights64(const uint32_t (&s)[64], uint64_t c2, uint64_t mc2, uint64_t (&sum)[2], uint32_t addr) {
+#pragma unroll
+    for (int k0 = 0; k0 < 64; k0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(s[k0 + k]), __uint_as_float(s[k0 + k + 1])), c2, mc2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+            pk[k / 2] = pack_bf16x2(a, b);
+        }
+        tmem_st16(addr + k0 / 2, pk);
+    }
+}
+
+// Bounded wait of a whole warp for the phase of the given parity; the first wait of the CTA to run
+// out raises stop, and every later wait gives up at once.  The warp is together again behind it
+// (the roles keep warp-uniform state, and tcgen05 instructions are warp-wide).
+__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *stop) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const unsigned long long t0 = global_ns();
+        while (true) {
+            ok = mbar_try_wait(bar, parity);
+            if (__all_sync(0xffffffffu, ok)) break;
+            const bool late = *stop || global_ns() - t0 > kWaitLimitNs;
+            if (__any_sync(0xffffffffu, late)) {
+                if (!*stop) atomicOr(status, SLM_ROWS_TIMEOUT);
+                *stop = 1;
+                return false;
+            }
         }
     }
     return true;
-}
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *status, volatile int *stop) {
-    return mbar_try_wait(bar, parity) || tc_wait_slow(bar, parity, status, stop);
 }
 
 // The blocks of a piece that tile i takes part in, and its tokens.
@@ -204,7 +261,9 @@ __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages) {
 template <int HDP, bool PAGED>
 __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
     constexpr int NP = HDP / 64;  // 64-column panels of a [128][head_dim] operand
-    constexpr uint32_t kO = 256, kP = HDP == 64 ? 384 : 0;  // P has columns of its own, or S's
+    // Tensor memory columns: S 128 i, O 256 + HDP i.  P (64 columns) has its own where O leaves
+    // room, else the upper half of S, which the softmax holds in registers by then.
+    constexpr uint32_t kO = 256, kP = HDP == 64 ? 384 : 64, kPStep = HDP == 64 ? 64 : 128;
     const RowsArgs &A = T.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -226,6 +285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             mbar_init(&B->q_full[i], 1);
             mbar_init(&B->q_empty[i], 1);
             mbar_init(&B->s_full[i], 1);
+            mbar_init(&B->p_half[i], 4);
             mbar_init(&B->p_ready[i], 4);
             mbar_init(&B->o_full[i], 1);
         }
@@ -240,19 +300,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_before();
+    pdl_wait();  // what stands above touches no memory of an earlier kernel
+    pdl_trigger();
     rows_layout(A, seq, wstart, tid, kTcThreads);  // ends with a __syncthreads()
     tc_after();
     const uint32_t tmem = B->tmem;
-    const long long total = wstart[A.nseq];
+    const long long unit = range_units(wstart[A.nseq], A.P);
     RowsWalk w;
-    w.begin(seq, wstart, A.nseq, A.geom, range_start(total, A.P, blockIdx.x), range_start(total, A.P, blockIdx.x + 1));
+    w.begin(seq, wstart, A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1));
     RowsPiece p;
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax, a thread per row
         const int i = warp >> 2, r = tid & 127;                 // tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lanes + 128 * i, tP = kP ? tmem + lanes + kP + 64 * i : tS, tO = tmem + lanes + kO + HDP * i;
+        const uint32_t tS = tmem + lanes + 128 * i, tP = tmem + lanes + kP + kPStep * i, tO = tmem + lanes + kO + HDP * i;
         const int tok = r / G, head = r - tok * G;
         const float c = A.scale_log2;
         uint32_t sp = 0, op = 0;  // phases of s_full, o_full
@@ -268,7 +330,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             bool ok = true;
             if (!whole && p.kb0 == 0) {
                 joined = true;
-                if (tid == 0) write_join(A, blockIdx.x, seq, total, &p);
+                if (tid == 0) write_join(A, blockIdx.x, seq, unit, &p);
             }
             for (int j = 0; j < v.n; j++) {
                 if (!(ok = tc_wait(&B->s_full[i], sp, A.status, stop))) break;
@@ -276,20 +338,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (busy) {
                     tc_after();
                     __syncwarp();
-                    uint32_t s[128];
-                    tmem_ld128(tS, s);
+                    // Keys 0-63 for the maximum only, keys 64-127 to stay, then 0-63 once more: the
+                    // row fits the registers in halves, and tensor memory is quick to read twice.
                     const int lim = seen - (p.kb0 + j) * kTcBlk;  // keys of the block that the row sees
-                    if (__any_sync(0xffffffffu, lim < kTcBlk)) {
-#pragma unroll
-                        for (int k = 0; k < 128; k++)
-                            if (k >= lim) s[k] = 0xff800000u;  // -infinity
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 128; k += 4)
-#pragma unroll
-                        for (int q = 0; q < 4; q++) mx[q] = fmaxf(mx[q], __uint_as_float(s[k + q]));
-                    const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool cut = __any_sync(0xffffffffu, lim < kTcBlk);
+                    uint32_t lo[64], hi[64];
+                    tmem_ld64(tS, lo);
+                    if (cut) mask64(lo, lim);
+                    float mb = max64(lo);
+                    tmem_ld64(tS + 64, hi);
+                    if (cut) mask64(hi, lim - 64);
+                    mb = fmaxf(mb, max64(hi));
                     if (j == 0) {
                         m = mb;
                     } else {
@@ -309,23 +368,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                         }
                     }
                     const float mc = m == -INFINITY ? 0.f : m * c;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k0 = 0; k0 < 128; k0 += 32) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float a = fast_exp2(fmaf(__uint_as_float(s[k0 + k]), c, -mc));
-                            const float b = fast_exp2(fmaf(__uint_as_float(s[k0 + k + 1]), c, -mc));
-                            sum[k & 2] += a;
-                            sum[(k & 2) + 1] += b;
-                            pk[k / 2] = pack_bf16x2(a, b);
-                        }
-                        tmem_st16(tP + k0 / 2, pk);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
+                    uint64_t sum[2] = {0, 0};  // two packed pairs of fp32 zeros
+                    weights64(hi, c2, mc2, sum, tP + 32);
+                    tmem_wait_st();  // keys 64-127: the tensor core can begin
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B->p_half[i]);
+                    __syncwarp();
+                    tmem_ld64(tS, lo);
+                    if (cut) mask64(lo, lim);
+                    weights64(lo, c2, mc2, sum, tP);
+                    float a, b;
+                    unpack2(add2(sum[0], sum[1]), a, b);
+                    l += a + b;
                     tmem_wait_st();
                     tc_before();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B->p_half[i]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->p_ready[i]);
@@ -377,11 +438,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             }
             tc_before();
         }
-        if (!joined && tid == 0) write_join(A, blockIdx.x, seq, total, nullptr);
+        if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
     } else if (warp == 8) {
         // ---------------------------------------------------------------- tensor core
         constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
         const int ksteps = (A.hd + 15) / 16;
+        // descriptors of the query tiles and of ring stage 0
+        const uint32_t dq = desc_lo(sq, 16), dk = desc_lo(ring, 16), dv = desc_lo(ring, kPanel);
         uint32_t st = 0, ph = 0;        // the ring stage that comes next, its phase
         uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
         bool ok = true;
@@ -392,18 +455,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             }
         };
         auto issue_s = [&](int i, uint32_t ks) {  // S_i = Q_i K^T
-            const uint8_t *a = sq + (size_t)i * NP * kPanel, *b = ring + (size_t)ks * NP * kPanel;
-            for (int k = 0; k < ksteps; k++) {
-                const int off = (k >> 2) * kPanel + (k & 3) * 32;
-                mma_ss(tmem + 128 * i, operand_desc(a + off, 16), operand_desc(b + off, 16), idS, k != 0);
+            const uint32_t a = dq + i * (NP * kPanel / 16), b = dk + ks * (NP * kPanel / 16);
+#pragma unroll
+            for (int k = 0; k < HDP / 16; k++) {
+                const int off = (k >> 2) * (kPanel / 16) + (k & 3) * 2;
+                if (k < ksteps) mma_ss(tmem + 128 * i, a + off, b + off, idS, k != 0);
             }
         };
-        auto issue_o = [&](int i, uint32_t vs, bool first) {  // O_i (+)= P_i V
-            const uint8_t *b = ring + (size_t)vs * NP * kPanel;
+        auto issue_o = [&](int i, uint32_t vs, int half, bool first) {  // O_i (+)= P_i V, 64 keys
+            const uint32_t b = dv + vs * (NP * kPanel / 16);
+            const uint32_t a = tmem + kP + kPStep * i;
 #pragma unroll
-            for (int k = 0; k < kTcBlk / 16; k++)
-                mma_ts(tmem + kO + HDP * i, tmem + (kP ? kP + 64 * i : 128 * i) + 8 * k, operand_desc(b + k * 2048, kPanel),
-                       idO, !(first && k == 0));
+            for (int k = 0; k < 4; k++)
+                mma_ts(tmem + kO + HDP * i, a + 8 * (4 * half + k), b + (4 * half + k) * 128, idO, !(first && k == 0));
         };
         while (ok && w.next(seq, A.nseq, A.geom, p)) {
             const SeqRows sr = seq[p.s];
@@ -434,10 +498,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 next_stage(st);
                 if (j == n - 1 && tail < kTcBlk) {
                     // V rows that nobody sees: whole 128-byte rows, so the swizzle does not matter
-                    for (int e = lane; e < NP * (kTcBlk - tail) * 8; e += 32) {
-                        const int pn = e / ((kTcBlk - tail) * 8), x = e - pn * (kTcBlk - tail) * 8;
-                        *(uint4 *)(ring + ((size_t)vs * NP + pn) * kPanel + tail * 128 + x * 16) = make_uint4(0, 0, 0, 0);
-                    }
+                    const uint32_t v0 = smem_addr(ring) + vs * NP * kPanel + tail * 128;
+                    for (int pn = 0; pn < NP; pn++)
+                        for (int x = lane * 16; x < (kTcBlk - tail) * 128; x += 512)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + pn * kPanel + x), "r"(0)
+                                         : "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
@@ -446,11 +511,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
                     if (j < nt[i]) {
+                        if (!(ok = tc_wait(&B->p_half[i], pph[i], A.status, stop))) break;
+                        tc_after();
+                        if (lane == 0) issue_o(i, vs, 1, j == 0);
                         if (!(ok = tc_wait(&B->p_ready[i], pph[i], A.status, stop))) break;
                         pph[i] ^= 1;
                         tc_after();
                         if (lane == 0) {
-                            issue_o(i, vs, j == 0);
+                            issue_o(i, vs, 0, false);
                             if (j == nt[i] - 1) tc_commit(&B->o_full[i]);
                         }
                     }
@@ -479,7 +547,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             }
             __syncwarp();
         }
-    } else {
+    } else if (warp == 9) {
         // ---------------------------------------------------------------- TMA producer
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
         uint32_t qn[2] = {0, 0};              // query tiles loaded so far
@@ -582,8 +650,7 @@ template <int HDP, bool PAGED> static cudaError_t launch_tc(const RowsTcArgs &t,
     const size_t smem = tc_fixed_bytes(HDP, t.stages) + (size_t)t.a.nseq * sizeof(SeqRows) + (size_t)(t.a.nseq + 1) * 8;
     cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<HDP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    rows_tc_kernel<HDP, PAGED><<<t.a.P, kTcThreads, smem, s>>>(t);
-    return cudaGetLastError();
+    return launch_pdl(rows_tc_kernel<HDP, PAGED>, dim3(t.a.P), dim3(kTcThreads), smem, s, t);
 }
 
 cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {

@@ -7,8 +7,10 @@
 // has nb(t) = ceil((ctx + min((t + 1) PT, n)) / BLK) blocks and counts nb(t) + kItemCost
 // units (the unit on top stands for its queries and its epilogue).  All items of a batch,
 // in the order (sequence, kv head, item), form one line of `total` units, which is cut into
-// P equal ranges, one per CTA: every CTA gets the same work whatever the lengths are, and
-// an item that a cut divides is joined afterwards from the partial states of its pieces.
+// ranges of ceil(total / P) units, one per CTA: every CTA gets the same work whatever the
+// lengths are, and an item that a cut divides is joined afterwards from the partial states of
+// its pieces.  Where every item is short (split = 0), a CTA takes the items that begin in its
+// range whole, and nothing has to be joined.
 #pragma once
 
 #include <stdint.h>
@@ -56,19 +58,24 @@ SLM_HD bool seq_rows(int begin, int end, int ctx, int rows, long long cap, SeqRo
     return ok;
 }
 
+// Quotient of values that nearly always fit 32 bits (a 64-bit division is a long routine).
+SLM_HD unsigned long long udiv(unsigned long long a, unsigned long long b) {
+    return ((a | b) >> 32) == 0 ? (unsigned)a / (unsigned)b : a / b;
+}
+
 // sum over i in [0, n) of floor((a i + b) / m), by exchanging the roles of a and m (the
 // lattice points under a line, counted by rows and by columns in turn).
-SLM_HD unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned long long b) {
+SLM_HD unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
     unsigned long long s = 0;
     while (n > 0) {
         s += (unsigned long long)(a / m) * ((unsigned long long)n * (n - 1) / 2);
         a %= m;
         s += (unsigned long long)n * (b / m);
         b %= m;
-        const unsigned long long top = (unsigned long long)a * n + b;
-        if (top < m) break;
-        n = (unsigned)(top / m);
-        b = top % m;
+        const unsigned long long top = (unsigned long long)a * n + b, q = udiv(top, m);
+        if (q == 0) break;
+        n = (unsigned)q;
+        b = (unsigned)(top - q * m);
         const unsigned t = m;
         m = a;
         a = t;
@@ -80,6 +87,7 @@ struct RowsGeom {
     int KV;      // kv heads
     int PT;      // tokens per item
     int BLK;     // positions per block
+    int split;   // 1: ranges cut through items; 0: items stay whole
 };
 
 SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
@@ -94,21 +102,16 @@ SLM_HD int item_blocks(const RowsGeom &g, int ctx, int n, int t) {
 SLM_HD long long head_units(const RowsGeom &g, int ctx, int n, int t) {
     if (t <= 0) return 0;
     const int T = item_count(g, n), full = t < T ? t : T - 1;
-    long long s = (long long)floor_sum((unsigned)full, (unsigned)g.BLK, (unsigned)g.PT,
-                                       (unsigned long long)ctx + g.PT + g.BLK - 1);
+    long long s = full > 0 ? (long long)floor_sum((unsigned)full, (unsigned)g.BLK, (unsigned)g.PT,
+                                                  (unsigned)ctx + g.PT + g.BLK - 1)
+                           : 0;
     if (t >= T) s += item_blocks(g, ctx, n, T - 1);
     return s + (long long)kItemCost * (t < T ? t : T);
 }
 
-// First unit of CTA c of P on a line of `total` units.
-SLM_HD long long range_start(long long total, int P, int c) { return total * c / P; }
-
-// The CTA whose range holds unit x.
-SLM_HD int range_of(long long total, int P, long long x) {
-    int c = (int)((x * P) / total);
-    while (c + 1 < P && range_start(total, P, c + 1) <= x) c++;
-    while (c > 0 && range_start(total, P, c) > x) c--;
-    return c;
+// Units of a range.
+SLM_HD long long range_units(long long total, int P) {
+    return total > 0 ? (long long)udiv((unsigned long long)total + P - 1, (unsigned long long)P) : 1;
 }
 
 // One piece of one item: blocks [kb0, kb1) of its nb.
@@ -117,7 +120,7 @@ struct RowsPiece {
     long long base;  // the item's first unit
 };
 
-// Walks the pieces of the units [x, end).  seq: the checked sequences; wstart[s]: units of
+// Walks the pieces of the units [from, to).  seq: the checked sequences; wstart[s]: units of
 // the sequences before s (wstart[nseq] = total).
 struct RowsWalk {
     long long x, end, base;
@@ -128,10 +131,27 @@ struct RowsWalk {
         nb = item_blocks(G, seq[s].ctx, seq[s].n, t);
     }
 
+    // On to the item after this one; false behind the last.
+    SLM_HD bool advance(const SeqRows *seq, int nseq, const RowsGeom &G) {
+        base += kItemCost + nb;
+        if (++t == T) {
+            t = 0;
+            if (++g == G.KV) {
+                g = 0;
+                s++;
+                while (s < nseq && seq[s].n == 0) s++;
+            }
+        }
+        if (s >= nseq) return false;
+        open(seq, G);
+        return true;
+    }
+
     SLM_HD void begin(const SeqRows *seq, const long long *wstart, int nseq, const RowsGeom &G, long long from,
                       long long to) {
+        const long long total = wstart[nseq];
         x = from;
-        end = to;
+        end = to < total ? to : total;
         if (x >= end) return;
         int lo = 0, hi = nseq - 1;  // the last s with wstart[s] <= x (empty sequences have no units)
         while (lo < hi) {
@@ -142,28 +162,32 @@ struct RowsWalk {
                 hi = mid - 1;
         }
         s = lo;
-        const long long per = (wstart[s + 1] - wstart[s]) / G.KV;
-        long long rem = x - wstart[s];
-        g = (int)(rem / per);
-        rem -= (long long)g * per;
+        const unsigned long long per = udiv(wstart[s + 1] - wstart[s], G.KV);
+        unsigned long long rem = x - wstart[s];
+        g = (int)udiv(rem, per);
+        rem -= (unsigned long long)g * per;
         int a = 0, b = item_count(G, seq[s].n) - 1;  // the last t with head_units(t) <= rem
         while (a < b) {
             const int mid = (a + b + 1) >> 1;
-            if (head_units(G, seq[s].ctx, seq[s].n, mid) <= rem)
+            if ((unsigned long long)head_units(G, seq[s].ctx, seq[s].n, mid) <= rem)
                 a = mid;
             else
                 b = mid - 1;
         }
         t = a;
-        base = wstart[s] + (long long)g * per + head_units(G, seq[s].ctx, seq[s].n, t);
+        base = wstart[s] + (long long)(g * per) + head_units(G, seq[s].ctx, seq[s].n, t);
         open(seq, G);
+        if (!G.split && base < x) {  // the item belongs to the range that it begins in
+            if (!advance(seq, nseq, G)) end = x;
+            x = base;
+        }
     }
 
     // The next piece with at least one block; false at the end of the range.
     SLM_HD bool next(const SeqRows *seq, int nseq, const RowsGeom &G, RowsPiece &p) {
         while (x < end) {
-            const long long first = base + kItemCost, stop = base + kItemCost + nb;
-            const long long hi = end < stop ? end : stop;
+            const long long first = base + kItemCost, stop = first + nb;
+            const long long hi = end < stop && G.split ? end : stop;
             p.s = s;
             p.g = g;
             p.t = t;
@@ -172,21 +196,7 @@ struct RowsWalk {
             p.kb0 = x > first ? (int)(x - first) : 0;
             p.kb1 = hi > first ? (int)(hi - first) : 0;
             x = hi;
-            if (x >= stop) {  // on to the next item
-                base = stop;
-                if (++t == T) {
-                    t = 0;
-                    if (++g == G.KV) {
-                        g = 0;
-                        s++;
-                        while (s < nseq && seq[s].n == 0) s++;
-                    }
-                }
-                if (s < nseq)
-                    open(seq, G);
-                else
-                    end = x;
-            }
+            if (x >= stop && !advance(seq, nseq, G)) end = x;
             if (p.kb1 > p.kb0) return true;
         }
         return false;

@@ -36,7 +36,7 @@ static void test_sums() {
         CHECK(floor_sum(n, m, a, b) == want, "floor_sum(%u, %u, %u, %u)", n, m, a, b);
     }
     for (int i = 0; i < 500; i++) {
-        const RowsGeom g{pick(1, 4), pick(1, 128), 64 << pick(0, 1)};
+        const RowsGeom g{pick(1, 4), pick(1, 128), 64 << pick(0, 1), 1};
         const int n = pick(1, 3000), ctx = pick(0, 5000);
         long long sum = 0;
         for (int t = 0; t <= item_count(g, n); t++) {
@@ -45,7 +45,7 @@ static void test_sums() {
         }
     }
     // a sequence of two billion positions: no overflow
-    const RowsGeom g{1, 1, 64};
+    const RowsGeom g{1, 1, 64, 1};
     CHECK(head_units(g, 2000000000, 1000, 1000) > 1000LL * (2000000000LL / 64), "long context");
 }
 
@@ -67,7 +67,7 @@ static void test_lengths() {
 
 static void test_walk(int nseq, int maxn, int maxctx) {
     const int G = pick(1, 8), tile = pick(0, 1) ? 256 : pick(0, 1) ? 64 : 16;
-    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, 64 << pick(0, 1)};
+    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, 64 << pick(0, 1), pick(0, 2) > 0};
     const int P = pick(0, 3) ? pick(1, 400) : pick(1, 5);
     std::vector<SeqRows> seq(nseq);
     std::vector<long long> wstart(nseq + 1, 0);
@@ -83,13 +83,11 @@ static void test_walk(int nseq, int maxn, int maxctx) {
     std::map<int, std::tuple<int, int, int>> slots;           // slot -> item
     std::map<std::tuple<int, int, int>, std::vector<int>> of; // item -> its slots in order
     std::map<int, RowsPiece> joins;                           // CTA -> the item it starts
-    long long most = 0, least = 1LL << 60;
+    const long long unit = range_units(total, P);
+    CHECK(unit * P >= total && (unit == 1 || (unit - 1) * P < total), "range of %lld for %lld over %d", unit, total, P);
     for (int c = 0; c < P; c++) {
-        const long long a = range_start(total, P, c), b = range_start(total, P, c + 1);
-        most = b - a > most ? b - a : most;
-        least = b - a < least ? b - a : least;
         RowsWalk w;
-        w.begin(seq.data(), wstart.data(), nseq, g, a, b);
+        w.begin(seq.data(), wstart.data(), nseq, g, unit * c, unit * (c + 1));
         RowsPiece p;
         while (w.next(seq.data(), nseq, g, p)) {
             const auto item = std::make_tuple(p.s, p.g, p.t);
@@ -99,6 +97,7 @@ static void test_walk(int nseq, int maxn, int maxctx) {
             CHECK(p.base >= 0 && p.base + kItemCost + p.nb <= total, "item within the line");
             done[item] = p.kb1;
             if (p.kb0 == 0 && p.kb1 == p.nb) continue;
+            CHECK(g.split, "a whole item was divided");
             const int slot = piece_slot(c, p);
             CHECK(slot >= 0 && slot < 2 * P && !slots.count(slot), "slot %d used twice", slot);
             slots[slot] = item;
@@ -110,7 +109,6 @@ static void test_walk(int nseq, int maxn, int maxctx) {
             }
         }
     }
-    CHECK(most - least <= 1, "ranges differ by %lld", most - least);
     long long items = 0;
     for (int s = 0; s < nseq; s++) items += seq[s].n ? (long long)g.KV * item_count(g, seq[s].n) : 0;
     CHECK((long long)done.size() == items, "%zu items of %lld", done.size(), items);
@@ -119,10 +117,9 @@ static void test_walk(int nseq, int maxn, int maxctx) {
     size_t found = 0;
     for (auto &j : joins) {
         const RowsPiece &p = j.second;
-        const int c0 = j.first, c1 = range_of(total, P, p.base + kItemCost + p.nb - 1);
+        const int c0 = j.first, c1 = (int)((p.base + kItemCost + p.nb - 1) / unit);
         std::vector<int> want{2 * c0 + 1};
-        for (int c = c0 + 1; c <= c1; c++)
-            if (range_start(total, P, c + 1) > range_start(total, P, c)) want.push_back(2 * c);
+        for (int c = c0 + 1; c <= c1; c++) want.push_back(2 * c);
         CHECK(of[std::make_tuple(p.s, p.g, p.t)] == want, "pieces of a divided item");
         found++;
     }
