@@ -218,6 +218,17 @@ __device__ __forceinline__ void weights64(const uint32_t (&s)[64], uint64_t c2, 
     }
 }
 
+// One lane of the (converged) warp, always the same.  Behind this predicate the compiler keeps the
+// operands of the asynchronous instructions in uniform registers; behind `lane == 0` it moved them
+// there one by one, ~100 cycles an MMA, which bound the kernel.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // Bounded wait of a whole warp for the phase of the given parity; the first wait of the CTA to run
 // out raises stop, and every later wait gives up at once.  The warp is together again behind it
 // (the roles keep warp-uniform state, and tcgen05 instructions are warp-wide).
@@ -484,14 +495,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = tc_wait(&B->q_full[i], qph[i], A.status, stop))) break;
                 qph[i] ^= 1;
                 tc_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     issue_s(i, ks);
                     tc_commit(&B->s_full[i]);
                     if (nt[i] == 1) tc_commit(&B->q_empty[i]);
                 }
             }
             if (!ok) break;
-            if (lane == 0) tc_commit(&B->kv_empty[ks]);
+            if (elect_one()) tc_commit(&B->kv_empty[ks]);
             for (int j = 0; j < n && ok; j++) {
                 const uint32_t vs = st;
                 if (!(ok = tc_wait(&B->kv_full[vs], ph, A.status, stop))) break;
@@ -513,33 +524,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     if (j < nt[i]) {
                         if (!(ok = tc_wait(&B->p_half[i], pph[i], A.status, stop))) break;
                         tc_after();
-                        if (lane == 0) issue_o(i, vs, 1, j == 0);
+                        if (elect_one()) issue_o(i, vs, 1, j == 0);
                         if (!(ok = tc_wait(&B->p_ready[i], pph[i], A.status, stop))) break;
                         pph[i] ^= 1;
                         tc_after();
-                        if (lane == 0) {
+                        if (elect_one()) {
                             issue_o(i, vs, 0, false);
                             if (j == nt[i] - 1) tc_commit(&B->o_full[i]);
                         }
                     }
-                    if (i == 1 && lane == 0) tc_commit(&B->kv_empty[vs]);
+                    if (i == 1 && elect_one()) tc_commit(&B->kv_empty[vs]);
                     if (i == 0 && more) {
                         if (!(ok = tc_wait(&B->kv_full[ks], ph, A.status, stop))) break;
                         next_stage(st);
                         tc_after();
                     }
-                    if (j + 1 < nt[i] && lane == 0) {
+                    if (j + 1 < nt[i] && elect_one()) {
                         issue_s(i, ks);
                         tc_commit(&B->s_full[i]);
                         if (j + 2 == nt[i]) tc_commit(&B->q_empty[i]);
                     }
                 }
                 if (!ok) break;
-                if (more && lane == 0) tc_commit(&B->kv_empty[ks]);
+                if (more && elect_one()) tc_commit(&B->kv_empty[ks]);
             }
         }
         if (!ok) {  // what was issued still runs: wait for it, bounded
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_commit(&B->drain);
                 const unsigned long long t0 = global_ns();
                 while (!mbar_try_wait(&B->drain, 0) && global_ns() - t0 < kWaitLimitNs) {
