@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 from typing import Optional, Sequence, Tuple
 
 import numpy as np
@@ -154,47 +155,75 @@ def attention_decode_noalloc(q, k_cache, v_cache, ctx_len, out, kv_dtype: int, s
                                         _ptr(v_cache), lens, _ptr(out), _stream_ptr(stream))
 
 
+# ---- packed-row calls.  A decode step makes them once per layer, so the checks read every
+# property of a tensor once, and the structs go as packed bytes (a ctypes.Structure costs more
+# than the launch).
+
+_PACK_CACHE = struct.Struct("PPPiiiiii").pack
+_PACK_ROWS = struct.Struct("PPii").pack
+_torch_names = None
+
+
+def _torch():
+    """(float32, bfloat16, int32, current raw stream of a device), looked up once."""
+    global _torch_names
+    if _torch_names is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        _torch_names = (torch.float32, torch.bfloat16, torch.int32, raw)
+    return _torch_names
+
+
 def _dtype_code(t) -> int:
     """SLM_F32 / SLM_BF16 of a torch dtype."""
-    name = str(t)
-    if name == "torch.float32":
-        return SLM_F32
-    if name == "torch.bfloat16":
+    f32, bf16, _, _ = _torch()
+    if t is bf16:
         return SLM_BF16
-    raise ValueError(f"{name}: the packed-row calls take float32 and bfloat16")
+    if t is f32:
+        return SLM_F32
+    raise ValueError(f"{t}: the packed-row calls take float32 and bfloat16")
 
 
-def _heads(x, name: str, heads: int, head_dim: int, rows: int, dtype):
+def _heads(x, name: str, shape, dtype):
     """Row stride (elements) of a [rows][heads][head_dim] tensor whose heads are adjacent."""
-    if x.dtype != dtype or tuple(x.shape) != (rows, heads, head_dim):
-        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected {(rows, heads, head_dim)} {dtype}")
+    rows, heads, hd = shape
+    if x.dtype is not dtype or x.shape != shape:
+        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected {tuple(shape)} {dtype}")
     ld, h, d = x.stride()
-    if rows and ((d != 1 and head_dim > 1) or (h != head_dim and heads > 1)):
+    if rows and ((d != 1 and hd > 1) or (h != hd and heads > 1)):
         raise ValueError(f"{name}: the heads of a row must be adjacent (strides {x.stride()})")
-    return ld if rows > 1 else heads * head_dim
+    return ld if rows > 1 else heads * hd
 
 
 def _ints(x, name: str, *shape):
-    if str(x.dtype) != "torch.int32" or tuple(x.shape) != shape or not x.is_contiguous():
+    if x.dtype is not _torch()[2] or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected contiguous int32 {shape}")
     return x.data_ptr()
 
 
-def _packed(row_start, ctx_len, rows: int) -> slm_rows:
-    nseq = row_start.shape[0] - 1
-    return slm_rows(_ints(row_start, "row_start", nseq + 1),
-                    None if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
+def _packed(row_start, ctx_len, nseq: int, rows: int) -> bytes:
+    return _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
+                      0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
 
 
-def _cache(k_cache, v_cache, page_table, nseq: int) -> slm_kv_cache:
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or k_cache.dim() != 4:
+def _cache(k_cache, v_cache, page_table, nseq: int, kv: int, hd: int, what: str) -> bytes:
+    """The slm_kv_cache of a cache of kv heads (0: any number) of hd."""
+    shape, dt = k_cache.shape, k_cache.dtype
+    if shape != v_cache.shape or dt is not v_cache.dtype or len(shape) != 4:
         raise ValueError("k_cache and v_cache must be [pages][kv heads][page size][head_dim] of one shape and type")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k_cache and v_cache must be contiguous")
-    pages, kv, page, hd = k_cache.shape
+    pages, heads, page, chd = shape
+    if chd != hd or (kv and heads != kv):
+        raise ValueError(f"the cache has {heads} kv heads of {chd}, {what} {kv or 'heads'} of {hd}")
     ld = page_table.shape[-1]
-    return slm_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), _ints(page_table, "page_table", nseq, ld), pages, page,
-                        ld, kv, hd, _dtype_code(k_cache.dtype))
+    return _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), _ints(page_table, "page_table", nseq, ld), pages, page,
+                       ld, heads, chd, _dtype_code(dt))
+
+
+def _rows_stream(stream, x):
+    return _torch()[3](x.device.index or 0) if stream is None and x.is_cuda else _stream_ptr(stream)
 
 
 def _rows_check(rc: int, what: str):
@@ -209,26 +238,30 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
     positions ctx_len[s] + i (ctx_len None: from 0), rotated by rope [positions][head_dim / 2][2]
     when given; q [rows][heads][head_dim] is rotated into q_out (the cache's type).  Row strides
     are free.  status: int32[1] collecting SLM_ROWS_* bits.  Raises SlmError / ValueError."""
-    rows, kv, hd = k.shape
-    r = _packed(row_start, ctx_len, rows)
-    c = _cache(k_cache, v_cache, page_table, r.nseq)
-    dt = _dtype_code(k.dtype)
-    if c.n_kv_heads != kv or c.head_dim != hd:
-        raise ValueError(f"k holds {kv} heads of {hd}, the cache {c.n_kv_heads} of {c.head_dim}")
-    k_ld, v_ld = _heads(k, "k", kv, hd, rows, k.dtype), _heads(v, "v", kv, hd, rows, k.dtype)
-    n_rope, heads, q_ld, o_ld = 0, 0, 0, 0
+    shape, dt = k.shape, k.dtype
+    rows, kv, hd = shape
+    nseq = page_table.shape[0]
+    code = _dtype_code(dt)
+    c = _cache(k_cache, v_cache, page_table, nseq, kv, hd, "k")
+    r = _packed(row_start, ctx_len, nseq, rows)
+    k_ld, v_ld = _heads(k, "k", shape, dt), _heads(v, "v", shape, dt)
+    rope_ptr, n_rope, heads, q_ptr, q_ld, o_ptr, o_ld = None, 0, 0, None, 0, None, 0
     if rope is not None:
-        if str(rope.dtype) != "torch.float32" or tuple(rope.shape[1:]) != (hd // 2, 2) or not rope.is_contiguous():
-            raise ValueError(f"rope: {tuple(rope.shape)} {rope.dtype}, expected contiguous float32 [n][{hd // 2}][2]")
         n_rope = rope.shape[0]
+        if rope.dtype is not _torch()[0] or rope.shape != (n_rope, hd // 2, 2) or not rope.is_contiguous():
+            raise ValueError(f"rope: {tuple(rope.shape)} {rope.dtype}, expected contiguous float32 [n][{hd // 2}][2]")
+        rope_ptr = rope.data_ptr()
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
     if q is not None:
-        heads = q.shape[1]
-        q_ld, o_ld = _heads(q, "q", heads, hd, rows, k.dtype), _heads(q_out, "q_out", heads, hd, rows, k_cache.dtype)
-    _rows_check(slm_kv_append(ctypes.byref(c), ctypes.byref(r), dt, _ptr(k), k_ld, _ptr(v), v_ld, _ptr(rope), n_rope,
-                              heads, _ptr(q), q_ld, _ptr(q_out), o_ld, _ints(status, "status", 1), _stream_ptr(stream)),
-                "slm_kv_append")
+        qs = q.shape
+        heads = qs[1]
+        if qs[0] != rows or qs[2] != hd:
+            raise ValueError(f"q: {tuple(qs)}, expected ({rows}, heads, {hd})")
+        q_ld, o_ld = _heads(q, "q", qs, dt), _heads(q_out, "q_out", qs, k_cache.dtype)
+        q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
+    _rows_check(slm_kv_append(c, r, code, k.data_ptr(), k_ld, v.data_ptr(), v_ld, rope_ptr, n_rope, heads, q_ptr, q_ld,
+                              o_ptr, o_ld, _ints(status, "status", 1), _rows_stream(stream, k)), "slm_kv_append")
 
 
 def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -241,14 +274,14 @@ def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, wo
     the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
     already holds the rows' own keys and values).  workspace: uint8 tensor of
     attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
-    rows, heads, hd = q.shape
-    r = _packed(row_start, ctx_len, rows)
-    c = _cache(k_cache, v_cache, page_table, r.nseq)
-    if c.head_dim != hd:
-        raise ValueError(f"q has heads of {hd}, the cache of {c.head_dim}")
-    q_ld, o_ld = _heads(q, "q", heads, hd, rows, k_cache.dtype), _heads(out, "out", heads, hd, rows, k_cache.dtype)
-    _rows_check(slm_attention_paged(ctypes.byref(c), ctypes.byref(r), heads, _ptr(q), q_ld, _ptr(out), o_ld,
-                                    _ptr(workspace), workspace.nbytes, _ints(status, "status", 1), _stream_ptr(stream)),
+    shape, dt = q.shape, k_cache.dtype
+    rows, heads, hd = shape
+    nseq = page_table.shape[0]
+    c = _cache(k_cache, v_cache, page_table, nseq, 0, hd, "q")
+    r = _packed(row_start, ctx_len, nseq, rows)
+    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
+    _rows_check(slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, workspace.data_ptr(),
+                                    workspace.nbytes, _ints(status, "status", 1), _rows_stream(stream, q)),
                 "slm_attention_paged")
 
 
@@ -256,14 +289,16 @@ def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) ->
     """slm_attention_prompt over torch tensors of the current device: causal attention of the
     packed prompts q [rows][heads][head_dim], k, v [rows][kv heads][head_dim] into out.
     Raises SlmError / ValueError."""
-    rows, heads, hd = q.shape
-    kv = k.shape[1]
-    r = _packed(row_start, None, rows)
-    q_ld, o_ld = _heads(q, "q", heads, hd, rows, q.dtype), _heads(out, "out", heads, hd, rows, q.dtype)
-    k_ld, v_ld = _heads(k, "k", kv, hd, rows, q.dtype), _heads(v, "v", kv, hd, rows, q.dtype)
-    _rows_check(slm_attention_prompt(ctypes.byref(r), _dtype_code(q.dtype), heads, kv, hd, _ptr(q), q_ld, _ptr(k), k_ld,
-                                     _ptr(v), v_ld, _ptr(out), o_ld, _ptr(workspace), workspace.nbytes,
-                                     _ints(status, "status", 1), _stream_ptr(stream)), "slm_attention_prompt")
+    shape, ks, dt = q.shape, k.shape, q.dtype
+    rows, heads, hd = shape
+    if ks[0] != rows or ks[2] != hd:
+        raise ValueError(f"k: {tuple(ks)}, expected ({rows}, kv heads, {hd})")
+    r = _packed(row_start, None, row_start.shape[0] - 1, rows)
+    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
+    k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
+    _rows_check(slm_attention_prompt(r, _dtype_code(dt), heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld,
+                                     v.data_ptr(), v_ld, out.data_ptr(), o_ld, workspace.data_ptr(), workspace.nbytes,
+                                     _ints(status, "status", 1), _rows_stream(stream, q)), "slm_attention_prompt")
 
 
 def sample(logits, temperature: float, top_k: int, top_p: float, uniforms, next_ids, stream=None) -> int:
