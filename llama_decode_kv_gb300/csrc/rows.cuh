@@ -36,7 +36,7 @@ struct RowsArgs {
 };
 
 // Workspace: one RowsJoin per CTA, then 2 P slots of slot_rows unnormalised output rows
-// (fp32), their running maxima (log2 domain) and their sums.
+// (fp32, [hd / 4][slot_rows] quads), their running maxima (log2 domain) and their sums.
 struct RowsJoin {
     int pieces;               // of the item that this CTA starts and another one finishes; 0: none
     int row0, tokens, head0;  // the item's first packed row, its tokens, its first query head

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
 #pragma unroll
                     for (int c = 0; c < C; c++) {
                         const int d = 4 * tx + 64 * c;
-                        if (d < A.hd) *(float4 *)(part + (size_t)r * A.hd + d) = o[i][c];
+                        if (d < A.hd) *(float4 *)(part + ((size_t)(d / 4) * A.slot_rows + r) * 4) = o[i][c];
                     }
                 }
             if (tid < nr) {
@@ -302,18 +302,18 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
 // Piece i of an item has, per row, the maximum m_i, the sum l_i and the unnormalised O_i:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i.
 // Block x looks after the item that attention CTA x starts and another one finishes (RowsJoin);
-// its pieces are slot 2x + 1 and the slots 2c of the CTAs behind x.  A thread takes four columns
-// of a row and goes over the pieces in order, so the result does not depend on timing.  With
-// kJoinShared pieces or more (a long context over the whole GPU, few rows) the eight warps of a
-// block share the pieces of a row instead and add up in shared memory.
+// its pieces are slot 2x + 1 and the slots 2c of the CTAs behind x.  A slot holds O as
+// [head_dim / 4][row] quads, so that the attention kernels' row-per-thread epilogue and the reads
+// here are contiguous over the rows; a warp takes 32 rows and every eighth quad, and the results
+// go out through shared memory as whole rows.  Pieces are added in order, so the result does not
+// depend on timing.  With kJoinShared pieces or more (a long context over the whole GPU, few rows)
+// the eight warps of a block share the pieces of 32 quads instead and add up in shared memory.
 constexpr int kJoinShared = 12;
 
-template <typename T> __device__ __forceinline__ void store4(T *p, float4 v, float f);
-template <> __device__ __forceinline__ void store4<float>(float *p, float4 v, float f) {
-    *(float4 *)p = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-}
-template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v, float f) {
-    *(uint2 *)p = make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+template <typename T> __device__ __forceinline__ void store4(T *p, float4 v);
+template <> __device__ __forceinline__ void store4<float>(float *p, float4 v) { *(float4 *)p = v; }
+template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v) {
+    *(uint2 *)p = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 __device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
@@ -323,91 +323,125 @@ __device__ __forceinline__ void add4(float4 &a, float f, const float4 &b) {
     a.w = fmaf(f, b.w, a.w);
 }
 
-template <typename T>
+template <typename T, int Q>  // Q: quads per thread, head_dim at most 32 Q
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsArgs A) {
+    constexpr int kRows = 32 * (32 * Q * (int)sizeof(T) + 16), kSums = 256 * 24;
+    __shared__ __align__(16) uint8_t buf[kRows > kSums ? kRows : kSums];
     pdl_wait();
     pdl_trigger();
     const RowsJoin J = ((const RowsJoin *)A.ws)[blockIdx.x];
     if (J.pieces == 0) return;
-    const int n = J.pieces, nr = J.tokens * A.G, cols = A.hd / 4, c0 = blockIdx.x;
-    const size_t sf = slot_floats(A.slot_rows, A.hd);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = J.pieces, nr = J.tokens * A.G, cols = A.hd / 4, c0 = blockIdx.x, R = A.slot_rows;
+    const size_t sf = slot_floats(R, A.hd);
     const float *slots = (const float *)(A.ws + join_bytes(A.P));
-    const float *stats = slots + (size_t)A.slot_rows * A.hd;  // maxima, then sums, of slot 0
+    const float *stats = slots + (size_t)R * A.hd;  // maxima, then sums, of slot 0
     auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * sf; };
     auto dest = [&](int r) {
         const int tok = r / A.G;
         return (T *)A.out + (size_t)(J.row0 + tok) * A.out_ld + (size_t)(J.head0 + r - tok * A.G) * A.hd;
     };
     if (n < kJoinShared) {
-        for (int e = blockIdx.y * 256 + threadIdx.x; e < nr * cols; e += gridDim.y * 256) {
-            const int r = e / cols, d = (e - r * cols) * 4;
-            float m[kJoinShared], M = -INFINITY, l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // row r, quads q, q + qs, ...: the maximum first, then every piece's share
+        auto row = [&](int r, int q0, int qs, float4 (&acc)[Q]) {
+            float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < n; i++) M = fmaxf(M, stats[slot(i) + r]);
 #pragma unroll
-            for (int i = 0; i < kJoinShared; i++) {
-                m[i] = i < n ? stats[slot(i) + r] : -INFINITY;
-                M = fmaxf(M, m[i]);
-            }
+            for (int k = 0; k < Q; k++) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int i = 0; i < n; i++) {
+                const float *s = slots + slot(i), mi = s[(size_t)R * A.hd + r], li = s[(size_t)R * (A.hd + 1) + r];
+                if (mi == -INFINITY) continue;  // the row saw nothing of this piece: its O may not have been written
+                const float f = exp2f(mi - M);
+                l = fmaf(f, li, l);
 #pragma unroll
-            for (int i = 0; i < kJoinShared; i++) {
-                if (m[i] == -INFINITY) continue;  // no piece, or the row saw nothing of it: O was not written
-                const float f = exp2f(m[i] - M);
-                l = fmaf(f, stats[slot(i) + A.slot_rows + r], l);
-                add4(acc, f, *(const float4 *)(slots + slot(i) + (size_t)r * A.hd + d));
+                for (int k = 0; k < Q; k++)
+                    if (q0 + k * qs < cols) add4(acc[k], f, *(const float4 *)(s + ((size_t)(q0 + k * qs) * R + r) * 4));
             }
-            store4<T>(dest(r) + d, acc, 1.0f / l);
+            const float inv = 1.0f / l;
+#pragma unroll
+            for (int k = 0; k < Q; k++) acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+        };
+        float4 acc[Q];
+        if (nr < 32) {  // a decode step: Q quads a thread, the rows side by side
+            const int qs = (cols + Q - 1) / Q;
+            for (int e = blockIdx.y * 256 + threadIdx.x; e < nr * qs; e += gridDim.y * 256) {
+                const int q = e / nr, r = e - q * nr;
+                row(r, q, qs, acc);
+#pragma unroll
+                for (int k = 0; k < Q; k++)
+                    if (q + k * qs < cols) store4<T>(dest(r) + 4 * (q + k * qs), acc[k]);
+            }
+            return;
+        }
+        const int pitch = A.hd * (int)sizeof(T) + 16, chunks = A.hd * (int)sizeof(T) / 16;
+        for (int r0 = blockIdx.y * 32; r0 < nr; r0 += gridDim.y * 32) {
+            row(min(r0 + lane, nr - 1), warp, 8, acc);
+#pragma unroll
+            for (int k = 0; k < Q; k++)
+                if (warp + 8 * k < cols) store4<T>((T *)(buf + lane * pitch) + 4 * (warp + 8 * k), acc[k]);
+            __syncthreads();
+            const int rows = min(32, nr - r0);
+            for (int e = threadIdx.x; e < rows * chunks; e += 256) {
+                const int rr = e / chunks, x = e - rr * chunks;
+                *(uint4 *)((uint8_t *)dest(r0 + rr) + x * 16) = *(const uint4 *)(buf + rr * pitch + x * 16);
+            }
+            __syncthreads();
         }
         return;
     }
-    __shared__ __align__(16) float red[8][256];
-    __shared__ float rm[8], rl[8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int r = blockIdx.y; r < nr; r += gridDim.y) {
+    float4 *ro = (float4 *)buf;                     // [8][32] sums of O
+    float *rm = (float *)(ro + 256), *rl = rm + 256;  // [8][32] maxima and sums
+    for (int e0 = blockIdx.y * 32; e0 < nr * cols; e0 += gridDim.y * 32) {
+        const int e = min(e0 + lane, nr * cols - 1), q = e / nr, r = e - q * nr;
         float M = -INFINITY, l = 0.f;
-        for (int i = warp + 8 * lane; i < n; i += 256) M = fmaxf(M, stats[slot(i) + r]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int i = warp; i < n; i += 8) M = fmaxf(M, stats[slot(i) + r]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int i = warp; i < n; i += 8) {
             const float mi = stats[slot(i) + r];
-            if (mi == -INFINITY) continue;
+            if (mi == -INFINITY) continue;  // the row saw nothing of this piece: its O may not have been written
             const float f = exp2f(mi - M);
-            l = fmaf(f, stats[slot(i) + A.slot_rows + r], l);
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-                if (lane + 32 * k < cols) add4(acc[k], f, *(const float4 *)(slots + slot(i) + (size_t)r * A.hd + 4 * (lane + 32 * k)));
+            l = fmaf(f, stats[slot(i) + R + r], l);
+            add4(acc, f, *(const float4 *)(slots + slot(i) + ((size_t)q * R + r) * 4));
         }
-        __syncthreads();  // the last row's sums have been read
-        if (lane == 0) {
-            rm[warp] = M;
-            rl[warp] = l;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; k++) *(float4 *)(red[warp] + 4 * (lane + 32 * k)) = acc[k];
+        ro[warp * 32 + lane] = acc;
+        rm[warp * 32 + lane] = M;
+        rl[warp * 32 + lane] = l;
         __syncthreads();
-        if (threadIdx.x < cols) {
-            float Ma = -INFINITY, la = 0.f;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < 8; w++) Ma = fmaxf(Ma, rm[w]);
+        if (warp == 0) {
+            M = -INFINITY;
+            for (int w = 0; w < 8; w++) M = fmaxf(M, rm[w * 32 + lane]);
+            l = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int w = 0; w < 8; w++) {
-                if (rm[w] == -INFINITY) continue;
-                const float f = exp2f(rm[w] - Ma);
-                la = fmaf(f, rl[w], la);
-                add4(a, f, *(const float4 *)(red[w] + 4 * threadIdx.x));
+                if (rm[w * 32 + lane] == -INFINITY) continue;
+                const float f = exp2f(rm[w * 32 + lane] - M);
+                l = fmaf(f, rl[w * 32 + lane], l);
+                add4(acc, f, ro[w * 32 + lane]);
             }
-            store4<T>(dest(r) + 4 * threadIdx.x, a, 1.0f / la);
+            const float inv = 1.0f / l;
+            if (e0 + lane < nr * cols)
+                store4<T>(dest(r) + 4 * q, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         }
+        __syncthreads();
     }
 }
 
 cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
     if (a.P < 2) return cudaSuccess;
-    // an item's rows are spread over up to 16 blocks
-    const int gy = (int)std::min<long long>(16, ((long long)a.slot_rows * (a.hd / 4) + 255) / 256);
+    // an item's rows, 32 at a time, over up to 8 blocks
+    const int gy = std::min(8, (a.slot_rows + 31) / 32 * 2);
     const dim3 grid(a.P - 1, gy);
-    return bf16 ? launch_pdl(rows_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a)
-                : launch_pdl(rows_join_kernel<float>, grid, dim3(256), 0, s, a);
+    if (a.hd <= 64)
+        return bf16 ? launch_pdl(rows_join_kernel<__nv_bfloat16, 2>, grid, dim3(256), 0, s, a)
+                    : launch_pdl(rows_join_kernel<float, 2>, grid, dim3(256), 0, s, a);
+    if (a.hd <= 128)
+        return bf16 ? launch_pdl(rows_join_kernel<__nv_bfloat16, 4>, grid, dim3(256), 0, s, a)
+                    : launch_pdl(rows_join_kernel<float, 4>, grid, dim3(256), 0, s, a);
+    return bf16 ? launch_pdl(rows_join_kernel<__nv_bfloat16, 8>, grid, dim3(256), 0, s, a)
+                : launch_pdl(rows_join_kernel<float, 8>, grid, dim3(256), 0, s, a);
 }
 
 // ---- launch

@@ -6,7 +6,9 @@
 // token * G + head), so keys and values are read once for the whole group, and a decode step is
 // the same kernel with one tile that is mostly empty.  An item is two such tiles, one behind
 // the other, over the same keys: while the softmax of one runs, the tensor core works for the
-// other.  Items are cut into equal ranges of 128-position blocks (rows_plan.h), one persistent
+// other.  An item of 64-wide heads with one tile only (a decode step, the end of a chunk) is worked on
+// twice over: the first softmax group takes its even blocks, the second the odd ones, each with its own S, O,
+// maximum and sum, added up at the end.  Items are cut into equal ranges of 128-position blocks (rows_plan.h), one persistent
 // CTA per SM; pieces of items leave as partial states for rows_join_kernel.
 //
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
@@ -51,11 +53,14 @@ struct RowsTcArgs {
     int TT;      // tokens per tile
     int box;     // positions per key / value box
     int stages;  // ring depth
+    int wide;    // output heads begin on 32-byte boundaries and are multiples of 16 long
 };
 
 struct TcBars {
     uint64_t kv_full[16], kv_empty[16];
     uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
+    uint64_t x_full, x_free;       // twin items: group 1's statistics stand in xm, xl; group 0 is done
+    float xm[128], xl[128];
     uint32_t tmem;
     int stop;
 };
@@ -218,6 +223,10 @@ __device__ __forceinline__ void weights64(const uint32_t (&s)[64], uint64_t c2, 
     }
 }
 
+__device__ __forceinline__ void st_global32(void *p, const uint32_t (&h)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), SLM_I8(h, 0) : "memory");
+}
+
 // One lane of the (converged) warp, always the same.  Behind this predicate the compiler keeps the
 // operands of the asynchronous instructions in uniform registers; behind `lane == 0` it moved them
 // there one by one, ~100 cycles an MMA, which bound the kernel.
@@ -250,16 +259,31 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *sta
     return true;
 }
 
-// The blocks of a piece that tile i takes part in, and its tokens.
+// The blocks of a piece that softmax group i works on, and its tokens: its own tile's, or (twin)
+// every second block of tile 0's.
 struct TileView {
-    int n, tok0, ntok;  // blocks from p.kb0 on; first token in the sequence; tokens
+    bool twin;
+    int n, tok0, ntok;  // blocks; first token in the sequence; tokens
+    int first, step;    // block j is first + j step
 };
+template <bool TWIN>
 __device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece &p, int TT, int PT, int i) {
     TileView v;
-    v.tok0 = p.t * PT + i * TT;
-    v.ntok = max(0, min(TT, sr.n - v.tok0));
-    const int nb = v.ntok > 0 ? (sr.ctx + v.tok0 + v.ntok + kTcBlk - 1) / kTcBlk : 0;
-    v.n = max(0, min(p.kb1, nb) - p.kb0);
+    const int left = sr.n - p.t * PT;  // tokens from the item's first on, at least 1
+    v.twin = TWIN && left <= TT;
+    if (v.twin) {
+        v.tok0 = p.t * PT;
+        v.ntok = left;
+        v.n = (p.kb1 - p.kb0 + 1 - i) >> 1;
+        v.first = p.kb0 + i;
+        v.step = 2;
+    } else {
+        v.tok0 = p.t * PT + i * TT;
+        v.ntok = max(0, min(TT, sr.n - v.tok0));
+        v.n = v.ntok > 0 ? max(0, min(p.kb1, (sr.ctx + v.tok0 + v.ntok + kTcBlk - 1) / kTcBlk) - p.kb0) : 0;
+        v.first = p.kb0;
+        v.step = 1;
+    }
     return v;
 }
 
@@ -275,6 +299,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     // Tensor memory columns: S 128 i, O 256 + HDP i.  P (64 columns) has its own where O leaves
     // room, else the upper half of S, which the softmax holds in registers by then.
     constexpr uint32_t kO = 256, kP = HDP == 64 ? 384 : 64, kPStep = HDP == 64 ? 64 : 128;
+    // One-tile items twice over only where it pays: a block of 64-wide heads arrives faster than one
+    // group's chain of S, softmax and P V (4 x 32,768 positions: 72 us with one group, 52 with two);
+    // 128-wide ones come at 95% of the copy rate with one group, and joining the halves costs 4%.
+    constexpr bool kTwin = HDP == 64;
     const RowsArgs &A = T.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -301,6 +329,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             mbar_init(&B->o_full[i], 1);
         }
         mbar_init(&B->drain, 1);
+        mbar_init(&B->x_full, 4);
+        mbar_init(&B->x_free, 4);
         B->stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -328,17 +358,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         const uint32_t tS = tmem + lanes + 128 * i, tP = tmem + lanes + kP + kPStep * i, tO = tmem + lanes + kO + HDP * i;
         const int tok = r / G, head = r - tok * G;
         const float c = A.scale_log2;
-        uint32_t sp = 0, op = 0;  // phases of s_full, o_full
+        uint32_t sp = 0, op = 0, xp = 0;  // phases of s_full; of both o_full (bit i); of x_full, x_free
+        bool lent = false;                // group 1: group 0 may still read O and xm, xl of a twin item
         bool joined = false;
         while (w.next(seq, A.nseq, A.geom, p)) {
             const SeqRows sr = seq[p.s];
-            const TileView v = tile_view(sr, p, TT, PT, i);
+            const TileView v = tile_view<kTwin>(sr, p, TT, PT, i);
             const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
             const bool valid = tok < v.ntok && r < TT * G;
             const bool busy = __any_sync(0xffffffffu, valid);    // else only the hand-offs
             const int seen = sr.ctx + v.tok0 + tok + 1;          // positions the row sees
             float m = -INFINITY, l = 0.f;
             bool ok = true;
+            const uint32_t op0 = op;  // phases that this piece's O completes
+            if (v.twin) {
+                op ^= (p.kb1 - p.kb0 > 1) ? 3u : 1u;
+            } else {
+                const TileView u = tile_view<kTwin>(sr, p, TT, PT, 1 - i);
+                op ^= (uint32_t)(v.n > 0) << i | (uint32_t)(u.n > 0) << (1 - i);
+            }
+            if (i == 1 && lent && v.n > 0) {
+                if (!tc_wait(&B->x_free, xp, A.status, stop)) break;
+                xp ^= 1;
+                lent = false;
+            }
             if (!whole && p.kb0 == 0) {
                 joined = true;
                 if (tid == 0) write_join(A, blockIdx.x, seq, unit, &p);
@@ -351,7 +394,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     __syncwarp();
                     // Keys 0-63 for the maximum only, keys 64-127 to stay, then 0-63 once more: the
                     // row fits the registers in halves, and tensor memory is quick to read twice.
-                    const int lim = seen - (p.kb0 + j) * kTcBlk;  // keys of the block that the row sees
+                    const int lim = seen - (v.first + j * v.step) * kTcBlk;  // keys of the block that the row sees
                     const bool cut = __any_sync(0xffffffffu, lim < kTcBlk);
                     uint32_t lo[64], hi[64];
                     tmem_ld64(tS, lo);
@@ -403,41 +446,82 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(&B->p_ready[i]);
             }
             if (!ok) break;
-            if (v.n > 0) {
-                if (!tc_wait(&B->o_full[i], op, A.status, stop)) break;
-                op ^= 1;
+            // twin: group 1 hands its statistics over, group 0 adds both halves up
+            const bool both = v.twin && p.kb1 - p.kb0 > 1;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (both && i == 1) {
+                B->xm[r] = m;
+                B->xl[r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B->x_full);
+                lent = true;
+                continue;
             }
-            if (!busy) continue;
+            if (v.n > 0 && !tc_wait(&B->o_full[i], op0 >> i & 1, A.status, stop)) break;
+            if (both) {
+                if (!tc_wait(&B->o_full[1], op0 >> 1 & 1, A.status, stop)) break;
+                if (!tc_wait(&B->x_full, xp, A.status, stop)) break;
+                xp ^= 1;
+                const float m1 = B->xm[r], M = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : fast_exp2((m - M) * c);
+                f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - M) * c);
+                l = l * f0 + B->xl[r] * f1;
+                m = M;
+            }
+            if (!busy || (v.twin && i == 1)) {
+                __syncwarp();
+                if (both && lane == 0) mbar_arrive(&B->x_free);
+                continue;
+            }
             tc_after();
             __syncwarp();
+            // O of this row, 32 columns at a time
+            auto row_o = [&](int d, uint32_t (&o)[32]) {
+                tmem_ld32(tO + d, o);
+                if (both) {
+                    uint32_t o1[32];
+                    tmem_ld32(tO + HDP + d, o1);
+#pragma unroll
+                    for (int k = 0; k < 32; k++)
+                        o[k] = __float_as_uint(__uint_as_float(o[k]) * f0 + __uint_as_float(o1[k]) * f1);
+                }
+            };
             if (whole) {
                 const float inv = 1.0f / l;
                 uint16_t *dst = (uint16_t *)A.out + (size_t)(sr.row0 + v.tok0 + tok) * A.out_ld + (size_t)(p.g * G + head) * A.hd;
 #pragma unroll 1
                 for (int d = 0; d < HDP; d += 32) {
                     uint32_t o[32];
-                    tmem_ld32(tO + d, o);
+                    row_o(d, o);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        uint32_t h[4];
+                    for (int k = 0; k < 32; k += 16) {
+                        uint32_t h[8];
 #pragma unroll
-                        for (int q = 0; q < 4; q++)
+                        for (int q = 0; q < 8; q++)
                             h[q] = pack_bf16x2(__uint_as_float(o[k + 2 * q]) * inv, __uint_as_float(o[k + 2 * q + 1]) * inv);
-                        if (valid && d + k < A.hd) *(uint4 *)(dst + d + k) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if (!valid) continue;
+                        if (T.wide) {  // whole 32-byte sectors: a lane writes its own row
+                            if (d + k < A.hd) st_global32(dst + d + k, h);
+                        } else {
+                            if (d + k < A.hd) *(uint4 *)(dst + d + k) = make_uint4(h[0], h[1], h[2], h[3]);
+                            if (d + k + 8 < A.hd) *(uint4 *)(dst + d + k + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
                     }
                     __syncwarp();
                 }
             } else {
                 float *part = slot_ptr(A, piece_slot(blockIdx.x, p));
-                const int row = i * TT * G + r;
+                const int row = (v.twin ? 0 : i) * TT * G + r;
                 if (v.n > 0) {
 #pragma unroll 1
                     for (int d = 0; d < HDP; d += 32) {
                         uint32_t o[32];
-                        tmem_ld32(tO + d, o);
+                        row_o(d, o);
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            if (valid && d + k < A.hd) *(uint4 *)(part + (size_t)row * A.hd + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            if (valid && d + k < A.hd)
+                                *(uint4 *)(part + ((size_t)((d + k) / 4) * A.slot_rows + row) * 4) =
+                                    make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                         __syncwarp();
                     }
                 }
@@ -448,6 +532,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 }
             }
             tc_before();
+            __syncwarp();
+            if (both && lane == 0) mbar_arrive(&B->x_free);
         }
         if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
     } else if (warp == 8) {
@@ -456,97 +542,133 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         const int ksteps = (A.hd + 15) / 16;
         // descriptors of the query tiles and of ring stage 0
         const uint32_t dq = desc_lo(sq, 16), dk = desc_lo(ring, 16), dv = desc_lo(ring, kPanel);
-        uint32_t st = 0, ph = 0;        // the ring stage that comes next, its phase
-        uint32_t qph[2] = {0, 0}, pph[2] = {0, 0};
+        // the ring stages of the next block's K and V (K, V, K, V, ... in the ring), and their phases
+        uint32_t ks = 0, kph = 0, vs = 1, vph = 0;
+        uint32_t qph = 0, pph = 0;  // phases of q_full and of p_half, p_ready: bit i
         bool ok = true;
-        auto next_stage = [&](uint32_t &s) {
-            if (++s == (uint32_t)T.stages) {
-                s = 0;
+        auto forward = [&](uint32_t &st, uint32_t &ph) {
+            st += 2;
+            if (st >= (uint32_t)T.stages) {
+                st -= T.stages;
                 ph ^= 1;
             }
         };
-        auto issue_s = [&](int i, uint32_t ks) {  // S_i = Q_i K^T
-            const uint32_t a = dq + i * (NP * kPanel / 16), b = dk + ks * (NP * kPanel / 16);
+        auto issue_s = [&](int i, int qi) {  // S_i = Q_qi K^T
+            const uint32_t a = dq + qi * (NP * kPanel / 16), b = dk + ks * (NP * kPanel / 16);
 #pragma unroll
             for (int k = 0; k < HDP / 16; k++) {
                 const int off = (k >> 2) * (kPanel / 16) + (k & 3) * 2;
                 if (k < ksteps) mma_ss(tmem + 128 * i, a + off, b + off, idS, k != 0);
             }
         };
-        auto issue_o = [&](int i, uint32_t vs, int half, bool first) {  // O_i (+)= P_i V, 64 keys
+        auto issue_o = [&](int i, int half, bool first) {  // O_i (+)= P_i V, 64 keys
             const uint32_t b = dv + vs * (NP * kPanel / 16);
             const uint32_t a = tmem + kP + kPStep * i;
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 mma_ts(tmem + kO + HDP * i, a + 8 * (4 * half + k), b + (4 * half + k) * 128, idO, !(first && k == 0));
         };
+        // P_i V for one block of group i; `last`: O_i is complete
+        auto weigh = [&](int i, bool first, bool last) {
+            if (!tc_wait(&B->p_half[i], pph >> i & 1, A.status, stop)) return false;
+            tc_after();
+            if (elect_one()) issue_o(i, 1, first);
+            if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
+            pph ^= 1u << i;
+            tc_after();
+            if (elect_one()) {
+                issue_o(i, 0, false);
+                if (last) tc_commit(&B->o_full[i]);
+            }
+            return true;
+        };
+        // V of the next block; the rows from `tail` on are nobody's and become zero: whole 128-byte
+        // rows, so the swizzle does not matter
+        auto take_v = [&](int tail) {
+            if (!tc_wait(&B->kv_full[vs], vph, A.status, stop)) return false;
+            if (tail < kTcBlk) {
+                const uint32_t v0 = smem_addr(ring) + vs * NP * kPanel + tail * 128;
+                for (int pn = 0; pn < NP; pn++)
+                    for (int x = lane * 16; x < (kTcBlk - tail) * 128; x += 512)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + pn * kPanel + x), "r"(0)
+                                     : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            }
+            return true;
+        };
+        auto drop_v = [&] {
+            if (elect_one()) tc_commit(&B->kv_empty[vs]);
+            forward(vs, vph);
+        };
+        auto drop_k = [&] {
+            if (elect_one()) tc_commit(&B->kv_empty[ks]);
+            forward(ks, kph);
+        };
         while (ok && w.next(seq, A.nseq, A.geom, p)) {
             const SeqRows sr = seq[p.s];
             const int n = p.kb1 - p.kb0;
-            const int nt[2] = {tile_view(sr, p, TT, PT, 0).n, tile_view(sr, p, TT, PT, 1).n};
             const int L = sr.ctx + min(p.t * PT + PT, sr.n);  // positions the item sees
             const int tail = p.kb1 == p.nb ? L - (p.nb - 1) * kTcBlk : kTcBlk;  // of the last block
-            uint32_t ks = st;
-            if (!(ok = tc_wait(&B->kv_full[ks], ph, A.status, stop))) break;
-            next_stage(st);
+            const TileView v0 = tile_view<kTwin>(sr, p, TT, PT, 0);
+            if (v0.twin) {
+                // one tile: block b belongs to group b & 1
+                auto score = [&](int b) {
+                    if (!tc_wait(&B->kv_full[ks], kph, A.status, stop)) return false;
+                    tc_after();
+                    if (elect_one()) {
+                        issue_s(b & 1, 0);
+                        tc_commit(&B->s_full[b & 1]);
+                        if (b == n - 1) tc_commit(&B->q_empty[0]);
+                    }
+                    drop_k();
+                    return true;
+                };
+                if (!(ok = tc_wait(&B->q_full[0], qph & 1, A.status, stop))) break;
+                qph ^= 1;
+                if (!(ok = score(0)) || (n > 1 && !(ok = score(1)))) break;
+                for (int b = 0; b < n; b++) {
+                    if (!(ok = take_v(b == n - 1 ? tail : kTcBlk)) || !(ok = weigh(b & 1, b < 2, b + 2 >= n))) break;
+                    drop_v();
+                    if (b + 2 < n && !(ok = score(b + 2))) break;
+                }
+                continue;
+            }
+            const int nt[2] = {v0.n, tile_view<kTwin>(sr, p, TT, PT, 1).n};
+            if (!(ok = tc_wait(&B->kv_full[ks], kph, A.status, stop))) break;
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 if (nt[i] == 0) continue;
-                if (!(ok = tc_wait(&B->q_full[i], qph[i], A.status, stop))) break;
-                qph[i] ^= 1;
+                if (!(ok = tc_wait(&B->q_full[i], qph >> i & 1, A.status, stop))) break;
+                qph ^= 1u << i;
                 tc_after();
                 if (elect_one()) {
-                    issue_s(i, ks);
+                    issue_s(i, i);
                     tc_commit(&B->s_full[i]);
                     if (nt[i] == 1) tc_commit(&B->q_empty[i]);
                 }
             }
             if (!ok) break;
-            if (elect_one()) tc_commit(&B->kv_empty[ks]);
-            for (int j = 0; j < n && ok; j++) {
-                const uint32_t vs = st;
-                if (!(ok = tc_wait(&B->kv_full[vs], ph, A.status, stop))) break;
-                next_stage(st);
-                if (j == n - 1 && tail < kTcBlk) {
-                    // V rows that nobody sees: whole 128-byte rows, so the swizzle does not matter
-                    const uint32_t v0 = smem_addr(ring) + vs * NP * kPanel + tail * 128;
-                    for (int pn = 0; pn < NP; pn++)
-                        for (int x = lane * 16; x < (kTcBlk - tail) * 128; x += 512)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + pn * kPanel + x), "r"(0)
-                                         : "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
+            drop_k();
+            for (int j = 0; j < n; j++) {
+                if (!(ok = take_v(j == n - 1 ? tail : kTcBlk))) break;
                 const bool more = j + 1 < n;
-                if (more) ks = st;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    if (j < nt[i]) {
-                        if (!(ok = tc_wait(&B->p_half[i], pph[i], A.status, stop))) break;
-                        tc_after();
-                        if (elect_one()) issue_o(i, vs, 1, j == 0);
-                        if (!(ok = tc_wait(&B->p_ready[i], pph[i], A.status, stop))) break;
-                        pph[i] ^= 1;
-                        tc_after();
-                        if (elect_one()) {
-                            issue_o(i, vs, 0, false);
-                            if (j == nt[i] - 1) tc_commit(&B->o_full[i]);
-                        }
-                    }
-                    if (i == 1 && elect_one()) tc_commit(&B->kv_empty[vs]);
+                    if (j < nt[i] && !(ok = weigh(i, j == 0, j == nt[i] - 1))) break;
+                    if (i == 1) drop_v();
                     if (i == 0 && more) {
-                        if (!(ok = tc_wait(&B->kv_full[ks], ph, A.status, stop))) break;
-                        next_stage(st);
+                        if (!(ok = tc_wait(&B->kv_full[ks], kph, A.status, stop))) break;
                         tc_after();
                     }
                     if (j + 1 < nt[i] && elect_one()) {
-                        issue_s(i, ks);
+                        issue_s(i, i);
                         tc_commit(&B->s_full[i]);
                         if (j + 2 == nt[i]) tc_commit(&B->q_empty[i]);
                     }
                 }
                 if (!ok) break;
-                if (more && elect_one()) tc_commit(&B->kv_empty[ks]);
+                if (more) drop_k();
             }
         }
         if (!ok) {  // what was issued still runs: wait for it, bounded
@@ -608,8 +730,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     if (kb == p.kb0 && is_v == 0) {  // the queries, behind the first keys
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
-                            const TileView v = tile_view(sr, p, TT, PT, i);
-                            if (v.n == 0) continue;
+                            const TileView v = tile_view<kTwin>(sr, p, TT, PT, i);
+                            if (v.n == 0 || (v.twin && i == 1)) continue;
                             if (qn[i] > 0 && !(ok = tc_wait(&B->q_empty[i], (qn[i] - 1) & 1, A.status, stop))) break;
                             qn[i]++;
                             if (lane == 0) {
@@ -669,6 +791,7 @@ cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {
     t.a = a;
     t.TT = a.geom.PT / 2;
     t.stages = tc_stages(a.hd, a.nseq);
+    t.wide = ((uintptr_t)a.out & 31) == 0 && a.hd % 16 == 0 && a.out_ld % 16 == 0;
     const bool paged = a.kv.table != nullptr;
     const uint64_t hb = (uint64_t)a.hd * 2;  // bytes of a head
     const uint64_t qd[] = {(uint64_t)a.hd, (uint64_t)a.H, (uint64_t)a.rows}, qs[] = {hb, (uint64_t)a.q_ld * 2};
