@@ -111,7 +111,7 @@ int attn_fail(int code, const char *fmt, ...);  // records the text, returns the
 // The joining launch: every item that several CTAs share, from its partial states.
 cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 
-// CUDA-core attention: any head_dim up to 256, fp32 or bf16.
+// CUDA-core attention: fp32, and bf16 heads wider than 128.
 int rows_simt_tile(int rows, int nseq, int G, int hd);  // query rows (token, head) per item
 int rows_simt_ctas(int sms, int hd, int R, int nseq);
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s);

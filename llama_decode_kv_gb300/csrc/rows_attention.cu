@@ -50,10 +50,14 @@ __device__ __forceinline__ size_t rows_kv_offset(const RowsArgs &A, bool is_v, i
     return row * A.hd;
 }
 
+// Two key / value buffers for fp32 heads of up to 128: the next block is copied (cp.async) while
+// this one is multiplied.  bf16 has to be widened on the way and 256-wide heads fill the shared
+// memory, so those load a block when they need it.
+template <typename T, int HDP> constexpr bool kSimtAsync = sizeof(T) == 4 && HDP <= 128;
 template <int HDP> constexpr int simt_ld() { return HDP + 4; }
-template <int HDP, int R> constexpr size_t simt_smem(int nseq) {
-    return (size_t)(R + 2 * kSimtBlk) * simt_ld<HDP>() * 4 + (size_t)R * (kSimtBlk + 4) * 4 + 3 * R * 4 +
-           (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 + 16;
+template <typename T, int HDP, int R> constexpr size_t simt_smem(int nseq) {
+    return (size_t)(R + 2 * kSimtBlk * (kSimtAsync<T, HDP> ? 2 : 1)) * simt_ld<HDP>() * 4 + (size_t)R * (kSimtBlk + 4) * 4 +
+           3 * R * 4 + (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 + 16;
 }
 
 template <typename T, int HDP, int R>
@@ -68,7 +72,8 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
     long long *wstart = (long long *)smem;
     SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
     float *qs = (float *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
-    float *ks = qs + R * LD, *vs = ks + kSimtBlk * LD, *ps = vs + kSimtBlk * LD;
+    constexpr bool ASYNC = kSimtAsync<T, HDP>;
+    float *kv = qs + R * LD, *ps = kv + (ASYNC ? 4 : 2) * kSimtBlk * LD;  // [buffer][keys, values][64][LD]
     float *alpha = ps + R * PLD, *mrow = alpha + R, *lrow = mrow + R;
     const int tid = threadIdx.x;
     const int tx = tid & 15, kq = (tid >> 4) % KQ, ty = (tid >> 4) / KQ;
@@ -110,24 +115,48 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
         for (int i = 0; i < 4; i++)
 #pragma unroll
             for (int c = 0; c < C; c++) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool some = 4 * ty < nr;  // this thread's rows exist (else it only loads and keeps step)
 
-        for (int kb = p.kb0; kb < p.kb1; kb++) {
+        // keys and values of block kb into buffer b; rows that no row of the item sees are zero
+        auto load = [&](int kb, int b) {
+            float *ks = kv + (size_t)b * 2 * kSimtBlk * LD, *vs = ks + kSimtBlk * LD;
             const int k0 = kb * kSimtBlk;
-            // keys and values of the block; rows that no row of the item sees are zero
             for (int e = tid; e < kSimtBlk * (HDP / E); e += kSimtThreads) {
                 const int j = e / (HDP / E), d = (e - j * (HDP / E)) * E;
                 float *kd = ks + j * LD + d, *vd = vs + j * LD + d;
                 if (k0 + j < L && d < A.hd) {
-                    widen16((const T *)A.kv.k + rows_kv_offset(A, false, p.s, sr.row0, p.g, k0 + j) + d, kd);
-                    widen16((const T *)A.kv.v + rows_kv_offset(A, true, p.s, sr.row0, p.g, k0 + j) + d, vd);
+                    const T *k = (const T *)A.kv.k + rows_kv_offset(A, false, p.s, sr.row0, p.g, k0 + j) + d;
+                    const T *v = (const T *)A.kv.v + rows_kv_offset(A, true, p.s, sr.row0, p.g, k0 + j) + d;
+                    if (ASYNC) {
+                        cp_async16(kd, k);
+                        cp_async16(vd, v);
+                    } else {
+                        widen16(k, kd);
+                        widen16(v, vd);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < E; i++) kd[i] = vd[i] = 0.f;
                 }
             }
+            if (ASYNC) cp_async_commit();
+        };
+        if (ASYNC) load(p.kb0, 0);
+
+        for (int kb = p.kb0; kb < p.kb1; kb++) {
+            const int k0 = kb * kSimtBlk, buf = ASYNC ? (kb - p.kb0) & 1 : 0;
+            float *ks = kv + (size_t)buf * 2 * kSimtBlk * LD, *vs = ks + kSimtBlk * LD;
+            if (!ASYNC) {
+                load(kb, 0);
+            } else if (kb + 1 < p.kb1) {
+                load(kb + 1, buf ^ 1);  // its last readers are behind the barrier that ended block kb - 1
+                cp_async_wait_upto(1);
+            } else {
+                cp_async_wait_upto(0);
+            }
             __syncthreads();
             // S: rows 4 ty + i, keys kq * 16 + tx (+ 16 j)
-            {
+            if (some) {
                 float s[4][KS];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -201,8 +230,9 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
                     o[i][c].z *= f[i];
                     o[i][c].w *= f[i];
                 }
+            const int jend = some ? (kq + 1) * (kSimtBlk / KQ) : 0;
 #pragma unroll 2
-            for (int j = kq * (kSimtBlk / KQ); j < (kq + 1) * (kSimtBlk / KQ); j += 4) {
+            for (int j = kq * (kSimtBlk / KQ); j < jend; j += 4) {
                 float4 pv[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) pv[i] = *(const float4 *)(ps + (4 * ty + i) * PLD + j);
@@ -223,7 +253,8 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
             }
             __syncthreads();  // keys, values and weights are free again
         }
-        // the key groups' sums of O (over the key buffer: KQ R rows are exactly its length)
+        // the key groups' sums of O (over the first key buffer: KQ R rows are exactly its length)
+        float *ks = kv;
         if (KQ > 1) {
 #pragma unroll
             for (int i = 0; i < 4; i++)
@@ -454,10 +485,10 @@ int rows_simt_tile(int rows, int nseq, int G, int hd) {
     return hd <= 128 ? 64 : 32;
 }
 
-static size_t simt_bytes(int hd, int R, int nseq) {
-    if (hd <= 64) return R == 16 ? simt_smem<64, 16>(nseq) : simt_smem<64, 64>(nseq);
-    if (hd <= 128) return R == 16 ? simt_smem<128, 16>(nseq) : simt_smem<128, 64>(nseq);
-    return R == 16 ? simt_smem<256, 16>(nseq) : simt_smem<256, 32>(nseq);
+static size_t simt_bytes(int hd, int R, int nseq) {  // fp32: bf16 needs no more
+    if (hd <= 64) return R == 16 ? simt_smem<float, 64, 16>(nseq) : simt_smem<float, 64, 64>(nseq);
+    if (hd <= 128) return R == 16 ? simt_smem<float, 128, 16>(nseq) : simt_smem<float, 128, 64>(nseq);
+    return R == 16 ? simt_smem<float, 256, 16>(nseq) : simt_smem<float, 256, 32>(nseq);
 }
 
 // CTAs of a launch: as many as the shared memory lets run at a time, at most two per SM (the
@@ -467,21 +498,18 @@ int rows_simt_ctas(int sms, int hd, int R, int nseq) {
 }
 
 template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsArgs &a, cudaStream_t s) {
-    const size_t smem = simt_smem<HDP, R>(a.nseq);
+    const size_t smem = simt_smem<T, HDP, R>(a.nseq);
     cudaError_t e = cudaFuncSetAttribute(rows_simt_kernel<T, HDP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_simt_kernel<T, HDP, R>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
 }
 
-template <typename T> static cudaError_t launch_simt_hd(const RowsArgs &a, cudaStream_t s) {
-    const bool small = a.geom.PT * a.G <= 16;
-    if (a.hd <= 64) return small ? launch_simt<T, 64, 16>(a, s) : launch_simt<T, 64, 64>(a, s);
-    if (a.hd <= 128) return small ? launch_simt<T, 128, 16>(a, s) : launch_simt<T, 128, 64>(a, s);
-    return small ? launch_simt<T, 256, 16>(a, s) : launch_simt<T, 256, 32>(a, s);
-}
-
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_simt_hd<__nv_bfloat16>(a, s) : launch_simt_hd<float>(a, s);
+    const bool small = a.geom.PT * a.G <= 16;
+    if (bf16) return small ? launch_simt<__nv_bfloat16, 256, 16>(a, s) : launch_simt<__nv_bfloat16, 256, 32>(a, s);
+    if (a.hd <= 64) return small ? launch_simt<float, 64, 16>(a, s) : launch_simt<float, 64, 64>(a, s);
+    if (a.hd <= 128) return small ? launch_simt<float, 128, 16>(a, s) : launch_simt<float, 128, 64>(a, s);
+    return small ? launch_simt<float, 256, 16>(a, s) : launch_simt<float, 256, 32>(a, s);
 }
 
 }  // namespace slm
