@@ -190,10 +190,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-__device__ __forceinline__ void mask64(uint32_t (&s)[64], int lim) {
+// Keys from `lim` on become -infinity.  `all` (at most any lane's lim): no lane's key before it does,
+// so groups of 16 below it are left alone (two instructions an element at half rate: a diagonal
+// block took twice as long as the others).
+__device__ __forceinline__ void mask64(uint32_t (&s)[64], int lim, int all) {
 #pragma unroll
-    for (int k = 0; k < 64; k++)
-        if (k >= lim) s[k] = 0xff800000u;  // -infinity
+    for (int k0 = 0; k0 < 64; k0 += 16)
+        if (k0 + 16 > all) {
+#pragma unroll
+            for (int k = k0; k < k0 + 16; k++)
+                if (k >= lim) s[k] = 0xff800000u;
+        }
 }
 
 __device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
@@ -395,13 +402,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     // Keys 0-63 for the maximum only, keys 64-127 to stay, then 0-63 once more: the
                     // row fits the registers in halves, and tensor memory is quick to read twice.
                     const int lim = seen - (v.first + j * v.step) * kTcBlk;  // keys of the block that the row sees
-                    const bool cut = __any_sync(0xffffffffu, lim < kTcBlk);
+                    const int all = __reduce_min_sync(0xffffffffu, lim);
+                    const bool cut = all < kTcBlk;
                     uint32_t lo[64], hi[64];
                     tmem_ld64(tS, lo);
-                    if (cut) mask64(lo, lim);
+                    if (cut) mask64(lo, lim, all);
                     float mb = max64(lo);
                     tmem_ld64(tS + 64, hi);
-                    if (cut) mask64(hi, lim - 64);
+                    if (cut) mask64(hi, lim - 64, all - 64);
                     mb = fmaxf(mb, max64(hi));
                     if (j == 0) {
                         m = mb;
@@ -431,7 +439,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     if (lane == 0) mbar_arrive(&B->p_half[i]);
                     __syncwarp();
                     tmem_ld64(tS, lo);
-                    if (cut) mask64(lo, lim);
+                    if (cut) mask64(lo, lim, all);
                     weights64(lo, c2, mc2, sum, tP);
                     float a, b;
                     unpack2(add2(sum[0], sum[1]), a, b);

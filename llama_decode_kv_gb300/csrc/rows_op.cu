@@ -127,11 +127,11 @@ static RowsTiling rows_tiling(int sms, int dtype, int rows, int nseq, int H, int
     RowsTiling t{};
     const int G = H / KV;
     if (on_tensor_cores(dtype, hd)) {
-        t.geom = {KV, 2 * (128 / G), 128, 1};
+        t.geom = {KV, 2 * (128 / G), 7, 1};
         t.P = sms;
     } else {
         const int R = rows_simt_tile(rows, nseq, G, hd);
-        t.geom = {KV, R / G, 64, 1};
+        t.geom = {KV, R / G, 6, 1};
         t.P = rows_simt_ctas(sms, hd, R, nseq);
     }
     t.slot_rows = (int)std::min<long long>((long long)t.geom.PT * G, (long long)std::max(rows, 1) * G);
@@ -155,7 +155,7 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     a.slot_rows = t.slot_rows;
     a.geom = t.geom;
     // Items of a few blocks stay whole: a block takes about 1 us, the joining launch 3.
-    a.geom.split = longest > (on_tensor_cores(dtype, a.hd) ? 4 : 2) * t.geom.BLK;
+    a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
     a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)a.hd));
     const bool bf16 = dtype == SLM_BF16;

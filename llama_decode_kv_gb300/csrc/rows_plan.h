@@ -86,24 +86,23 @@ SLM_HD unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned
 struct RowsGeom {
     int KV;      // kv heads
     int PT;      // tokens per item
-    int BLK;     // positions per block
+    int shift;   // log2 of the positions per block (BLK)
     int split;   // 1: ranges cut through items; 0: items stay whole
 };
 
 SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
 
 SLM_HD int item_blocks(const RowsGeom &g, int ctx, int n, int t) {
-    const long long end = (long long)(t + 1) * g.PT;
-    const int last = end < n ? (int)end : n;
-    return (int)(((long long)ctx + last + g.BLK - 1) / g.BLK);
+    const int left = n - t * g.PT, end = left < g.PT ? n : n - left + g.PT;
+    return (int)(((unsigned)ctx + (unsigned)end + (1u << g.shift) - 1) >> g.shift);
 }
 
 // Units of the items [0, t) of one kv head of a sequence.
 SLM_HD long long head_units(const RowsGeom &g, int ctx, int n, int t) {
     if (t <= 0) return 0;
     const int T = item_count(g, n), full = t < T ? t : T - 1;
-    long long s = full > 0 ? (long long)floor_sum((unsigned)full, (unsigned)g.BLK, (unsigned)g.PT,
-                                                  (unsigned)ctx + g.PT + g.BLK - 1)
+    long long s = full > 0 ? (long long)floor_sum((unsigned)full, 1u << g.shift, (unsigned)g.PT,
+                                                  (unsigned)ctx + g.PT + (1u << g.shift) - 1)
                            : 0;
     if (t >= T) s += item_blocks(g, ctx, n, T - 1);
     return s + (long long)kItemCost * (t < T ? t : T);
@@ -124,17 +123,15 @@ struct RowsPiece {
 // the sequences before s (wstart[nseq] = total).
 struct RowsWalk {
     long long x, end, base;
-    int s, g, t, T, nb;
+    int s, g, t, nb;
 
-    SLM_HD void open(const SeqRows *seq, const RowsGeom &G) {
-        T = item_count(G, seq[s].n);
-        nb = item_blocks(G, seq[s].ctx, seq[s].n, t);
-    }
+    SLM_HD void open(const SeqRows *seq, const RowsGeom &G) { nb = item_blocks(G, seq[s].ctx, seq[s].n, t); }
 
     // On to the item after this one; false behind the last.
     SLM_HD bool advance(const SeqRows *seq, int nseq, const RowsGeom &G) {
         base += kItemCost + nb;
-        if (++t == T) {
+        t++;
+        if ((long long)t * G.PT >= seq[s].n) {
             t = 0;
             if (++g == G.KV) {
                 g = 0;

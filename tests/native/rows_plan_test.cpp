@@ -36,7 +36,7 @@ static void test_sums() {
         CHECK(floor_sum(n, m, a, b) == want, "floor_sum(%u, %u, %u, %u)", n, m, a, b);
     }
     for (int i = 0; i < 500; i++) {
-        const RowsGeom g{pick(1, 4), pick(1, 128), 64 << pick(0, 1), 1};
+        const RowsGeom g{pick(1, 4), pick(1, 128), pick(6, 7), 1};
         const int n = pick(1, 3000), ctx = pick(0, 5000);
         long long sum = 0;
         for (int t = 0; t <= item_count(g, n); t++) {
@@ -44,8 +44,14 @@ static void test_sums() {
             if (t < item_count(g, n)) sum += item_blocks(g, ctx, n, t) + kItemCost;
         }
     }
+    for (int i = 0; i < 500; i++) {
+        const RowsGeom g{1, pick(1, 128), pick(6, 7), 1};
+        const int n = pick(1, 3000), ctx = pick(0, 5000), t = pick(0, item_count(g, n) - 1);
+        const int last = (t + 1) * g.PT < n ? (t + 1) * g.PT : n;
+        CHECK(item_blocks(g, ctx, n, t) == (ctx + last + (1 << g.shift) - 1) / (1 << g.shift), "item_blocks");
+    }
     // a sequence of two billion positions: no overflow
-    const RowsGeom g{1, 1, 64, 1};
+    const RowsGeom g{1, 1, 6, 1};
     CHECK(head_units(g, 2000000000, 1000, 1000) > 1000LL * (2000000000LL / 64), "long context");
 }
 
@@ -67,7 +73,7 @@ static void test_lengths() {
 
 static void test_walk(int nseq, int maxn, int maxctx) {
     const int G = pick(1, 8), tile = pick(0, 1) ? 256 : pick(0, 1) ? 64 : 16;
-    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, 64 << pick(0, 1), pick(0, 2) > 0};
+    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, pick(6, 7), pick(0, 2) > 0};
     const int P = pick(0, 3) ? pick(1, 400) : pick(1, 5);
     std::vector<SeqRows> seq(nseq);
     std::vector<long long> wstart(nseq + 1, 0);
