@@ -368,7 +368,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         uint32_t sp = 0, op = 0, xp = 0;  // phases of s_full; of both o_full (bit i); of x_full, x_free
         bool lent = false;                // group 1: group 0 may still read O and xm, xl of a twin item
         bool joined = false;
-        while (w.next(seq, A.nseq, A.geom, p)) {
+        RowsPiece ahead;  // the next piece, found while the tensor core finishes this one
+        bool more = w.next(seq, A.nseq, A.geom, ahead);
+        while (more) {
+            p = ahead;
             const SeqRows sr = seq[p.s];
             const TileView v = tile_view<kTwin>(sr, p, TT, PT, i);
             const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
@@ -454,6 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(&B->p_ready[i]);
             }
             if (!ok) break;
+            more = w.next(seq, A.nseq, A.geom, ahead);
             // twin: group 1 hands its statistics over, group 0 adds both halves up
             const bool both = v.twin && p.kb1 - p.kb0 > 1;
             float f0 = 1.0f, f1 = 0.0f;
@@ -613,7 +617,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             if (elect_one()) tc_commit(&B->kv_empty[ks]);
             forward(ks, kph);
         };
-        while (ok && w.next(seq, A.nseq, A.geom, p)) {
+        RowsPiece ahead;  // the next piece, found while the softmax of this one's first block runs
+        bool another = w.next(seq, A.nseq, A.geom, ahead);
+        while (ok && another) {
+            p = ahead;
             const SeqRows sr = seq[p.s];
             const int n = p.kb1 - p.kb0;
             const int L = sr.ctx + min(p.t * PT + PT, sr.n);  // positions the item sees
@@ -635,6 +642,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = tc_wait(&B->q_full[0], qph & 1, A.status, stop))) break;
                 qph ^= 1;
                 if (!(ok = score(0)) || (n > 1 && !(ok = score(1)))) break;
+                another = w.next(seq, A.nseq, A.geom, ahead);
                 for (int b = 0; b < n; b++) {
                     if (!(ok = take_v(b == n - 1 ? tail : kTcBlk)) || !(ok = weigh(b & 1, b < 2, b + 2 >= n))) break;
                     drop_v();
@@ -658,6 +666,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             }
             if (!ok) break;
             drop_k();
+            another = w.next(seq, A.nseq, A.geom, ahead);
             for (int j = 0; j < n; j++) {
                 if (!(ok = take_v(j == n - 1 ? tail : kTcBlk))) break;
                 const bool more = j + 1 < n;
