@@ -373,42 +373,45 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
         return (T *)A.out + (size_t)(J.row0 + tok) * A.out_ld + (size_t)(J.head0 + r - tok * A.G) * A.hd;
     };
     if (n < kJoinShared) {
-        // row r, quads q, q + qs, ...: the maximum first, then every piece's share
-        auto row = [&](int r, int q0, int qs, float4 (&acc)[Q]) {
+        // quads q, q + 8, ... of row r: the maximum first, then every piece's share
+        auto row = [&](int r, int q0, auto &acc) {
+            constexpr int N = sizeof(acc) / sizeof(float4);
             float M = -INFINITY, l = 0.f;
 #pragma unroll 4
             for (int i = 0; i < n; i++) M = fmaxf(M, stats[slot(i) + r]);
 #pragma unroll
-            for (int k = 0; k < Q; k++) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+            for (int k = 0; k < N; k++) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(N == 1 ? 4 : 2)
             for (int i = 0; i < n; i++) {
                 const float *s = slots + slot(i), mi = s[(size_t)R * A.hd + r], li = s[(size_t)R * (A.hd + 1) + r];
+                float4 v[N];
+#pragma unroll
+                for (int k = 0; k < N; k++)
+                    if (q0 + 8 * k < cols) v[k] = *(const float4 *)(s + ((size_t)(q0 + 8 * k) * R + r) * 4);
                 if (mi == -INFINITY) continue;  // the row saw nothing of this piece: its O may not have been written
                 const float f = exp2f(mi - M);
                 l = fmaf(f, li, l);
 #pragma unroll
-                for (int k = 0; k < Q; k++)
-                    if (q0 + k * qs < cols) add4(acc[k], f, *(const float4 *)(s + ((size_t)(q0 + k * qs) * R + r) * 4));
+                for (int k = 0; k < N; k++)
+                    if (q0 + 8 * k < cols) add4(acc[k], f, v[k]);
             }
             const float inv = 1.0f / l;
 #pragma unroll
-            for (int k = 0; k < Q; k++) acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+            for (int k = 0; k < N; k++) acc[k] = make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
         };
-        float4 acc[Q];
-        if (nr < 32) {  // a decode step: Q quads a thread, the rows side by side
-            const int qs = (cols + Q - 1) / Q;
-            for (int e = blockIdx.y * 256 + threadIdx.x; e < nr * qs; e += gridDim.y * 256) {
+        if (nr < 32) {  // a decode step: a quad a thread, the rows side by side
+            for (int e = blockIdx.y * 256 + threadIdx.x; e < nr * cols; e += gridDim.y * 256) {
                 const int q = e / nr, r = e - q * nr;
-                row(r, q, qs, acc);
-#pragma unroll
-                for (int k = 0; k < Q; k++)
-                    if (q + k * qs < cols) store4<T>(dest(r) + 4 * (q + k * qs), acc[k]);
+                float4 one[1];
+                row(r, q, one);
+                store4<T>(dest(r) + 4 * q, one[0]);
             }
             return;
         }
+        float4 acc[Q];
         const int pitch = A.hd * (int)sizeof(T) + 16, chunks = A.hd * (int)sizeof(T) / 16;
         for (int r0 = blockIdx.y * 32; r0 < nr; r0 += gridDim.y * 32) {
-            row(min(r0 + lane, nr - 1), warp, 8, acc);
+            row(min(r0 + lane, nr - 1), warp, acc);
 #pragma unroll
             for (int k = 0; k < Q; k++)
                 if (warp + 8 * k < cols) store4<T>((T *)(buf + lane * pitch) + 4 * (warp + 8 * k), acc[k]);
