@@ -328,6 +328,196 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
     if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
 }
 
+// ---- 64-row tiles (fp32 heads of up to 128): the same walk with every row inside one warp
+//
+// A warp owns 8 rows: thread (ty, tx) has rows 4 ty + i and keys tx + 16 j of S and columns 4 tx of
+// O, so the softmax of a row stays within 16 lanes (its maximum by shuffles, its sum as 16 partial
+// sums until the end) and the weights go through the warp's own piece of shared memory.  One block
+// barrier per 64 positions is left, for the key / value buffers, so a warp's softmax runs beside the
+// other warps' multiplications.
+template <int HDP>
+__global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kernel(const __grid_constant__ RowsArgs A) {
+    constexpr int R = 64, LD = simt_ld<HDP>(), PLD = kSimtBlk + 4, C = HDP / 64;
+    extern __shared__ __align__(16) uint8_t smem[];
+    long long *wstart = (long long *)smem;
+    SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
+    float *qs = (float *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
+    float *kv = qs + R * LD, *ps = kv + 4 * kSimtBlk * LD;  // [2 buffers][keys, values][64][LD]
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const float *Q = (const float *)A.q, *K = (const float *)A.kv.k, *V = (const float *)A.kv.v;
+
+    pdl_wait();
+    pdl_trigger();
+    rows_layout(A, seq, wstart, tid, kSimtThreads);
+    const long long unit = range_units(wstart[A.nseq], A.P);
+    RowsWalk w;
+    w.begin(seq, wstart, A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1));
+    RowsPiece p;
+    bool joined = false;
+    while (w.next(seq, A.nseq, A.geom, p)) {
+        const SeqRows sr = seq[p.s];
+        const int tok0 = p.t * A.geom.PT, ntok = min(A.geom.PT, sr.n - tok0), nr = ntok * A.G;
+        const int L = sr.ctx + tok0 + ntok;  // positions the item sees
+        __syncthreads();                     // the last piece is done with every buffer
+        // keys and values of block kb into buffer b; rows that no row of the item sees are zero
+        auto load = [&](int kb, int b) {
+            float *ks = kv + (size_t)b * 2 * kSimtBlk * LD, *vs = ks + kSimtBlk * LD;
+            const int k0 = kb * kSimtBlk;
+#pragma unroll 4
+            for (int e = tid; e < kSimtBlk * (HDP / 4); e += kSimtThreads) {
+                const int j = e / (HDP / 4), d = (e - j * (HDP / 4)) * 4;
+                float *kd = ks + j * LD + d, *vd = vs + j * LD + d;
+                if (k0 + j < L && d < A.hd) {
+                    cp_async16(kd, K + rows_kv_offset(A, false, p.s, sr.row0, p.g, k0 + j) + d);
+                    cp_async16(vd, V + rows_kv_offset(A, true, p.s, sr.row0, p.g, k0 + j) + d);
+                } else {
+                    *(float4 *)kd = *(float4 *)vd = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            cp_async_commit();
+        };
+        load(p.kb0, 0);
+        // queries, times log2(e) / sqrt(hd)
+        for (int e = tid; e < R * (HDP / 4); e += kSimtThreads) {
+            const int r = e / (HDP / 4), d = (e - r * (HDP / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < nr && d < A.hd) {
+                const int tok = r / A.G, h = p.g * A.G + (r - tok * A.G);
+                x = *(const float4 *)(Q + (size_t)(sr.row0 + tok0 + tok) * A.q_ld + (size_t)h * A.hd + d);
+            }
+            *(float4 *)(qs + r * LD + d) = make_float4(x.x * A.scale_log2, x.y * A.scale_log2, x.z * A.scale_log2, x.w * A.scale_log2);
+        }
+        float4 o[4][C];
+        float m[4], l[4];
+        int seen[4];  // positions that the rows see
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            seen[i] = sr.ctx + tok0 + (4 * ty + i) / A.G + 1;
+#pragma unroll
+            for (int c = 0; c < C; c++) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const bool some = 8 * (ty >> 1) < nr;  // the warp has rows (else it only loads and keeps step)
+
+        for (int kb = p.kb0; kb < p.kb1; kb++) {
+            const int k0 = kb * kSimtBlk, buf = (kb - p.kb0) & 1;
+            const float *ks = kv + (size_t)buf * 2 * kSimtBlk * LD, *vs = ks + kSimtBlk * LD;
+            cp_async_wait_upto(0);
+            __syncthreads();  // block kb has landed, and everyone is done with block kb - 1
+            if (kb + 1 < p.kb1) load(kb + 1, buf ^ 1);
+            if (!some) continue;
+            float s[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) s[i][j] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < HDP; d += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) a[i] = *(const float4 *)(qs + (4 * ty + i) * LD + d);
+#pragma unroll
+                for (int j = 0; j < 4; j++) b[j] = *(const float4 *)(ks + (tx + 16 * j) * LD + d);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    }
+            }
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int lim = seen[i] - k0;  // keys of the block that the row sees
+                float mx = m[i];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    if (tx + 16 * j >= lim) s[i][j] = -INFINITY;
+                    mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int off = 8; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float m0 = mx == -INFINITY ? 0.f : mx;  // nothing seen yet: every weight is 2^-inf = 0
+                f[i] = exp2f(m[i] - m0);
+                m[i] = mx;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float x = exp2f(s[i][j] - m0);
+                    sum += x;
+                    ps[(4 * ty + i) * PLD + tx + 16 * j] = x;
+                }
+                l[i] = l[i] * f[i] + sum;
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    o[i][c].x *= f[i];
+                    o[i][c].y *= f[i];
+                    o[i][c].z *= f[i];
+                    o[i][c].w *= f[i];
+                }
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int j = 0; j < kSimtBlk; j += 4) {
+                float4 pv[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) pv[i] = *(const float4 *)(ps + (4 * ty + i) * PLD + j);
+#pragma unroll
+                for (int jj = 0; jj < 4; jj++)
+#pragma unroll
+                    for (int c = 0; c < C; c++) {
+                        const float4 v = *(const float4 *)(vs + (j + jj) * LD + 4 * tx + 64 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float a = jj == 0 ? pv[i].x : jj == 1 ? pv[i].y : jj == 2 ? pv[i].z : pv[i].w;
+                            o[i][c].x = fmaf(a, v.x, o[i][c].x);
+                            o[i][c].y = fmaf(a, v.y, o[i][c].y);
+                            o[i][c].z = fmaf(a, v.z, o[i][c].z);
+                            o[i][c].w = fmaf(a, v.w, o[i][c].w);
+                        }
+                    }
+            }
+            __syncwarp();  // the weights have been read
+        }
+        const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
+        if (!whole && p.kb0 == 0) {
+            joined = true;
+            if (tid == 0) write_join(A, blockIdx.x, seq, unit, &p);
+        }
+        float *part = slot_ptr(A, piece_slot(blockIdx.x, p));
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+#pragma unroll
+            for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+            const int r = 4 * ty + i;
+            if (r >= nr) continue;
+            if (whole) {
+                const int tok = r / A.G, h = p.g * A.G + (r - tok * A.G);
+                const float inv = 1.0f / l[i];
+                float *dst = (float *)A.out + (size_t)(sr.row0 + tok0 + tok) * A.out_ld + (size_t)h * A.hd;
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    if (4 * tx + 64 * c < A.hd)
+                        *(float4 *)(dst + 4 * tx + 64 * c) =
+                            make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv);
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    if (4 * tx + 64 * c < A.hd) *(float4 *)(part + ((size_t)(tx + 16 * c) * A.slot_rows + r) * 4) = o[i][c];
+                if (tx == 0) {
+                    part[(size_t)A.slot_rows * A.hd + r] = m[i];
+                    part[(size_t)A.slot_rows * (A.hd + 1) + r] = l[i];
+                }
+            }
+        }
+    }
+    if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
+}
+
 // ---- joining
 //
 // Piece i of an item has, per row, the maximum m_i, the sum l_i and the unnormalised O_i:
@@ -500,6 +690,13 @@ int rows_simt_ctas(int sms, int hd, int R, int nseq) {
     return sms * (2 * (simt_bytes(hd, R, nseq) + 1024) <= 228 * 1024 ? 2 : 1);
 }
 
+template <int HDP> static cudaError_t launch_fma(const RowsArgs &a, cudaStream_t s) {
+    const size_t smem = simt_smem<float, HDP, 64>(a.nseq);
+    cudaError_t e = cudaFuncSetAttribute(rows_fma_kernel<HDP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rows_fma_kernel<HDP>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
+}
+
 template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsArgs &a, cudaStream_t s) {
     const size_t smem = simt_smem<T, HDP, R>(a.nseq);
     cudaError_t e = cudaFuncSetAttribute(rows_simt_kernel<T, HDP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -510,8 +707,8 @@ template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsA
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
     const bool small = a.geom.PT * a.G <= 16;
     if (bf16) return small ? launch_simt<__nv_bfloat16, 256, 16>(a, s) : launch_simt<__nv_bfloat16, 256, 32>(a, s);
-    if (a.hd <= 64) return small ? launch_simt<float, 64, 16>(a, s) : launch_simt<float, 64, 64>(a, s);
-    if (a.hd <= 128) return small ? launch_simt<float, 128, 16>(a, s) : launch_simt<float, 128, 64>(a, s);
+    if (a.hd <= 64) return small ? launch_simt<float, 64, 16>(a, s) : launch_fma<64>(a, s);
+    if (a.hd <= 128) return small ? launch_simt<float, 128, 16>(a, s) : launch_fma<128>(a, s);
     return small ? launch_simt<float, 256, 16>(a, s) : launch_simt<float, 256, 32>(a, s);
 }
 
