@@ -368,8 +368,9 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
                 const int j = e / (HDP / 4), d = (e - j * (HDP / 4)) * 4;
                 float *kd = ks + j * LD + d, *vd = vs + j * LD + d;
                 if (k0 + j < L && d < A.hd) {
-                    cp_async16(kd, K + rows_kv_offset(A, false, p.s, sr.row0, p.g, k0 + j) + d);
-                    cp_async16(vd, V + rows_kv_offset(A, true, p.s, sr.row0, p.g, k0 + j) + d);
+                    const size_t at = rows_kv_offset(A, false, p.s, sr.row0, p.g, k0 + j) + d;
+                    cp_async16(kd, K + at);
+                    cp_async16(vd, V + (A.kv.table ? at : rows_kv_offset(A, true, p.s, sr.row0, p.g, k0 + j) + d));
                 } else {
                     *(float4 *)kd = *(float4 *)vd = make_float4(0.f, 0.f, 0.f, 0.f);
                 }

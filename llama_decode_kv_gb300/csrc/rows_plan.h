@@ -13,6 +13,7 @@
 // range whole, and nothing has to be joined.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #ifdef __CUDACC__
@@ -163,16 +164,26 @@ struct RowsWalk {
         unsigned long long rem = x - wstart[s];
         g = (int)udiv(rem, per);
         rem -= (unsigned long long)g * per;
-        int a = 0, b = item_count(G, seq[s].n) - 1;  // the last t with head_units(t) <= rem
-        while (a < b) {
-            const int mid = (a + b + 1) >> 1;
-            if ((unsigned long long)head_units(G, seq[s].ctx, seq[s].n, mid) <= rem)
-                a = mid;
-            else
-                b = mid - 1;
+        // The last item with head_units(t) <= rem.  About t^2 PT / (2 BLK) + t b units stand before item
+        // t, b being the first item's; from that guess it is a step or two.
+        const int ctx = seq[s].ctx, n = seq[s].n, T = item_count(G, n);
+        unsigned long long at = 0;  // head_units(t)
+        t = 0;
+        if (T > 1) {
+            const float blk = (float)(1 << G.shift), qa = 0.5f * (float)G.PT / blk;
+            const float qb = kItemCost + 0.5f + ((float)ctx + 0.5f * (float)G.PT) / blk;
+            const float guess = 2.0f * (float)rem / (qb + sqrtf(qb * qb + 4.0f * qa * (float)rem));
+            t = guess < (float)(T - 1) ? (int)guess : T - 1;
+            at = (unsigned long long)head_units(G, ctx, n, t);
+            while (at > rem) at -= kItemCost + item_blocks(G, ctx, n, --t);
+            while (t < T - 1) {
+                const unsigned long long after = at + kItemCost + item_blocks(G, ctx, n, t);
+                if (after > rem) break;
+                at = after;
+                t++;
+            }
         }
-        t = a;
-        base = wstart[s] + (long long)(g * per) + head_units(G, seq[s].ctx, seq[s].n, t);
+        base = wstart[s] + (long long)(g * per + at);
         open(seq, G);
         if (!G.split && base < x) {  // the item belongs to the range that it begins in
             if (!advance(seq, nseq, G)) end = x;

@@ -139,6 +139,7 @@ int main() {
     for (int i = 0; i < 100; i++) test_walk(pick(1, 64), 1, 4000);
     for (int i = 0; i < 100; i++) test_walk(pick(1, 3), 2, 100);
     for (int i = 0; i < 20; i++) test_walk(1, 1, 200000);
+    for (int i = 0; i < 20; i++) test_walk(pick(1, 3), 20000, i % 2 ? 0 : 300000);
     test_walk(1024, 3, 50);
     if (fails) return 1;
     std::printf("ok\n");
