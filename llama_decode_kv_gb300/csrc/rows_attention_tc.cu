@@ -59,8 +59,7 @@ struct RowsTcArgs {
 struct TcBars {
     uint64_t kv_full[16], kv_empty[16];
     uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
-    uint64_t x_full, x_free;       // twin items: group 1's statistics stand in xm, xl; group 0 is done
-    float xm[128], xl[128];
+    uint64_t x_full, x_free;  // twin items: group 1's statistics stand in shared memory; group 0 is done
     uint32_t tmem;
     int stop;
 };
@@ -295,7 +294,7 @@ __device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece
 }
 
 __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages) {
-    return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16;
+    return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16 + (HDP == 64 ? 1024 : 0);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -316,7 +315,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     uint8_t *sq = base;                             // [2 tiles][NP][128][64]
     uint8_t *ring = base + 2 * NP * kPanel;         // [stages][NP][128][64]
     TcBars *B = (TcBars *)(ring + (size_t)T.stages * NP * kPanel);
-    long long *wstart = (long long *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);
+    float *xm = (float *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);  // [128] maxima, [128] sums
+    long long *wstart = (long long *)(xm + (kTwin ? 256 : 0));
     SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
     volatile int *stop = &B->stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -462,8 +462,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             const bool both = v.twin && p.kb1 - p.kb0 > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (both && i == 1) {
-                B->xm[r] = m;
-                B->xl[r] = l;
+                xm[r] = m;
+                xm[128 + r] = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->x_full);
                 lent = true;
@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!tc_wait(&B->o_full[1], op0 >> 1 & 1, A.status, stop)) break;
                 if (!tc_wait(&B->x_full, xp, A.status, stop)) break;
                 xp ^= 1;
-                const float m1 = B->xm[r], M = fmaxf(m, m1);
+                const float m1 = xm[r], M = fmaxf(m, m1);
                 f0 = m == -INFINITY ? 0.f : fast_exp2((m - M) * c);
                 f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - M) * c);
-                l = l * f0 + B->xl[r] * f1;
+                l = l * f0 + xm[128 + r] * f1;
                 m = M;
             }
             if (!busy || (v.twin && i == 1)) {

@@ -533,6 +533,47 @@ def test_two_streams_at_once(slm, dtype):
             assert torch.equal(o, a)
 
 
+@pytest.mark.parametrize("dtype,H,KV,hd", [(BF16, 6, 2, 64), (BF16, 8, 2, 128), (BF16, 4, 4, 64), (F32, 6, 2, 64)])
+def test_ragged_batch(slm, dtype, H, KV, hd):
+    """Decode steps, chunks of one and of several tiles and idle slots, of all lengths, in one
+    call: items of every kind follow one another in a CTA."""
+    S = 41
+    new = [(1, 1, 70, 0, 1, 13, 150, 33)[i % 8] for i in range(S)]
+    ctx = [(i * 211) % 1500 for i in range(S)]
+    b = Batch(dtype, H, KV, hd, new, ctx, 32, None, 1, 2, seed=70 + hd)
+    b.fill([n + c for n, c in zip(b.new, b.ctx)])
+    out, ws = b.out(), b.workspace(slm)
+    slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, ws, b.status)
+    check_attention(b, out, b.seq_k, b.seq_v, dtype)
+    again = b.out()
+    slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, again, ws, b.status)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("hd,gap", [(64, 8), (64, 16), (80, 8), (16, 16)])
+def test_outputs_into_a_wider_buffer(slm, dtype, hd, gap):
+    """Outputs as a column range of a wider buffer (row strides of 16 mod 32 bytes among them):
+    the columns beside it stay as they were."""
+    b = Batch(dtype, 6, 2, hd, [150, 1, 40], None, 16, None, 0, 3, seed=hd + gap)
+    wide = torch.full((b.rows, 6 * hd + gap), 7.0, dtype=dtype, device="cuda")
+    out = wide[:, gap:].unflatten(1, (6, hd))
+    slm.attention_prompt(b.q, b.k, b.v, b.row_start, out, b.workspace(slm), b.status)
+    parts = [slice(b.starts[s], b.starts[s] + n) for s, n in enumerate(b.new)]
+    check_attention(b, out, [b.k[p] for p in parts], [b.v[p] for p in parts], dtype)
+    assert bool((wide[:, :gap] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_long_context_over_the_whole_gpu(slm, dtype):
+    """One kv head, one token, a context that every CTA gets a piece of: the join of many pieces."""
+    b = Batch(dtype, 5, 1, 64, [1], [40001], 64, seed=80)
+    b.fill([40002])
+    out = b.out()
+    slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, b.workspace(slm), b.status)
+    check_attention(b, out, b.seq_k, b.seq_v, dtype)
+
+
 def test_no_rows(slm):
     b = Batch(BF16, 4, 2, 64, [0, 0], [5, 0], 16, seed=1, pad=2)
     b.fill([5, 0])
