@@ -566,25 +566,36 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
     if (n < kJoinShared) {
         // quads q, q + 8, ... of row r: the maximum first, then every piece's share
         auto row = [&](int r, int q0, auto &acc) {
-            constexpr int N = sizeof(acc) / sizeof(float4);
+            constexpr int N = sizeof(acc) / sizeof(float4), AT = N == 1 ? 4 : 2;  // pieces in flight
             float M = -INFINITY, l = 0.f;
-#pragma unroll 4
-            for (int i = 0; i < n; i++) M = fmaxf(M, stats[slot(i) + r]);
+            for (int i0 = 0; i0 < n; i0 += 4) {
+                float mi[4];
+#pragma unroll
+                for (int a = 0; a < 4; a++) mi[a] = i0 + a < n ? stats[slot(i0 + a) + r] : -INFINITY;
+                M = fmaxf(M, fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])));
+            }
 #pragma unroll
             for (int k = 0; k < N; k++) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll(N == 1 ? 4 : 2)
-            for (int i = 0; i < n; i++) {
-                const float *s = slots + slot(i), mi = s[(size_t)R * A.hd + r], li = s[(size_t)R * (A.hd + 1) + r];
-                float4 v[N];
+            for (int i0 = 0; i0 < n; i0 += AT) {
+                float mi[AT], li[AT];
+                float4 v[AT][N];
 #pragma unroll
-                for (int k = 0; k < N; k++)
-                    if (q0 + 8 * k < cols) v[k] = *(const float4 *)(s + ((size_t)(q0 + 8 * k) * R + r) * 4);
-                if (mi == -INFINITY) continue;  // the row saw nothing of this piece: its O may not have been written
-                const float f = exp2f(mi - M);
-                l = fmaf(f, li, l);
+                for (int a = 0; a < AT; a++) {
+                    const float *s = slots + slot(min(i0 + a, n - 1));
+                    mi[a] = i0 + a < n ? s[(size_t)R * A.hd + r] : -INFINITY;
+                    li[a] = s[(size_t)R * (A.hd + 1) + r];
 #pragma unroll
-                for (int k = 0; k < N; k++)
-                    if (q0 + 8 * k < cols) add4(acc[k], f, v[k]);
+                    for (int k = 0; k < N; k++)
+                        v[a][k] = *(const float4 *)(s + ((size_t)min(q0 + 8 * k, cols - 1) * R + r) * 4);
+                }
+#pragma unroll
+                for (int a = 0; a < AT; a++) {
+                    if (mi[a] == -INFINITY) continue;  // no piece, or the row saw nothing of it: O may not have been written
+                    const float f = exp2f(mi[a] - M);
+                    l = fmaf(f, li[a], l);
+#pragma unroll
+                    for (int k = 0; k < N; k++) add4(acc[k], f, v[a][k]);
+                }
             }
             const float inv = 1.0f / l;
 #pragma unroll
