@@ -25,8 +25,8 @@
  *     device", the library checks the pointer's kind itself.
  *   - `stream` is a cudaStream_t passed as void* (NULL = the legacy default stream).
  *     Work is enqueued asynchronously on it unless the call says otherwise.  Stream
- *     order holds as usual: the prefill's kernels are launched with programmatic
- *     dependent launch among themselves, and each waits for the work before it on the
+ *     order holds as usual: the kernels of the prefill and of the packed-row calls are
+ *     launched with programmatic dependent launch, and each waits for the work before it on the
  *     stream to complete before it reads or writes any memory.
  *   - A context is not thread-safe: calls on one context must not overlap.
  *   - Every device-side wait in the library's kernels is bounded in time; a wait that
@@ -258,7 +258,7 @@ void slm_destroy(slm_ctx *ctx);
 
 /* slm_last_error -- text of the context's last failure ("" if none).  With ctx = NULL:
  * the last failure, on the calling thread, of a call that has no context
- * (slm_create, slm_attention_decode). */
+ * (slm_create, slm_attention_decode, slm_kv_append, ...). */
 const char *slm_last_error(const slm_ctx *ctx);
 
 /* slm_status_string -- static text for a status code. */
@@ -431,7 +431,7 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
  *                     for that sequence.
  * No call reads or writes outside its buffers because of a length or a page id.
  *
- * Requirements of all three: nseq in [1, 1024]; n_heads % n_kv_heads == 0; head_dim a multiple
+ * Requirements of all three: nseq in [1, 1024]; rows at most 2^30; n_heads % n_kv_heads == 0; head_dim a multiple
  * of 8 in [8, 256]; q, k, v, out and the cache 16-byte aligned; row strides (*_ld, in elements,
  * from one packed row to the next) of at least heads * head_dim and a multiple of 16 bytes, so
  * q, k and v may be column ranges of one projection's output; heads of a row are adjacent.

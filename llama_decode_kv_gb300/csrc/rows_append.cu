@@ -16,6 +16,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "rows.cuh"
 
@@ -73,11 +75,7 @@ __device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int
     s = (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
     if (lane || s >= A.nseq) return o;  // s = nseq: behind the last sequence
     const int first = __ldg(A.row_start + s);
-    if (r < first) {
-        // before the first sequence, or row_start is not ascending
-        if (s > 0) atomicOr(A.status, SLM_ROWS_LENGTH);
-        return o;
-    }
+    if (r < first || r >= __ldg(A.row_start + s + 1)) return o;  // before the first sequence, or not ascending
     const int ctx = A.ctx_len ? __ldg(A.ctx_len + s) : 0;
     const long long pos = (long long)ctx + ((long long)r - first);
     if (ctx < 0 || pos >= A.cap || (A.rope && pos >= A.rope_len)) {
@@ -101,6 +99,14 @@ __global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __gri
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = blockIdx.x * rpc, nr = min(rpc, A.rows - r0);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == kAppendThreads / 32 - 1) {
+        bool bad = false;
+        for (int i = lane; i < A.nseq; i += 32) {
+            const int a = __ldg(A.row_start + i), b = __ldg(A.row_start + i + 1);
+            bad |= a < 0 || b < a || b > A.rows;
+        }
+        if (bad) atomicOr(A.status, SLM_ROWS_LENGTH);
+    }
     if (warp < nr) {
         const AppendRow a = resolve_row(A, r0 + warp, lane);
         if (lane == 0) rows[warp] = a;
@@ -151,7 +157,7 @@ static cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     // One row per CTA, its units spread over grid.y, while the rows alone do not fill the GPU;
     // then four rows per CTA, so that a CTA's chain of lookups is paid once for four rows.
     const int rpc = a.rows >= 2048 ? 4 : 1;
-    const int gy = rpc > 1 ? 1 : (units + kAppendThreads - 1) / kAppendThreads;
+    const int gy = rpc > 1 ? 1 : std::min((units + kAppendThreads - 1) / kAppendThreads, 65535);
     const dim3 grid((a.rows + rpc - 1) / rpc, gy);
     return launch_pdl(vec == 8 ? rows_append_kernel<TI, TC, 8> : rows_append_kernel<TI, TC, 4>, grid, dim3(kAppendThreads), 0, s,
                       a, rpc);

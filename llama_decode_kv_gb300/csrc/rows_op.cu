@@ -66,7 +66,7 @@ static int check_heads(int H, int KV, int hd) {
 static int check_rows(const slm_rows *r) {
     if (!r) return attn_fail(SLM_EINVAL, "rows is NULL");
     if (r->nseq < 1 || r->nseq > kRowsMaxSeqs) return attn_fail(SLM_EINVAL, "nseq %d outside [1, %d]", r->nseq, kRowsMaxSeqs);
-    if (r->rows < 0) return attn_fail(SLM_EINVAL, "rows %d < 0", r->rows);
+    if (r->rows < 0 || r->rows > (1 << 30)) return attn_fail(SLM_EINVAL, "rows %d outside [0, 2^30]", r->rows);
     if (!r->row_start) return attn_fail(SLM_EINVAL, "row_start is NULL");
     if ((uintptr_t)r->row_start % 4 || (uintptr_t)r->ctx_len % 4) return attn_fail(SLM_EINVAL, "row_start and ctx_len must be 4-byte aligned");
     return SLM_OK;

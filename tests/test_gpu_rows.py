@@ -250,6 +250,12 @@ def test_append_skips_rows_with_bad_pages_and_positions(slm):
         slm.kv_append(b.k, b.v, b.k_cache, b.v_cache, b.page_table, b.row_start, ctx, b.status)
         assert int(b.status.item()) == slm.SLM_ROWS_LENGTH
         assert int((~torch.isnan(b.k_cache[..., 0])).sum()) == 4 + (3 if ctx0 == 29 else 0)
+    for starts in ((0, 10, 5), (0, 4, 9), (-3, 4, 8)):  # descends; past the buffer; before it
+        b.status.zero_()
+        b.k_cache.fill_(float("nan"))
+        rs = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        slm.kv_append(b.k, b.v, b.k_cache, b.v_cache, b.page_table, rs, None, b.status)
+        assert int(b.status.item()) == slm.SLM_ROWS_LENGTH
     b.status.zero_()  # past the rotation table
     slm.kv_append(b.k, b.v, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, b.status, rope[:17])
     assert int(b.status.item()) == slm.SLM_ROWS_LENGTH

@@ -59,7 +59,7 @@ CACHES = [(dict(kv_dtype=2), "kv_dtype"), (dict(n_kv_heads=0), "n_kv_heads"), (d
           (dict(page_size=24), "page_size"), (dict(page_size=1 << 21), "page_size"), (dict(page_size=-16), "page_size"),
           (dict(n_pages=0), "n_pages"), (dict(table_ld=0), "table_ld"), (dict(k=None), "non-NULL"),
           (dict(page_table=None), "non-NULL"), (dict(v=A + 8), "aligned"), (dict(page_table=A + 2), "aligned")]
-ROWS = [(dict(nseq=0), "nseq"), (dict(nseq=1025), "nseq"), (dict(rows=-1), "rows"), (dict(row_start=None), "row_start"),
+ROWS = [(dict(nseq=0), "nseq"), (dict(nseq=1025), "nseq"), (dict(rows=-1), "rows"), (dict(rows=(1 << 30) + 1), "rows"), (dict(row_start=None), "row_start"),
         (dict(row_start=A + 1), "aligned")]
 
 
