@@ -161,53 +161,47 @@ def attention_decode_noalloc(q, k_cache, v_cache, ctx_len, out, kv_dtype: int, s
 
 _PACK_CACHE = struct.Struct("PPPiiiiii").pack
 _PACK_ROWS = struct.Struct("PPii").pack
-_torch_names = None
+_F32 = _BF16 = _INT = _raw_stream = None  # torch's types and the current stream of a device number
 
 
-def _torch():
-    """(float32, bfloat16, int32, current raw stream of a device), looked up once."""
-    global _torch_names
-    if _torch_names is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda d: torch.cuda.current_stream(d).cuda_stream)
-        _torch_names = (torch.float32, torch.bfloat16, torch.int32, raw)
-    return _torch_names
+def _torch_names():
+    """Look the names up (torch is not imported before it is needed)."""
+    global _F32, _BF16, _INT, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _F32, _BF16, _INT = torch.float32, torch.bfloat16, torch.int32
 
 
 def _dtype_code(t) -> int:
     """SLM_F32 / SLM_BF16 of a torch dtype."""
-    f32, bf16, _, _ = _torch()
-    if t is bf16:
+    if _INT is None:
+        _torch_names()
+    if t is _BF16:
         return SLM_BF16
-    if t is f32:
+    if t is _F32:
         return SLM_F32
     raise ValueError(f"{t}: the packed-row calls take float32 and bfloat16")
 
 
 def _heads(x, name: str, shape, dtype):
     """Row stride (elements) of a [rows][heads][head_dim] tensor whose heads are adjacent."""
-    rows, heads, hd = shape
     if x.dtype is not dtype or x.shape != shape:
         raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected {tuple(shape)} {dtype}")
+    rows, heads, hd = shape
     ld, h, d = x.stride()
-    if rows and ((d != 1 and hd > 1) or (h != hd and heads > 1)):
+    if (h != hd and heads > 1 or d != 1 and hd > 1) and rows:
         raise ValueError(f"{name}: the heads of a row must be adjacent (strides {x.stride()})")
     return ld if rows > 1 else heads * hd
 
 
 def _ints(x, name: str, *shape):
-    if x.dtype is not _torch()[2] or x.shape != shape or not x.is_contiguous():
+    if x.dtype is not _INT or x.shape != shape or not x.is_contiguous():
         raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected contiguous int32 {shape}")
     return x.data_ptr()
 
 
-def _packed(row_start, ctx_len, nseq: int, rows: int) -> bytes:
-    return _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
-                      0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
-
-
-def _cache(k_cache, v_cache, page_table, nseq: int, kv: int, hd: int, what: str) -> bytes:
+def _cache(k_cache, v_cache, page_table, kv: int, hd: int, what: str) -> bytes:
     """The slm_kv_cache of a cache of kv heads (0: any number) of hd."""
     shape, dt = k_cache.shape, k_cache.dtype
     if shape != v_cache.shape or dt is not v_cache.dtype or len(shape) != 4:
@@ -217,18 +211,14 @@ def _cache(k_cache, v_cache, page_table, nseq: int, kv: int, hd: int, what: str)
     pages, heads, page, chd = shape
     if chd != hd or (kv and heads != kv):
         raise ValueError(f"the cache has {heads} kv heads of {chd}, {what} {kv or 'heads'} of {hd}")
-    ld = page_table.shape[-1]
+    nseq, ld = page_table.shape
     return _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), _ints(page_table, "page_table", nseq, ld), pages, page,
                        ld, heads, chd, _dtype_code(dt))
 
 
 def _rows_stream(stream, x):
-    return _torch()[3](x.device.index or 0) if stream is None and x.is_cuda else _stream_ptr(stream)
-
-
-def _rows_check(rc: int, what: str):
-    if rc != 0:
-        raise SlmError(rc, what, slm_last_error(None).decode())
+    dev = x.get_device()
+    return _raw_stream(dev) if stream is None and dev >= 0 else _stream_ptr(stream)
 
 
 def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, rope=None, q=None, q_out=None,
@@ -239,16 +229,17 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
     when given; q [rows][heads][head_dim] is rotated into q_out (the cache's type).  Row strides
     are free.  status: int32[1] collecting SLM_ROWS_* bits.  Raises SlmError / ValueError."""
     shape, dt = k.shape, k.dtype
+    code = _dtype_code(dt)
     rows, kv, hd = shape
     nseq = page_table.shape[0]
-    code = _dtype_code(dt)
-    c = _cache(k_cache, v_cache, page_table, nseq, kv, hd, "k")
-    r = _packed(row_start, ctx_len, nseq, rows)
+    c = _cache(k_cache, v_cache, page_table, kv, hd, "k")
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
+                   0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
     k_ld, v_ld = _heads(k, "k", shape, dt), _heads(v, "v", shape, dt)
     rope_ptr, n_rope, heads, q_ptr, q_ld, o_ptr, o_ld = None, 0, 0, None, 0, None, 0
     if rope is not None:
         n_rope = rope.shape[0]
-        if rope.dtype is not _torch()[0] or rope.shape != (n_rope, hd // 2, 2) or not rope.is_contiguous():
+        if rope.dtype is not _F32 or rope.shape != (n_rope, hd // 2, 2) or not rope.is_contiguous():
             raise ValueError(f"rope: {tuple(rope.shape)} {rope.dtype}, expected contiguous float32 [n][{hd // 2}][2]")
         rope_ptr = rope.data_ptr()
     if (q is None) != (q_out is None):
@@ -260,8 +251,10 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
             raise ValueError(f"q: {tuple(qs)}, expected ({rows}, heads, {hd})")
         q_ld, o_ld = _heads(q, "q", qs, dt), _heads(q_out, "q_out", qs, k_cache.dtype)
         q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
-    _rows_check(slm_kv_append(c, r, code, k.data_ptr(), k_ld, v.data_ptr(), v_ld, rope_ptr, n_rope, heads, q_ptr, q_ld,
-                              o_ptr, o_ld, _ints(status, "status", 1), _rows_stream(stream, k)), "slm_kv_append")
+    rc = slm_kv_append(c, r, code, k.data_ptr(), k_ld, v.data_ptr(), v_ld, rope_ptr, n_rope, heads, q_ptr, q_ld, o_ptr,
+                       o_ld, _ints(status, "status", 1), _rows_stream(stream, k))
+    if rc:
+        raise SlmError(rc, "slm_kv_append", slm_last_error(None).decode())
 
 
 def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -277,12 +270,16 @@ def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, wo
     shape, dt = q.shape, k_cache.dtype
     rows, heads, hd = shape
     nseq = page_table.shape[0]
-    c = _cache(k_cache, v_cache, page_table, nseq, 0, hd, "q")
-    r = _packed(row_start, ctx_len, nseq, rows)
+    if _INT is None:
+        _torch_names()
+    c = _cache(k_cache, v_cache, page_table, 0, hd, "q")
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
+                   0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
-    _rows_check(slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, workspace.data_ptr(),
-                                    workspace.nbytes, _ints(status, "status", 1), _rows_stream(stream, q)),
-                "slm_attention_paged")
+    rc = slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, workspace.data_ptr(),
+                             workspace.nbytes, _ints(status, "status", 1), _rows_stream(stream, q))
+    if rc:
+        raise SlmError(rc, "slm_attention_paged", slm_last_error(None).decode())
 
 
 def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) -> None:
@@ -293,12 +290,15 @@ def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) ->
     rows, heads, hd = shape
     if ks[0] != rows or ks[2] != hd:
         raise ValueError(f"k: {tuple(ks)}, expected ({rows}, kv heads, {hd})")
-    r = _packed(row_start, None, row_start.shape[0] - 1, rows)
+    code, nseq = _dtype_code(dt), row_start.shape[0] - 1
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1), 0, nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
     k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
-    _rows_check(slm_attention_prompt(r, _dtype_code(dt), heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld,
-                                     v.data_ptr(), v_ld, out.data_ptr(), o_ld, workspace.data_ptr(), workspace.nbytes,
-                                     _ints(status, "status", 1), _rows_stream(stream, q)), "slm_attention_prompt")
+    rc = slm_attention_prompt(r, code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                              out.data_ptr(), o_ld, workspace.data_ptr(), workspace.nbytes, _ints(status, "status", 1),
+                              _rows_stream(stream, q))
+    if rc:
+        raise SlmError(rc, "slm_attention_prompt", slm_last_error(None).decode())
 
 
 def sample(logits, temperature: float, top_k: int, top_p: float, uniforms, next_ids, stream=None) -> int:
