@@ -90,7 +90,7 @@ __device__ __forceinline__ void write_join(const RowsArgs &A, int cta, const Seq
     RowsJoin j{};
     if (p) {
         const SeqRows r = seq[p->s];
-        j.pieces = (int)udiv(p->base + kItemCost + p->nb - 1, unit) - cta + 1;
+        j.pieces = (int)udiv(p->base + A.geom.cost + p->nb - 1, unit) - cta + 1;
         j.row0 = r.row0 + p->t * A.geom.PT;
         j.tokens = min(A.geom.PT, r.n - p->t * A.geom.PT);
         j.head0 = p->g * A.G;

@@ -4,8 +4,8 @@
 // Sequence s of a batch has n new rows (tokens) after ctx cached positions.  Its work for
 // one kv head is cut into items of up to PT tokens (all G query heads of the group
 // together); an item walks the blocks of BLK positions [0, ctx + its last token], so item t
-// has nb(t) = ceil((ctx + min((t + 1) PT, n)) / BLK) blocks and counts nb(t) + kItemCost
-// units (the unit on top stands for its queries and its epilogue).  All items of a batch,
+// has nb(t) = ceil((ctx + min((t + 1) PT, n)) / BLK) blocks and counts nb(t) + cost units
+// (the units on top stand for its queries and its epilogue).  All items of a batch,
 // in the order (sequence, kv head, item), form one line of `total` units, which is cut into
 // ranges of ceil(total / P) units, one per CTA: every CTA gets the same work whatever the
 // lengths are, and an item that a cut divides is joined afterwards from the partial states of
@@ -26,7 +26,6 @@ namespace slm {
 
 constexpr int kRowsMaxSeqs = 1024;  // sequences per call (their lengths sit in shared memory)
 constexpr int kRowsMaxGroup = 64;   // query heads per kv head
-constexpr int kItemCost = 1;
 
 // A sequence's rows after its lengths were checked: first packed row, rows, cached positions.
 struct SeqRows {
@@ -89,6 +88,7 @@ struct RowsGeom {
     int PT;      // tokens per item
     int shift;   // log2 of the positions per block (BLK)
     int split;   // 1: ranges cut through items; 0: items stay whole
+    int cost;    // units of an item besides its blocks
 };
 
 SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
@@ -106,7 +106,7 @@ SLM_HD long long head_units(const RowsGeom &g, int ctx, int n, int t) {
                                                   (unsigned)ctx + g.PT + (1u << g.shift) - 1)
                            : 0;
     if (t >= T) s += item_blocks(g, ctx, n, T - 1);
-    return s + (long long)kItemCost * (t < T ? t : T);
+    return s + (long long)g.cost * (t < T ? t : T);
 }
 
 // Units of a range.
@@ -130,7 +130,7 @@ struct RowsWalk {
 
     // On to the item after this one; false behind the last.
     SLM_HD bool advance(const SeqRows *seq, int nseq, const RowsGeom &G) {
-        base += kItemCost + nb;
+        base += G.cost + nb;
         t++;
         if ((long long)t * G.PT >= seq[s].n) {
             t = 0;
@@ -171,13 +171,13 @@ struct RowsWalk {
         t = 0;
         if (T > 1) {
             const float blk = (float)(1 << G.shift), qa = 0.5f * (float)G.PT / blk;
-            const float qb = kItemCost + 0.5f + ((float)ctx + 0.5f * (float)G.PT) / blk;
+            const float qb = G.cost + 0.5f + ((float)ctx + 0.5f * (float)G.PT) / blk;
             const float guess = 2.0f * (float)rem / (qb + sqrtf(qb * qb + 4.0f * qa * (float)rem));
             t = guess < (float)(T - 1) ? (int)guess : T - 1;
             at = (unsigned long long)head_units(G, ctx, n, t);
-            while (at > rem) at -= kItemCost + item_blocks(G, ctx, n, --t);
+            while (at > rem) at -= G.cost + item_blocks(G, ctx, n, --t);
             while (t < T - 1) {
-                const unsigned long long after = at + kItemCost + item_blocks(G, ctx, n, t);
+                const unsigned long long after = at + G.cost + item_blocks(G, ctx, n, t);
                 if (after > rem) break;
                 at = after;
                 t++;
@@ -194,7 +194,7 @@ struct RowsWalk {
     // The next piece with at least one block; false at the end of the range.
     SLM_HD bool next(const SeqRows *seq, int nseq, const RowsGeom &G, RowsPiece &p) {
         while (x < end) {
-            const long long first = base + kItemCost, stop = first + nb;
+            const long long first = base + G.cost, stop = first + nb;
             const long long hi = end < stop && G.split ? end : stop;
             p.s = s;
             p.g = g;

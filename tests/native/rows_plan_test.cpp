@@ -36,22 +36,22 @@ static void test_sums() {
         CHECK(floor_sum(n, m, a, b) == want, "floor_sum(%u, %u, %u, %u)", n, m, a, b);
     }
     for (int i = 0; i < 500; i++) {
-        const RowsGeom g{pick(1, 4), pick(1, 128), pick(6, 7), 1};
+        const RowsGeom g{pick(1, 4), pick(1, 128), pick(6, 7), 1, pick(1, 3)};
         const int n = pick(1, 3000), ctx = pick(0, 5000);
         long long sum = 0;
         for (int t = 0; t <= item_count(g, n); t++) {
             CHECK(head_units(g, ctx, n, t) == sum, "head_units ctx %d n %d t %d", ctx, n, t);
-            if (t < item_count(g, n)) sum += item_blocks(g, ctx, n, t) + kItemCost;
+            if (t < item_count(g, n)) sum += item_blocks(g, ctx, n, t) + g.cost;
         }
     }
     for (int i = 0; i < 500; i++) {
-        const RowsGeom g{1, pick(1, 128), pick(6, 7), 1};
+        const RowsGeom g{1, pick(1, 128), pick(6, 7), 1, pick(1, 3)};
         const int n = pick(1, 3000), ctx = pick(0, 5000), t = pick(0, item_count(g, n) - 1);
         const int last = (t + 1) * g.PT < n ? (t + 1) * g.PT : n;
         CHECK(item_blocks(g, ctx, n, t) == (ctx + last + (1 << g.shift) - 1) / (1 << g.shift), "item_blocks");
     }
     // a sequence of two billion positions: no overflow
-    const RowsGeom g{1, 1, 6, 1};
+    const RowsGeom g{1, 1, 6, 1, 1};
     CHECK(head_units(g, 2000000000, 1000, 1000) > 1000LL * (2000000000LL / 64), "long context");
 }
 
@@ -73,7 +73,7 @@ static void test_lengths() {
 
 static void test_walk(int nseq, int maxn, int maxctx) {
     const int G = pick(1, 8), tile = pick(0, 1) ? 256 : pick(0, 1) ? 64 : 16;
-    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, pick(6, 7), pick(0, 2) > 0};
+    const RowsGeom g{pick(1, 8), tile / G > 0 ? tile / G : 1, pick(6, 7), pick(0, 2) > 0, pick(1, 3)};
     const int P = pick(0, 3) ? pick(1, 400) : pick(1, 5);
     std::vector<SeqRows> seq(nseq);
     std::vector<long long> wstart(nseq + 1, 0);
@@ -100,7 +100,7 @@ static void test_walk(int nseq, int maxn, int maxctx) {
             CHECK(p.s >= 0 && p.s < nseq && p.g >= 0 && p.g < g.KV && p.t >= 0 && p.t < item_count(g, seq[p.s].n), "item bounds");
             CHECK(p.nb == item_blocks(g, seq[p.s].ctx, seq[p.s].n, p.t), "blocks of the item");
             CHECK(p.kb0 == done[item] && p.kb1 > p.kb0 && p.kb1 <= p.nb, "blocks in order, once");
-            CHECK(p.base >= 0 && p.base + kItemCost + p.nb <= total, "item within the line");
+            CHECK(p.base >= 0 && p.base + g.cost + p.nb <= total, "item within the line");
             done[item] = p.kb1;
             if (p.kb0 == 0 && p.kb1 == p.nb) continue;
             CHECK(g.split, "a whole item was divided");
@@ -123,7 +123,7 @@ static void test_walk(int nseq, int maxn, int maxctx) {
     size_t found = 0;
     for (auto &j : joins) {
         const RowsPiece &p = j.second;
-        const int c0 = j.first, c1 = (int)((p.base + kItemCost + p.nb - 1) / unit);
+        const int c0 = j.first, c1 = (int)((p.base + g.cost + p.nb - 1) / unit);
         std::vector<int> want{2 * c0 + 1};
         for (int c = c0 + 1; c <= c1; c++) want.push_back(2 * c);
         CHECK(of[std::make_tuple(p.s, p.g, p.t)] == want, "pieces of a divided item");
