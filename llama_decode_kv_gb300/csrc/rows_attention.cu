@@ -257,30 +257,28 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
         }
         // the key groups' sums of O (over the first key buffer: KQ R rows are exactly its length)
         float *ks = kv;
-        if (KQ > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int c = 0; c < C; c++)
+                *(float4 *)(ks + ((size_t)kq * R + 4 * ty + i) * LD + 4 * tx + 64 * c) = o[i][c];
+        __syncthreads();
+        if (kq == 0) {
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
-                for (int c = 0; c < C; c++)
-                    *(float4 *)(ks + ((size_t)kq * R + 4 * ty + i) * LD + 4 * tx + 64 * c) = o[i][c];
-            __syncthreads();
-            if (kq == 0) {
+                for (int c = 0; c < C; c++) {
+                    float4 a = o[i][c];
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-#pragma unroll
-                    for (int c = 0; c < C; c++) {
-                        float4 a = o[i][c];
-#pragma unroll
-                        for (int q = 1; q < KQ; q++) {
-                            const float4 b = *(const float4 *)(ks + ((size_t)q * R + 4 * ty + i) * LD + 4 * tx + 64 * c);
-                            a.x += b.x;
-                            a.y += b.y;
-                            a.z += b.z;
-                            a.w += b.w;
-                        }
-                        o[i][c] = a;
+                    for (int q = 1; q < KQ; q++) {
+                        const float4 b = *(const float4 *)(ks + ((size_t)q * R + 4 * ty + i) * LD + 4 * tx + 64 * c);
+                        a.x += b.x;
+                        a.y += b.y;
+                        a.z += b.z;
+                        a.w += b.w;
                     }
-            }
+                    o[i][c] = a;
+                }
         }
         const bool whole = p.kb0 == 0 && p.kb1 == p.nb;
         if (!whole && p.kb0 == 0) {

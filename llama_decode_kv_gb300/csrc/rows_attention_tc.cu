@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (more) drop_k();
             }
         }
-        if (!ok) {  // what was issued still runs: wait for it, bounded
+        if (!ok || __any_sync(0xffffffffu, *stop)) {  // what was issued still runs: wait for it, bounded
             if (elect_one()) {
                 tc_commit(&B->drain);
                 const unsigned long long t0 = global_ns();
