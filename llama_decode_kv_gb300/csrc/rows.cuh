@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "rows_plan.h"
@@ -97,6 +98,11 @@ __device__ __forceinline__ void write_join(const RowsArgs &A, int cta, const Seq
     }
     ((RowsJoin *)A.ws)[cta] = j;
 }
+
+// The maximum of a row's partial state (log2 domain).  -infinity tells the join that the row sees
+// none of the piece's positions; a row that sees some has a finite one, also where every score is
+// NaN (maxima skip those) or -infinity.
+__device__ __forceinline__ float piece_max(float m, bool sees) { return sees ? fmaxf(m, -FLT_MAX) : -INFINITY; }
 
 __device__ __forceinline__ float *slot_ptr(const RowsArgs &A, int slot) {
     return (float *)(A.ws + join_bytes(A.P)) + (size_t)slot * slot_floats(A.slot_rows, A.hd);

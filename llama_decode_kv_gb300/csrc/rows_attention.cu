@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
                     }
                 }
             if (tid < nr) {
-                pm[tid] = mrow[tid];
+                pm[tid] = piece_max(mrow[tid], sr.ctx + tok0 + tid / A.G + 1 > p.kb0 * kSimtBlk);
                 pm[A.slot_rows + tid] = lrow[tid];
             }
         }
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
                 for (int c = 0; c < C; c++)
                     if (4 * tx + 64 * c < A.hd) *(float4 *)(part + ((size_t)(tx + 16 * c) * A.slot_rows + r) * 4) = o[i][c];
                 if (tx == 0) {
-                    part[(size_t)A.slot_rows * A.hd + r] = m[i];
+                    part[(size_t)A.slot_rows * A.hd + r] = piece_max(m[i], seen[i] > p.kb0 * kSimtBlk);
                     part[(size_t)A.slot_rows * (A.hd + 1) + r] = l[i];
                 }
             }
@@ -523,6 +523,9 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
 //
 // Piece i of an item has, per row, the maximum m_i, the sum l_i and the unnormalised O_i:
 //     out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i.
+// m_i = -inf stands for a row that sees none of the piece's positions, and for nothing else: only
+// such a piece is left out (its O may not have been written); one whose scores are all NaN, or all
+// -inf, takes part with m_i = -FLT_MAX, so that what it holds reaches the result as in one pass.
 // Block x looks after the item that attention CTA x starts and another one finishes (RowsJoin);
 // its pieces are slot 2x + 1 and the slots 2c of the CTAs behind x.  A slot holds O as
 // [head_dim / 4][row] quads, so that the attention kernels' row-per-thread epilogue and the reads
@@ -591,7 +594,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
                 }
 #pragma unroll
                 for (int a = 0; a < AT; a++) {
-                    if (mi[a] == -INFINITY) continue;  // no piece, or the row saw nothing of it: O may not have been written
+                    if (mi[a] == -INFINITY) continue;  // no piece, or the row sees none of it
                     const float f = exp2f(mi[a] - M);
                     l = fmaf(f, li[a], l);
 #pragma unroll
@@ -638,7 +641,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
 #pragma unroll 4
         for (int i = warp; i < n; i += 8) {
             const float mi = stats[slot(i) + r];
-            if (mi == -INFINITY) continue;  // the row saw nothing of this piece: its O may not have been written
+            if (mi == -INFINITY) continue;  // the row sees none of this piece
             const float f = exp2f(mi - M);
             l = fmaf(f, stats[slot(i) + R + r], l);
             add4(acc, f, *(const float4 *)(slots + slot(i) + ((size_t)q * R + r) * 4));

@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 }
                 if (valid) {  // the maximum in the log2 domain, as the join takes it
                     float *pm = part + (size_t)A.slot_rows * A.hd + row;
-                    pm[0] = m == -INFINITY ? m : m * c;
+                    pm[0] = piece_max(m * c, seen > p.kb0 * kTcBlk);
                     pm[A.slot_rows] = l;
                 }
             }
