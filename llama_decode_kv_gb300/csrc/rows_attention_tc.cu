@@ -802,25 +802,18 @@ static int tc_stages(int hd, int nseq) {
     return n;
 }
 
-template <int HDP, bool PAGED> static cudaError_t launch_tc(const RowsTcArgs &t, cudaStream_t s) {
-    const size_t smem = tc_fixed_bytes(HDP, t.stages) + (size_t)t.a.nseq * sizeof(SeqRows) + (size_t)(t.a.nseq + 1) * 8;
+// The attribute comes first: it is the runtime call that makes the device's context current on a
+// host thread that has made none yet, and tensor maps are encoded by a driver call, which fails
+// without one.
+template <int HDP, bool PAGED> static cudaError_t launch_tc(RowsTcArgs &t, cudaStream_t s) {
+    const RowsArgs &a = t.a;
+    const size_t smem = tc_fixed_bytes(HDP, t.stages) + (size_t)a.nseq * sizeof(SeqRows) + (size_t)(a.nseq + 1) * 8;
     cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<HDP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<HDP, PAGED>, dim3(t.a.P), dim3(kTcThreads), smem, s, t);
-}
-
-cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {
-    RowsTcArgs t{};
-    t.a = a;
-    t.TT = a.geom.PT / 2;
-    t.stages = tc_stages(a.hd, a.nseq);
-    t.wide = ((uintptr_t)a.out & 31) == 0 && a.hd % 16 == 0 && a.out_ld % 16 == 0;
-    const bool paged = a.kv.table != nullptr;
     const uint64_t hb = (uint64_t)a.hd * 2;  // bytes of a head
     const uint64_t qd[] = {(uint64_t)a.hd, (uint64_t)a.H, (uint64_t)a.rows}, qs[] = {hb, (uint64_t)a.q_ld * 2};
     const uint32_t qb[] = {64, (uint32_t)a.G, (uint32_t)t.TT};
-    cudaError_t e = make_bf16_map_nd(&t.q, a.q, 3, qd, qs, qb);
-    if (paged) {
+    if (e == cudaSuccess) e = make_bf16_map_nd(&t.q, a.q, 3, qd, qs, qb);
+    if (PAGED) {
         const uint64_t page = 1ull << a.kv.page_shift;
         t.box = page < kTcBlk ? (int)page : kTcBlk;
         const uint64_t d[] = {(uint64_t)a.hd, page, (uint64_t)a.KV, (uint64_t)a.kv.n_pages};
@@ -837,6 +830,16 @@ cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {
         if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 3, d, vs, b);
     }
     if (e != cudaSuccess) return e;
+    return launch_pdl(rows_tc_kernel<HDP, PAGED>, dim3(a.P), dim3(kTcThreads), smem, s, t);
+}
+
+cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s) {
+    RowsTcArgs t{};
+    t.a = a;
+    t.TT = a.geom.PT / 2;
+    t.stages = tc_stages(a.hd, a.nseq);
+    t.wide = ((uintptr_t)a.out & 31) == 0 && a.hd % 16 == 0 && a.out_ld % 16 == 0;
+    const bool paged = a.kv.table != nullptr;
     if (a.hd <= 64) return paged ? launch_tc<64, true>(t, s) : launch_tc<64, false>(t, s);
     return paged ? launch_tc<128, true>(t, s) : launch_tc<128, false>(t, s);
 }

@@ -1,0 +1,58 @@
+"""The packed-row calls from host threads other than the main one."""
+import threading
+
+import pytest
+
+from test_gpu_rows import BF16, F32, Batch, slm  # noqa: F401  (slm: the fixture)
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def together(*jobs):
+    """Run the jobs at once, a thread each; what they raise."""
+    errors, start = [], threading.Barrier(len(jobs))
+
+    def work(job):
+        try:
+            start.wait()
+            job()
+        except Exception as e:  # noqa: BLE001  (seen by the caller)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 256)])
+def test_the_first_call_of_a_host_thread(slm, dtype, hd):  # noqa: F811
+    """A thread that has not used the GPU yet has no current context: each call makes its own."""
+    b = Batch(dtype, 4, 2, hd, [30, 1], None, 16, seed=1)
+    want, out, ws = b.out(), b.out(), b.workspace(slm)
+    stream = torch.cuda.Stream()
+
+    def append():
+        slm.kv_append(b.k, b.v, b.k_cache, b.v_cache, b.page_table, b.row_start, None, b.status, stream=stream)
+
+    def paged(o=out):
+        slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, None, o, ws, b.status, stream=stream)
+
+    def prompt():
+        slm.attention_prompt(b.q, b.k, b.v, b.row_start, out, ws, b.status, stream=stream)
+
+    torch.cuda.synchronize()
+    assert not together(append)
+    paged(want)
+    torch.cuda.synchronize()
+    for job in (paged, prompt):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        errors = together(job)
+        assert not errors, errors
+        assert torch.equal(out, want)
+    assert int(b.status.item()) == 0
