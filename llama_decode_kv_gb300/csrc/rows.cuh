@@ -114,6 +114,13 @@ __device__ __forceinline__ float *slot_ptr(const RowsArgs &A, int slot) {
 
 int attn_fail(int code, const char *fmt, ...);  // records the text, returns the code
 
+// Let the launches of `kernel` ask for up to kSmemLimit bytes of shared memory.  The attribute is
+// the function's, on the current device, not the launch's: with the same value from every call, no
+// other host thread's launch can find it lowered between here and there.
+inline cudaError_t allow_smem(const void *kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+}
+
 // The joining launch: every item that several CTAs share, from its partial states.
 cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 

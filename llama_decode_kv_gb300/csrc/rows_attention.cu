@@ -708,14 +708,14 @@ int rows_simt_ctas(int sms, int hd, int R, int nseq) {
 
 template <int HDP> static cudaError_t launch_fma(const RowsArgs &a, cudaStream_t s) {
     const size_t smem = simt_smem<float, HDP, 64>(a.nseq);
-    cudaError_t e = cudaFuncSetAttribute(rows_fma_kernel<HDP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem((const void *)rows_fma_kernel<HDP>);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_fma_kernel<HDP>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
 }
 
 template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsArgs &a, cudaStream_t s) {
     const size_t smem = simt_smem<T, HDP, R>(a.nseq);
-    cudaError_t e = cudaFuncSetAttribute(rows_simt_kernel<T, HDP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem((const void *)rows_simt_kernel<T, HDP, R>);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_simt_kernel<T, HDP, R>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
 }

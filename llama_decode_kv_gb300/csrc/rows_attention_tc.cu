@@ -808,7 +808,7 @@ static int tc_stages(int hd, int nseq) {
 template <int HDP, bool PAGED> static cudaError_t launch_tc(RowsTcArgs &t, cudaStream_t s) {
     const RowsArgs &a = t.a;
     const size_t smem = tc_fixed_bytes(HDP, t.stages) + (size_t)a.nseq * sizeof(SeqRows) + (size_t)(a.nseq + 1) * 8;
-    cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<HDP, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem((const void *)rows_tc_kernel<HDP, PAGED>);
     const uint64_t hb = (uint64_t)a.hd * 2;  // bytes of a head
     const uint64_t qd[] = {(uint64_t)a.hd, (uint64_t)a.H, (uint64_t)a.rows}, qs[] = {hb, (uint64_t)a.q_ld * 2};
     const uint32_t qb[] = {64, (uint32_t)a.G, (uint32_t)t.TT};

@@ -56,3 +56,32 @@ def test_the_first_call_of_a_host_thread(slm, dtype, hd):  # noqa: F811
         assert not errors, errors
         assert torch.equal(out, want)
     assert int(b.status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("chunk", [1, 40])
+def test_two_host_threads(slm, dtype, hd, chunk):  # noqa: F811
+    """Batches of very different numbers of sequences (and so of shared memory) on the same
+    kernel, a thread, a stream and a workspace each: every call succeeds, with the bits that it
+    gives alone.  chunk: the sequences' new tokens (the CUDA-core tile follows them)."""
+    few = Batch(dtype, 4, 2, hd, [chunk], [100], 16, seed=1)
+    many = Batch(dtype, 4, 2, hd, [chunk] * 500, [i % 50 for i in range(500)], 16, seed=2)
+    jobs, outs = [], []
+    for b in (few, many):
+        b.fill([n + c for n, c in zip(b.new, b.ctx)])
+        out, ws, stream = b.out(), b.workspace(slm), torch.cuda.Stream()
+
+        def call(b=b, out=out, ws=ws, stream=stream):
+            slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, ws, b.status,
+                                stream=stream)
+
+        torch.cuda.synchronize()
+        call()
+        torch.cuda.synchronize()
+        outs.append((b, out, out.clone()))
+        jobs.append(lambda call=call: [call() for _ in range(1500)])
+    errors = together(*jobs)
+    assert not errors, errors
+    for b, out, want in outs:
+        assert torch.equal(out, want)
+        assert int(b.status.item()) == 0
