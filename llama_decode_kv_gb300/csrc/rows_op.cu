@@ -50,6 +50,13 @@ static int check_pointers(int dev, const PtrCheck *list, int n) {
     return SLM_OK;
 }
 
+// A launch that was refused.  The runtime keeps the error for the thread's next check, which may be
+// another call's: it is taken here.
+static int launch_fail(const char *what, cudaError_t e) {
+    cudaGetLastError();
+    return attn_fail(SLM_ECUDA, "%s launch: %s", what, cudaGetErrorString(e));
+}
+
 static int elem_size(int dtype) { return dtype == SLM_F32 ? 4 : 2; }
 
 static int check_dtype(int dtype, const char *name) {
@@ -167,7 +174,7 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     }
     cudaError_t e = on_tensor_cores(dtype, a.hd) ? rows_tc_launch(a, s) : rows_simt_launch(a, bf16, s);
     if (e == cudaSuccess && a.geom.split) e = rows_join_launch(a, bf16, s);
-    if (e != cudaSuccess) return attn_fail(SLM_ECUDA, "attention launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return launch_fail("attention", e);
     return SLM_OK;
 }
 
@@ -229,7 +236,7 @@ extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, in
     a.page_shift = log2i(cache->page_size);
     a.status = status;
     const cudaError_t e = rows_append_launch(a, dtype == SLM_BF16, cache->kv_dtype == SLM_BF16, (cudaStream_t)stream);
-    if (e != cudaSuccess) return attn_fail(SLM_ECUDA, "append launch: %s", cudaGetErrorString(e));
+    if (e != cudaSuccess) return launch_fail("append", e);
     return SLM_OK;
 }
 

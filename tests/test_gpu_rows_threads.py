@@ -1,4 +1,6 @@
-"""The packed-row calls from host threads other than the main one."""
+"""The packed-row calls from host threads other than the main one, and after a launch that the
+driver refuses."""
+import ctypes
 import threading
 
 import pytest
@@ -85,3 +87,36 @@ def test_two_host_threads(slm, dtype, hd, chunk):  # noqa: F811
     for b, out, want in outs:
         assert torch.equal(out, want)
         assert int(b.status.item()) == 0
+
+
+def test_a_refused_launch_is_not_held_against_the_next_call(slm):  # noqa: F811
+    """The legacy stream takes no work while a blocking stream is captured: the packed-row calls
+    say so, and calls that follow do not meet the error again."""
+    try:
+        rt = ctypes.CDLL("libcudart.so.13")
+    except OSError:
+        pytest.skip("no shared CUDA runtime to capture with")
+    b = Batch(BF16, 4, 2, 64, [1], [30], 16, seed=3)
+    b.fill([31])
+    out, ws = b.out(), b.workspace(slm)
+    q = torch.ones(1, 4, 64, device="cuda")
+    kc, ref = torch.ones(1, 2, 8, 64, device="cuda"), torch.zeros(1, 4, 64, device="cuda")
+    aws = torch.empty(slm.slm_attention_workspace_bytes(1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    calls = [lambda: slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, ws, b.status,
+                                         stream=0),
+             lambda: slm.kv_append(b.k, b.v, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, b.status, stream=0)]
+    for call in calls:
+        stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(stream)) == 0
+        assert rt.cudaStreamBeginCapture(stream, 2) == 0  # relaxed: only this stream's work is watched
+        try:
+            with pytest.raises(slm.SlmError, match="launch"):
+                call()
+        finally:
+            rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+            rt.cudaGetLastError()
+            assert rt.cudaStreamDestroy(stream) == 0
+        assert slm.attention_decode(q, kc, kc, [8], ref, aws, slm.SLM_F32) == 0, slm.slm_last_error(None)
+        torch.cuda.synchronize()
+        assert bool((ref == 1).all())
