@@ -435,7 +435,7 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
  * of 8 in [8, 256]; q, k, v, out and the cache 16-byte aligned; row strides (*_ld, in elements,
  * from one packed row to the next) of at least heads * head_dim and a multiple of 16 bytes, so
  * q, k and v may be column ranges of one projection's output; heads of a row are adjacent.
- * rows = 0 is allowed and does nothing.  Every pointer but the structs themselves is device
+ * rows = 0 is allowed and does nothing (q, k, v and out may be NULL then).  Every pointer but the structs themselves is device
  * memory of the current device (checked).  The calls are asynchronous on `stream`, allocate
  * nothing and may be captured.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED, SLM_ECUDA; the text is
  * in slm_last_error(NULL).

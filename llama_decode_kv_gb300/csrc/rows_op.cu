@@ -94,8 +94,10 @@ static int check_cache(const slm_kv_cache *c) {
     return SLM_OK;
 }
 
-// Packed rows of `heads` heads: base and row stride (elements) on 16-byte boundaries.
+// Packed rows of `heads` heads: base and row stride (elements) on 16-byte boundaries.  Without rows
+// neither means anything (an empty tensor has no address).
 static int check_packed(const void *p, long long ld, int heads, int hd, int dtype, int rows, const char *name) {
+    if (rows == 0) return SLM_OK;
     if (!p) return attn_fail(SLM_EINVAL, "%s is NULL", name);
     if ((uintptr_t)p & 15) return attn_fail(SLM_EINVAL, "%s must be 16-byte aligned", name);
     if (rows > 1 && (ld < (long long)heads * hd || ld > (1LL << 32)))
