@@ -480,9 +480,10 @@ int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype
                   int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status, void *stream);
 
 /*
- * slm_attention_rows_workspace_bytes -- bytes of workspace for slm_attention_paged and
- * slm_attention_prompt at this shape on the current device, whatever the lengths are; 0 for
- * arguments that they refuse, or without a device.
+ * slm_attention_rows_workspace_bytes -- bytes of workspace for slm_attention_paged (dtype: the
+ * cache's) and slm_attention_prompt at this shape on the current device, whatever the lengths are;
+ * 0 for arguments that they refuse, or without a device.  The bytes do not grow when rows or nseq
+ * shrink, so the workspace of a program's largest batch serves all its batches of that shape.
  */
 size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t nseq, int32_t n_heads,
                                           int32_t n_kv_heads, int32_t head_dim);

@@ -125,7 +125,9 @@ inline cudaError_t allow_smem(const void *kernel) {
 cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 
 // CUDA-core attention: fp32, and bf16 heads wider than 128.
-int rows_simt_tile(int rows, int nseq, int G, int hd);  // query rows (token, head) per item
+constexpr int kSimtSmallTile = 16;                      // query rows (token, head) per item: of the small tile,
+int rows_simt_wide_tile(int hd);                        // of the wide one,
+int rows_simt_tile(int rows, int nseq, int G, int hd);  // and of the one that a call takes
 int rows_simt_ctas(int sms, int hd, int R, int nseq);
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 

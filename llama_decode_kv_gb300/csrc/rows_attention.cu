@@ -689,9 +689,10 @@ cudaError_t rows_join_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
 // 16 rows when the average sequence's rows fit them (decode steps), else 64 (32 for heads wider
 // than 128, whose keys and values fill the shared memory).  The choice needs no length: any
 // item of either tile is right.
+int rows_simt_wide_tile(int hd) { return hd <= 128 ? 64 : 32; }
 int rows_simt_tile(int rows, int nseq, int G, int hd) {
-    if ((long long)rows * G <= 16LL * nseq && G <= 16) return 16;
-    return hd <= 128 ? 64 : 32;
+    if ((long long)rows * G <= (long long)kSimtSmallTile * nseq && G <= kSimtSmallTile) return kSimtSmallTile;
+    return rows_simt_wide_tile(hd);
 }
 
 static size_t simt_bytes(int hd, int R, int nseq) {  // fp32: bf16 needs no more
@@ -721,7 +722,7 @@ template <typename T, int HDP, int R> static cudaError_t launch_simt(const RowsA
 }
 
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s) {
-    const bool small = a.geom.PT * a.G <= 16;
+    const bool small = a.geom.PT * a.G <= kSimtSmallTile;
     if (bf16) return small ? launch_simt<__nv_bfloat16, 256, 16>(a, s) : launch_simt<__nv_bfloat16, 256, 32>(a, s);
     if (a.hd <= 64) return small ? launch_simt<float, 64, 16>(a, s) : launch_fma<64>(a, s);
     if (a.hd <= 128) return small ? launch_simt<float, 128, 16>(a, s) : launch_fma<128>(a, s);

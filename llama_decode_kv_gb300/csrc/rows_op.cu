@@ -145,8 +145,19 @@ static RowsTiling rows_tiling(int sms, int dtype, int rows, int nseq, int H, int
         t.geom = {KV, R / G, 6, 1, 1};
         t.P = rows_simt_ctas(sms, hd, R, nseq);
     }
-    t.slot_rows = (int)std::min<long long>((long long)t.geom.PT * G, (long long)std::max(rows, 1) * G);
-    t.ws = rows_ws_bytes(t.P, t.slot_rows, hd);
+    auto slot = [&](int PT) { return (int)std::min<long long>((long long)PT * G, (long long)std::max(rows, 1) * G); };
+    t.slot_rows = slot(t.geom.PT);
+    // A workspace serves every call of no more rows and sequences: on the CUDA cores the tile and the
+    // CTAs of a launch do not only grow with them, so it is the most of both tiles, at the CTAs of one
+    // sequence.
+    if (on_tensor_cores(dtype, hd)) {
+        t.ws = rows_ws_bytes(t.P, t.slot_rows, hd);
+    } else {
+        const int wide = rows_simt_wide_tile(hd);
+        t.ws = rows_ws_bytes(rows_simt_ctas(sms, hd, wide, 1), slot(wide / G), hd);
+        if (G <= kSimtSmallTile)
+            t.ws = std::max(t.ws, rows_ws_bytes(rows_simt_ctas(sms, hd, kSimtSmallTile, 1), slot(kSimtSmallTile / G), hd));
+    }
     return t;
 }
 

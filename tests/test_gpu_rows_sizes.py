@@ -1,7 +1,10 @@
-"""The sizes at the ends of what the packed-row calls take: no row at all."""
+"""The sizes at the ends of what the packed-row calls take: no row at all, and a workspace that
+is kept for the largest batch."""
+import itertools
+
 import pytest
 
-from test_gpu_rows import BF16, F32, Batch, rope_table, slm  # noqa: F401  (slm: the fixture)
+from test_gpu_rows import BF16, F32, Batch, check_attention, rope_table, slm  # noqa: F401  (slm: the fixture)
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -22,3 +25,29 @@ def test_empty_tensors(slm, dtype):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.equal(b.k_cache.nan_to_num(9.0), kc.nan_to_num(9.0)) and torch.equal(b.v_cache.nan_to_num(9.0), vc.nan_to_num(9.0))
     assert int(b.status.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_workspace_of_a_large_batch_serves_the_smaller_ones(slm, dtype):  # noqa: F811
+    """The bytes do not grow when rows or nseq shrink."""
+    rows, seqs = (1, 2, 5, 16, 17, 63, 64, 65, 500, 5000), (1, 2, 5, 64, 300, 523, 524, 1024)
+    for G, hd in itertools.product((1, 3, 4, 7, 16, 17, 32), (8, 64, 72, 128, 136, 256)):
+        size = lambda r, n: slm.attention_rows_workspace_bytes(dtype, r, n, 2 * G, 2, hd)  # noqa: E731, B023
+        for i, j in itertools.product(range(len(rows)), range(len(seqs))):
+            here = size(rows[i], seqs[j])
+            assert here > 0
+            assert i == 0 or size(rows[i - 1], seqs[j]) <= here, (G, hd, rows[i - 1], seqs[j])
+            assert j == 0 or size(rows[i], seqs[j - 1]) <= here, (G, hd, rows[i], seqs[j - 1])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_workspace_for_a_shrinking_batch(slm, dtype):  # noqa: F811
+    """A workspace of 64 tokens in 64 sequences, then a chunk of 64 tokens in one."""
+    keep = None
+    for new in ([1] * 64, [64]):
+        b = Batch(dtype, 6, 2, 64, new, [700] * len(new), 16, seed=len(new))
+        b.fill([n + c for n, c in zip(b.new, b.ctx)])
+        keep = b.workspace(slm) if keep is None else keep
+        out = b.out()
+        slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, keep, b.status)
+        check_attention(b, out, b.seq_k, b.seq_v, dtype)
