@@ -73,7 +73,7 @@ static int check_heads(int H, int KV, int hd) {
 static int check_rows(const slm_rows *r) {
     if (!r) return attn_fail(SLM_EINVAL, "rows is NULL");
     if (r->nseq < 1 || r->nseq > kRowsMaxSeqs) return attn_fail(SLM_EINVAL, "nseq %d outside [1, %d]", r->nseq, kRowsMaxSeqs);
-    if (r->rows < 0 || r->rows > (1 << 30)) return attn_fail(SLM_EINVAL, "rows %d outside [0, 2^30]", r->rows);
+    if (r->rows < 0 || r->rows > kRowsMaxRows) return attn_fail(SLM_EINVAL, "rows %d outside [0, 2^30]", r->rows);
     if (!r->row_start) return attn_fail(SLM_EINVAL, "row_start is NULL");
     if ((uintptr_t)r->row_start % 4 || (uintptr_t)r->ctx_len % 4) return attn_fail(SLM_EINVAL, "row_start and ctx_len must be 4-byte aligned");
     return SLM_OK;
@@ -255,7 +255,7 @@ extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, in
 
 extern "C" size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t nseq, int32_t n_heads,
                                                      int32_t n_kv_heads, int32_t head_dim) {
-    if (rows < 0 || nseq < 1 || nseq > kRowsMaxSeqs || check_dtype(dtype, "dtype") || check_heads(n_heads, n_kv_heads, head_dim) ||
+    if (rows < 0 || rows > kRowsMaxRows || nseq < 1 || nseq > kRowsMaxSeqs || check_dtype(dtype, "dtype") || check_heads(n_heads, n_kv_heads, head_dim) ||
         check_group(n_heads, n_kv_heads, head_dim))
         return 0;
     int dev = 0;

@@ -51,3 +51,8 @@ def test_one_workspace_for_a_shrinking_batch(slm, dtype):  # noqa: F811
         out = b.out()
         slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, keep, b.status)
         check_attention(b, out, b.seq_k, b.seq_v, dtype)
+
+
+def test_workspace_of_more_rows_than_a_call_takes_is_zero(slm):  # noqa: F811
+    assert slm.attention_rows_workspace_bytes(BF16, 1 << 30, 4, 4, 2, 64) > 0
+    assert slm.attention_rows_workspace_bytes(BF16, (1 << 30) + 1, 4, 4, 2, 64) == 0
