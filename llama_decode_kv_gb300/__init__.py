@@ -241,6 +241,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
         n_rope = rope.shape[0]
         if rope.dtype is not _F32 or rope.shape != (n_rope, hd // 2, 2) or not rope.is_contiguous():
             raise ValueError(f"rope: {tuple(rope.shape)} {rope.dtype}, expected contiguous float32 [n][{hd // 2}][2]")
+        if n_rope == 0:  # an empty tensor has no address, which would mean: no rotation
+            raise ValueError("rope holds no position")
         rope_ptr = rope.data_ptr()
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")

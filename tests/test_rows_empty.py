@@ -36,3 +36,12 @@ def test_binding_takes_empty_tensors():
         with pytest.raises(slm.SlmError) as e:  # host memory, or no device to look at
             call()
         assert _passes_the_checks(e.value.code), e.value
+
+
+def test_binding_refuses_an_empty_rotation_table():
+    """A table of no positions is not the same as no table (nothing rotated)."""
+    torch = pytest.importorskip("torch")
+    k, kc = torch.zeros(3, 2, 16), torch.zeros(4, 2, 16, 16)
+    tab, rs, st = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="no position"):
+        slm.kv_append(k, k, kc, kc, tab, rs, None, st, torch.zeros(0, 8, 2), stream=0)
