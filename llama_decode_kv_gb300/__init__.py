@@ -216,6 +216,12 @@ def _cache(k_cache, v_cache, page_table, kv: int, hd: int, what: str) -> bytes:
                        ld, heads, chd, _dtype_code(dt))
 
 
+def _workspace(x):
+    if not x.is_contiguous():  # the library writes nbytes in a row from its first element
+        raise ValueError(f"workspace must be contiguous (strides {x.stride()})")
+    return x.data_ptr(), x.nbytes
+
+
 def _rows_stream(stream, x):
     dev = x.get_device()
     return _raw_stream(dev) if stream is None and dev >= 0 else _stream_ptr(stream)
@@ -278,8 +284,8 @@ def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, wo
     r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
                    0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
-    rc = slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, workspace.data_ptr(),
-                             workspace.nbytes, _ints(status, "status", 1), _rows_stream(stream, q))
+    rc = slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace),
+                             _ints(status, "status", 1), _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_paged", slm_last_error(None).decode())
 
@@ -297,7 +303,7 @@ def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) ->
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
     k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
     rc = slm_attention_prompt(r, code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                              out.data_ptr(), o_ld, workspace.data_ptr(), workspace.nbytes, _ints(status, "status", 1),
+                              out.data_ptr(), o_ld, *_workspace(workspace), _ints(status, "status", 1),
                               _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_prompt", slm_last_error(None).decode())

@@ -1,5 +1,5 @@
-"""Empty tensors in the packed-row calls, on the CPU: what the argument checks make of them before
-the first look at a device."""
+"""Empty tensors and tensors with gaps in the packed-row calls, on the CPU: what the argument checks
+make of them before the first look at a device."""
 
 import pytest
 
@@ -45,3 +45,16 @@ def test_binding_refuses_an_empty_rotation_table():
     tab, rs, st = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="no position"):
         slm.kv_append(k, k, kc, kc, tab, rs, None, st, torch.zeros(0, 8, 2), stream=0)
+
+
+def test_binding_refuses_a_workspace_with_gaps():
+    """The library writes nbytes from the first element on: with gaps, past the tensor's elements
+    into its neighbours'."""
+    torch = pytest.importorskip("torch")
+    k, kc = torch.zeros(3, 2, 16), torch.zeros(4, 2, 16, 16)
+    tab, rs, st = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)[::2]
+    with pytest.raises(ValueError, match="workspace"):
+        slm.attention_paged(k, kc, kc, tab, rs, None, k, ws, st, stream=0)
+    with pytest.raises(ValueError, match="workspace"):
+        slm.attention_prompt(k, k, k, rs, k, ws, st, stream=0)
