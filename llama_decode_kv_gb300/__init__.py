@@ -266,7 +266,8 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
 
 
 def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
-    """slm_attention_rows_workspace_bytes; dtype is a torch dtype."""
+    """slm_attention_rows_workspace_bytes; dtype is a torch dtype: the cache's for attention_paged
+    (kv_append may have converted q), that of q, k, v for attention_prompt."""
     return int(slm_attention_rows_workspace_bytes(_dtype_code(dtype), rows, nseq, n_heads, n_kv_heads, head_dim))
 
 

@@ -1,6 +1,5 @@
 """Empty tensors and tensors with gaps in the packed-row calls, on the CPU: what the argument checks
 make of them before the first look at a device."""
-
 import pytest
 
 from test_rows_refusals import _append, _paged, _prompt, _rows, _why, slm
