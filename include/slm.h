@@ -431,13 +431,14 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
  *                     for that sequence.
  * No call reads or writes outside its buffers because of a length or a page id.
  *
- * Requirements of all three: nseq in [1, 1024]; rows at most 2^30; n_heads % n_kv_heads == 0; head_dim a multiple
- * of 8 in [8, 256]; q, k, v, out and the cache 16-byte aligned; row strides (*_ld, in elements,
- * from one packed row to the next) of at least heads * head_dim and a multiple of 16 bytes, so
- * q, k and v may be column ranges of one projection's output; heads of a row are adjacent.
- * rows = 0 is allowed and does nothing (q, k, v and out may be NULL then).  Every pointer but the structs themselves is device
- * memory of the current device (checked).  The calls are asynchronous on `stream`, allocate
- * nothing and may be captured.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED, SLM_ECUDA; the text is
+ * Requirements of all three: nseq in [1, 1024]; rows at most 2^30; n_heads % n_kv_heads == 0, at
+ * most 65,536 heads of either kind; head_dim a multiple of 8 in [8, 256]; q, k, v, out and the
+ * cache 16-byte aligned; row strides (*_ld, in elements, from one packed row to the next) of at
+ * least heads * head_dim and a multiple of 16 bytes, so q, k and v may be column ranges of one
+ * projection's output; heads of a row are adjacent.  rows = 0 is allowed and does nothing (q, k, v
+ * and out may be NULL then).  Every pointer but the structs themselves is device memory of the
+ * current device (checked).  The calls are asynchronous on `stream`, allocate nothing and may be
+ * captured; calls from several host threads may overlap.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED, SLM_ECUDA; the text is
  * in slm_last_error(NULL).
  */
 typedef struct {

@@ -66,6 +66,7 @@ static int check_dtype(int dtype, const char *name) {
 
 static int check_heads(int H, int KV, int hd) {
     if (H < 1 || KV < 1 || H % KV) return attn_fail(SLM_EINVAL, "n_heads %d must be a positive multiple of n_kv_heads %d", H, KV);
+    if (H > kRowsMaxHeads) return attn_fail(SLM_EINVAL, "n_heads %d above %d", H, kRowsMaxHeads);
     if (hd < 8 || hd % 8 || hd > 256) return attn_fail(SLM_EINVAL, "head_dim %d must be a multiple of 8 in [8, 256]", hd);
     return SLM_OK;
 }
@@ -82,7 +83,8 @@ static int check_rows(const slm_rows *r) {
 static int check_cache(const slm_kv_cache *c) {
     if (!c) return attn_fail(SLM_EINVAL, "cache is NULL");
     if (check_dtype(c->kv_dtype, "kv_dtype")) return SLM_EINVAL;
-    if (c->n_kv_heads < 1) return attn_fail(SLM_EINVAL, "n_kv_heads %d < 1", c->n_kv_heads);
+    if (c->n_kv_heads < 1 || c->n_kv_heads > kRowsMaxHeads)
+        return attn_fail(SLM_EINVAL, "n_kv_heads %d outside [1, %d]", c->n_kv_heads, kRowsMaxHeads);
     if (c->head_dim < 8 || c->head_dim % 8 || c->head_dim > 256)
         return attn_fail(SLM_EINVAL, "head_dim %d must be a multiple of 8 in [8, 256]", c->head_dim);
     if (c->page_size < 16 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)))

@@ -26,6 +26,7 @@ namespace slm {
 
 constexpr int kRowsMaxSeqs = 1024;  // sequences per call (their lengths sit in shared memory)
 constexpr int kRowsMaxRows = 1 << 30;  // packed rows per call
+constexpr int kRowsMaxHeads = 65536;  // a row's units are counted in 32 bits
 constexpr int kRowsMaxGroup = 64;   // query heads per kv head
 
 // A sequence's rows after its lengths were checked: first packed row, rows, cached positions.
