@@ -524,6 +524,16 @@ int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, i
                          void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
                          void *stream);
 
+/*
+ * slm_debug_rows_faults -- test hook for the abandoned calls of the tensor-core attention (no page
+ * counterpart; see slm_debug_faults).  In every following packed-row attention call of the process,
+ * lost = 1: the arrival of keys and values is never complete, so that the tensor core's wait runs
+ * out; lost = 2: an output tile is never complete, so that the softmax's wait runs out; 0: as usual.
+ * The call then finishes without hanging (after about a second, the limit of a wait, or two),
+ * SLM_ROWS_TIMEOUT is set and its results are invalid.  Returns SLM_OK or SLM_EINVAL.
+ */
+int slm_debug_rows_faults(int32_t lost);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,6 +92,7 @@ _SIGS = {
     "slm_attention_paged": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
     "slm_attention_prompt": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
                                             ctypes.c_size_t, _P, _P]),
+    "slm_debug_rows_faults": (ctypes.c_int, [_I32]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)

@@ -34,6 +34,7 @@ struct RowsArgs {
     uint8_t *ws;
     int P, slot_rows;
     RowsGeom geom;
+    int lost;                        // test hook: a hand-off that never completes (slm_debug_rows_faults)
 };
 
 // Workspace: one RowsJoin per CTA, then 2 P slots of slot_rows unnormalised output rows

@@ -35,7 +35,9 @@
 // Rounding: q, k, v as given; S, maxima, sums and O in fp32; P to bf16 (at most 2^-8 relative:
 // the tensor core takes 16-bit operands), the result to bf16.
 //
-// Every wait is bounded; the first to run out stops all roles, and tensor memory is freed.
+// Every wait is bounded; the first to run out stops all roles.  The MMA warp and the producer end
+// only when what they issued has run (bounded too), whoever gave up and whenever; then tensor memory
+// is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -329,8 +331,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     const int TT = T.TT, PT = A.geom.PT, G = A.G;
 
     if (tid == 0) {
+        // test hook (slm_debug_rows_faults): a barrier that waits for one more arrival never completes
+        const uint32_t kv_arrivals = 1 + (A.lost == 1), o_arrivals = 1 + (A.lost == 2);
         for (int s = 0; s < T.stages; s++) {
-            mbar_init(&B->kv_full[s], 1);
+            mbar_init(&B->kv_full[s], kv_arrivals);
             mbar_init(&B->kv_empty[s], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             mbar_init(&B->s_full[i], 1);
             mbar_init(&B->p_half[i], 4);
             mbar_init(&B->p_ready[i], 4);
-            mbar_init(&B->o_full[i], 1);
+            mbar_init(&B->o_full[i], o_arrivals);
         }
         mbar_init(&B->drain, 1);
         mbar_init(&B->x_full, 4);
@@ -384,6 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             const bool valid = tok < v.ntok && r < TT * G;
             const bool busy = __any_sync(0xffffffffu, valid);    // else only the hand-offs
             const int seen = sr.ctx + v.tok0 + tok + 1;          // positions the row sees
+            const bool sees = seen > p.kb0 * kTcBlk;             // some of the piece's
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             const uint32_t op0 = op;  // phases that this piece's O completes
@@ -545,7 +550,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 }
                 if (valid) {  // the maximum in the log2 domain, as the join takes it
                     float *pm = part + (size_t)A.slot_rows * A.hd + row;
-                    pm[0] = piece_max(m * c, seen > p.kb0 * kTcBlk);
+                    pm[0] = piece_max(m * c, sees);
                     pm[A.slot_rows] = l;
                 }
             }
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         // the ring stages of the next block's K and V (K, V, K, V, ... in the ring), and their phases
         uint32_t ks = 0, kph = 0, vs = 1, vph = 0;
         uint32_t qph = 0, pph = 0;  // phases of q_full and of p_half, p_ready: bit i
-        bool ok = true;
+        bool ok = true, ran = false;  // ran: something was issued
         auto forward = [&](uint32_t &st, uint32_t &ph) {
             st += 2;
             if (st >= (uint32_t)T.stages) {
@@ -637,6 +642,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 auto score = [&](int b) {
                     if (!tc_wait(&B->kv_full[ks], kph, A.status, stop)) return false;
                     tc_after();
+                    ran = true;
                     if (elect_one()) {
                         issue_s(b & 1, 0);
                         tc_commit(&B->s_full[b & 1]);
@@ -664,6 +670,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = tc_wait(&B->q_full[i], qph >> i & 1, A.status, stop))) break;
                 qph ^= 1u << i;
                 tc_after();
+                ran = true;
                 if (elect_one()) {
                     issue_s(i, i);
                     tc_commit(&B->s_full[i]);
@@ -694,15 +701,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (more) drop_k();
             }
         }
-        if (!ok || __any_sync(0xffffffffu, *stop)) {  // what was issued still runs: wait for it, bounded
-            if (elect_one()) {
-                tc_commit(&B->drain);
-                const unsigned long long t0 = global_ns();
-                while (!mbar_try_wait(&B->drain, 0) && global_ns() - t0 < kWaitLimitNs) {
-                }
+        // What was issued has run, and its commits have arrived, before the CTA gives up its tensor and
+        // shared memory -- in an abandoned call too, whoever gives up and however late.
+        if (ran && elect_one()) {
+            tc_commit(&B->drain);
+            const unsigned long long t0 = global_ns();
+            while (!mbar_try_wait(&B->drain, 0) && global_ns() - t0 < kWaitLimitNs) {
             }
-            __syncwarp();
         }
+        __syncwarp();
     } else if (warp == 9) {
         // ---------------------------------------------------------------- TMA producer
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
@@ -771,18 +778,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 page = after;
             }
         }
-        if (*stop) {  // copies in flight end before the shared memory goes: wait for them, bounded
-            const unsigned long long t0 = global_ns();
-            const uint32_t back = min(issued, (uint32_t)T.stages);
-            for (uint32_t b = 1; b <= back; b++) {
-                const uint32_t q = issued - b;
-                while (!mbar_try_wait(&B->kv_full[q % T.stages], (q / T.stages) & 1) && global_ns() - t0 < kWaitLimitNs) {
-                }
+        // The copies have landed before the shared memory goes, as above.
+        const unsigned long long t0 = global_ns();
+        const uint32_t back = min(issued, (uint32_t)T.stages);
+        for (uint32_t b = 1; b <= back; b++) {
+            const uint32_t q = issued - b;
+            while (!mbar_try_wait(&B->kv_full[q % T.stages], (q / T.stages) & 1) && global_ns() - t0 < kWaitLimitNs) {
             }
-            for (int i = 0; i < 2; i++)
-                while (qn[i] > 0 && !mbar_try_wait(&B->q_full[i], (qn[i] - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
-                }
         }
+        for (int i = 0; i < 2; i++)
+            while (qn[i] > 0 && !mbar_try_wait(&B->q_full[i], (qn[i] - 1) & 1) && global_ns() - t0 < kWaitLimitNs) {
+            }
     }
     tc_before();
     __syncthreads();

@@ -169,6 +169,8 @@ static int check_group(int H, int KV, int hd) {
     return SLM_OK;
 }
 
+static std::atomic<int> g_lost{0};  // slm_debug_rows_faults
+
 // The part that both attention calls share: workspace, kernel, join.
 static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long longest, void *ws, size_t ws_bytes,
                          cudaStream_t s) {
@@ -181,6 +183,7 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     // Items of a few blocks stay whole: a block takes about 1 us, the joining launch 3.
     a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
+    a.lost = g_lost.load(std::memory_order_relaxed);
     a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)a.hd));
     const bool bf16 = dtype == SLM_BF16;
     if (a.rows == 1) {  // one row: its stride has no meaning
@@ -347,4 +350,10 @@ extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t
     a.status = status;
     return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows,
                          workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int slm_debug_rows_faults(int32_t lost) {
+    if (lost < 0 || lost > 2) return attn_fail(SLM_EINVAL, "lost %d outside [0, 2]", lost);
+    g_lost.store(lost);
+    return SLM_OK;
 }
