@@ -1,5 +1,5 @@
-"""The sizes at the ends of what the packed-row calls take: no row at all, and a workspace that
-is kept for the largest batch."""
+"""The sizes at the ends of what the packed-row calls take: no row at all, the most sequences, and a
+workspace that is kept for the largest batch."""
 import itertools
 
 import pytest
@@ -56,3 +56,15 @@ def test_one_workspace_for_a_shrinking_batch(slm, dtype):  # noqa: F811
 def test_workspace_of_more_rows_than_a_call_takes_is_zero(slm):  # noqa: F811
     assert slm.attention_rows_workspace_bytes(BF16, 1 << 30, 4, 4, 2, 64) > 0
     assert slm.attention_rows_workspace_bytes(BF16, (1 << 30) + 1, 4, 4, 2, 64) == 0
+
+
+@pytest.mark.parametrize("dtype,hd", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 64), (F32, 128), (F32, 256)])
+@pytest.mark.parametrize("new", [[1] * 1024, [(3, 0, 40, 1)[i % 4] for i in range(1024)]])
+def test_the_most_sequences(slm, dtype, hd, new):  # noqa: F811
+    """1,024 sequences, whose lengths leave the least shared memory to the kernels (the shallowest
+    rings): single tokens, and chunks on the wide tiles."""
+    b = Batch(dtype, 4, 2, hd, new, [(i * 37) % 200 for i in range(1024)], 16, seed=61)
+    b.fill([n + c for n, c in zip(b.new, b.ctx)])
+    out = b.out()
+    slm.attention_paged(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, b.workspace(slm), b.status)
+    check_attention(b, out, b.seq_k, b.seq_v, dtype)
