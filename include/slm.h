@@ -428,7 +428,7 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
  *   SLM_ROWS_LENGTH   row_start does not ascend within [0, rows], a ctx_len is negative, or a
  *                     position lies outside the page table (or the rotation table): an append
  *                     writes nothing for such a row; an attention gives meaningless results
- *                     for that sequence.
+ *                     for that sequence (and, where row ranges overlap, for the others of a row).
  * No call reads or writes outside its buffers because of a length or a page id.
  *
  * Requirements of all three: nseq in [1, 1024]; rows at most 2^30; n_heads % n_kv_heads == 0, at
@@ -438,8 +438,8 @@ int slm_attention_decode_noalloc(int32_t batch, int32_t n_heads, int32_t n_kv_he
  * projection's output; heads of a row are adjacent.  rows = 0 is allowed and does nothing (q, k, v
  * and out may be NULL then).  Every pointer but the structs themselves is device memory of the
  * current device (checked).  The calls are asynchronous on `stream`, allocate nothing and may be
- * captured; calls from several host threads may overlap.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED, SLM_ECUDA; the text is
- * in slm_last_error(NULL).
+ * captured; calls from several host threads may overlap.  Errors: SLM_EINVAL, SLM_EUNSUPPORTED,
+ * SLM_ECUDA; the text is in slm_last_error(NULL).
  */
 typedef struct {
     void *k, *v;                /* device [n_pages][n_kv_heads][page_size][head_dim] of kv_dtype   */
@@ -495,7 +495,8 @@ size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t n
  * head h, with kv head g = h / (n_heads / n_kv_heads),
  *     out[row][h] = sum_t softmax_t(q[row][h] . k[s][g][t] / sqrt(head_dim)) v[s][g][t],  t = 0..p.
  * One new row per sequence is a decode step; many are a chunk of a prompt; a batch may mix both.
- *   q, out: [rows][n_heads][head_dim] of the cache's type.  q as given (already rotated).
+ *   q, out: [rows][n_heads][head_dim] of the cache's type.  q as given (already rotated).  out
+ *     overlaps none of the inputs.
  *   n_heads / n_kv_heads at most 64 (32 for head_dim > 128), else SLM_EUNSUPPORTED.
  *   workspace: device memory, 256-byte aligned, of slm_attention_rows_workspace_bytes(kv_dtype,
  *     rows, nseq, ...) bytes.  It needs no initialisation and carries nothing from call to call;
@@ -505,9 +506,10 @@ size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows, int32_t n
  *   where the softmax weights are rounded to bf16 before they multiply v; every other shape is
  *   fp32 throughout.  The same call with the same inputs gives the same bits.
  *   Keys and values that no row of a call sees (cache slots past a sequence's last position,
- *   other sequences' pages) may hold anything, infinities and NaN included.  Non-finite values
- *   at a position that some rows see and earlier rows of the same sequence do not may reach those
- *   earlier rows.
+ *   other sequences' pages) may hold anything, infinities and NaN included.  A NaN score makes its
+ *   row NaN, and a score of -infinity has the weight 0, however the work is divided.  Non-finite
+ *   values (v) at a position that some rows see and earlier rows of the same sequence do not may
+ *   reach those earlier rows: their weight of 0 is multiplied with them.
  */
 int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q, int64_t q_ld,
                         void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,

@@ -12,8 +12,8 @@
 // a thread's accesses are 16 bytes wide (8 for bf16 heads of 8 mod 16) and a warp's are
 // contiguous.  A CTA first resolves its rows -- owner by counting the sequences that end at or
 // before the row, position, page -- one warp per row, then all its threads share the units.
-// 8,000 rows of 48 heads of 64, fp32 to bf16: 30.6 us = 6.0 TB/s, 88% of the copy rate; one row
-// 2.5 us, which is the chain of lookups.
+// 8,000 rows of 48 heads of 64, fp32 to bf16: 30.7 us = 6.0 TB/s, 88% of the copy rate, in a captured
+// graph, 31.5 us through the binding; one row 2.5 us, which is the chain of lookups.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

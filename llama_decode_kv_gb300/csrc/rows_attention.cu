@@ -533,7 +533,9 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
 // go out through shared memory as whole rows.  Pieces are added in order, so the result does not
 // depend on timing.  With kJoinShared pieces or more (a long context over the whole GPU, few rows)
 // the eight warps of a block share the pieces of 32 quads instead and add up in shared memory.
-// 6 to 10 us a launch, two or three dependent reads of L2 long.
+// Two or three dependent reads of L2 long: 2 to 3 us more for a short call (its launch overlaps the
+// attention's); alone under the profiler, caches cold, 6 to 10 us, and 16 where 150 items of 250 rows
+// of 128 are joined.
 constexpr int kJoinShared = 12;
 
 template <typename T> __device__ __forceinline__ void store4(T *p, float4 v);

@@ -12,10 +12,16 @@
 // 128-position blocks (rows_plan.h), one persistent CTA per SM; pieces of items leave as partial
 // states for rows_join_kernel.
 //
-// Long prompts and chunks are bound by the tensor core: prompts of 8,192 and fewer tokens, 32 / 8
-// heads of 128, 364 us = 1.55 PFLOP/s, 83% of cuBLAS's rate (tensor pipe 64% busy by its counter).
-// Decode steps are bound by HBM: 64 sequences of up to 8,000 positions 164 us = 6.3 TB/s, 94% of
-// the copy rate.  Short calls are bound by one dependent chain: one token over 262 positions 8 us.
+// Long prompts and chunks are bound by the chain S, softmax, P V of a tile, which two tiles do not
+// hide altogether: prompts of 8,192 and fewer tokens, 32 / 8 heads of 128, 366 us = 1.54 PFLOP/s in a
+// short run (82% of cuBLAS's burst rate; tensor pipe 64% busy by its counter) and 396 us = 1.42 back to
+// back under the power cap (85% of its sustained rate).  64-wide heads take nearly the same chain for
+// half the operations: 2,048 tokens 35 us = 0.49 PFLOP/s.  Decode steps are bound by HBM: 64 sequences
+// of up to 8,000 positions 164 us = 6.3 TB/s, 94% of the copy rate.  Short calls are bound by one
+// dependent chain: one token over 262 positions 8.5 us.
+//
+// Heads of 72 to 112 run as 128-wide ones in P V and in shared memory (their S leaves the missing
+// columns out), so up to 44% of their P V and of their ring is padding.
 //
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
 //                   causal mask where the block needs one, the running maximum, P = 2^(S - m) as
@@ -801,7 +807,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
 // ------------------------------------------------------------------ host side
 
 static int tc_stages(int hd, int nseq) {
-    // as many ring stages as fit beside the batch's lengths (1,024 sequences: 20 KB)
+    // ring stages: up to 10 of 16 KB or 5 of 32 KB, fewer where the batch's lengths need the room (1,024
+    // sequences: 20 KB)
     const int HDP = hd <= 64 ? 64 : 128;
     int n = HDP == 64 ? 10 : 5;
     while (tc_fixed_bytes(HDP, n) + (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 > kSmemLimit) n--;

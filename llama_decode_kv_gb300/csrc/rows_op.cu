@@ -139,7 +139,9 @@ static RowsTiling rows_tiling(int sms, int dtype, int rows, int nseq, int H, int
     const int G = H / KV;
     if (on_tensor_cores(dtype, hd)) {
         // An item's start and end take about as long as one block of 64-wide heads and two of 128-wide
-        // ones (8,192-token prompts, 128: 381 us at 1, 364 at 2; 16 x 512, 64: 24 us at 1, 29 at 2).
+        // ones.  At 1 / 2: prompts of 8,192 tokens, 128: 380 / 367 us; chunks of 512 over 16,000, 128:
+        // 216.2 / 215.6; decode of 64 sequences, 128: 163.2 / 164.4; prompts 16 x 512, 64: 24.0 / 29.7;
+        // 2,048, 64: 35.1 / 35.3; decode of 4 x 32,768, 64: 53.3 / 53.1.
         t.geom = {KV, 2 * (128 / G), 7, 1, hd <= 64 ? 1 : 2};
         t.P = sms;
     } else {
@@ -180,7 +182,13 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     a.P = t.P;
     a.slot_rows = t.slot_rows;
     a.geom = t.geom;
-    // Items of a few blocks stay whole: a block takes about 1 us, the joining launch 3.
+    // Items of a few blocks stay whole: cutting and joining them costs a short call 2 to 3 us, a block
+    // about 1 us.  Whole / cut, bf16, tables of two blocks: one token, 9 / 3 heads of 64, 7.1 / 8.9 us,
+    // 16 sequences 8.2 / 11.2; 32 / 8 heads of 128: 8.4 / 9.5 and 9.5 / 11.3; of four blocks 9.0 / 9.6,
+    // 9.9 / 11.8, 11.2 / 9.8 and 12.0 / 13.9; of eight 12.9 / 10.2, 13.8 / 13.1, 17.2 / 11.0 and 18.3 /
+    // 21.2.  `longest` is what the caller's table (for prompts: the packed rows) could hold, since the
+    // lengths are not known here: a short context under a wide table is cut all the same (one token
+    // over 250 positions, table for 32,768: 9.1 us).
     a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
     a.lost = g_lost.load(std::memory_order_relaxed);
