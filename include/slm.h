@@ -458,7 +458,7 @@ typedef struct {
     int32_t nseq, rows;         /* rows: packed rows that the buffers hold (>= row_start[nseq])    */
 } slm_rows;
 
-enum { SLM_ROWS_TIMEOUT = 1, SLM_ROWS_PAGE = 2, SLM_ROWS_LENGTH = 4 };
+enum { SLM_ROWS_TIMEOUT = 1, SLM_ROWS_PAGE = 2, SLM_ROWS_LENGTH = 4, SLM_ROWS_POOL = 8 };
 
 /*
  * slm_kv_append -- write the keys and values of the packed rows into the cache, position
@@ -525,6 +525,136 @@ int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, i
                          const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
                          void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
                          void *stream);
+
+/*
+ * The calls below complete a serving step around the three above (continuous batching, as there):
+ * what a step's lengths and page tables are, rotation by positions that are not cache positions,
+ * scores that are capped, biased or masked, and the next tokens.  Their conventions are the same:
+ * device pointers of the current device (checked), asynchronous on `stream`, nothing allocated, may
+ * be captured and called from several host threads, device data checked by the kernels.
+ */
+
+/*
+ * slm_rows_plan -- the row ranges, page table and slots of one step, from what every sequence
+ * brings.  new_len[s] >= 0: so many rows after its seq_len[s] cached positions; new_len[s] < 0: the
+ * sequence ends, its place is empty afterwards and its pages are free.
+ *
+ * Free pages are a stack: free_pages[0 .. free_count - 1], the top last.  The pages of ended
+ * sequences (page_table[s][0 .. ceil(seq_len[s] / page_size) - 1]) are put on it in the order
+ * (sequence, block); then the pages of the new blocks of positions, ceil(seq_len / page_size) to
+ * ceil((seq_len + new_len) / page_size) - 1 of every other sequence, are taken from its top in the
+ * same order and written into page_table.  Every page belongs to one sequence.  No other entry of
+ * page_table is written, an ended sequence's neither.
+ *
+ *   row_start [nseq + 1], ctx_len [nseq]   what slm_rows takes: row_start from 0, ctx_len = seq_len
+ *                                          (0 where the sequence ends)
+ *   positions [rows], slots [rows]         each packed row's position, and where the cache holds it:
+ *                                          page * page_size + position % page_size; both -1 for rows
+ *                                          of no sequence.  Either may be NULL.
+ *   seq_len_out [nseq], free_count_out [1] after the step: seq_len + new_len (0: ended), free pages.
+ *                                          They may be seq_len and free_count themselves, so that a
+ *                                          captured step goes on from replay to replay; other outputs
+ *                                          and inputs do not overlap.
+ *
+ * If something does not fit, the step has no rows: row_start is all 0, ctx_len and seq_len_out are
+ * seq_len, free_count_out is free_count, positions and slots are -1 and nothing else is written.
+ * status says why: SLM_ROWS_POOL (too few free pages, or more than n_pages of them), SLM_ROWS_LENGTH
+ * (a seq_len is negative, a sequence outgrows its page table or 2^31 - 256 positions, or there are
+ * more rows than `rows`).
+ * A page id outside [0, n_pages) sets SLM_ROWS_PAGE, is passed on as it is, and its slots are -1.
+ * nseq in [1, 1024], rows in [0, 2^30], table_ld and n_pages at least 1, page_size a power of two in
+ * [16, 2^20].
+ */
+typedef struct {
+    int32_t *page_table;        /* device int32 [nseq][table_ld]                                   */
+    int32_t *free_pages;        /* device int32 [n_pages]                                          */
+    const int32_t *free_count;  /* device int32 [1]                                                */
+    const int32_t *seq_len;     /* device int32 [nseq]: cached positions                           */
+    int32_t nseq, table_ld, n_pages, page_size;
+} slm_page_pool;
+
+int slm_rows_plan(const slm_page_pool *pool, const int32_t *new_len, int32_t rows, int32_t *row_start, int32_t *ctx_len,
+                  int32_t *positions, int64_t *slots, int32_t *seq_len_out, int32_t *free_count_out, int32_t *status,
+                  void *stream);
+
+/*
+ * slm_kv_append_axes -- slm_kv_append with positions of several axes (time, height and width of an
+ * image's or a video's patches): the rows go to the same places of the cache, and pair j of a row
+ * is turned by rope[positions[axis_of_pair[j]][row]][j].
+ *   n_axes: 1 to 8.  positions: device int32 [n_axes][positions_ld], an entry per packed row;
+ *     positions_ld at least rows.  A position of an axis outside [0, rope_len) sets SLM_ROWS_LENGTH
+ *     and nothing is written for the row (rows of no sequence are not looked at).
+ *   axis_of_pair: host int8 [head_dim / 2], each the axis of a pair, or -1: it is not turned.  So
+ *     contiguous sections, axes in turns and rotations of a part of the head are all tables of this
+ *     call.  It is read before the call returns.
+ *   rope: not NULL; the other arguments as for slm_kv_append.
+ */
+int slm_kv_append_axes(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
+                       const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_axes,
+                       const int8_t *axis_of_pair, const int32_t *positions, int64_t positions_ld, int32_t n_heads,
+                       const void *q, int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status, void *stream);
+
+/*
+ * slm_attention_paged_scored, slm_attention_prompt_scored -- slm_attention_paged and
+ * slm_attention_prompt with other scores and masks.  For a row at position p of sequence s, of L
+ * positions with the row's own step, and query head h:
+ *     x_t = scale q . k_t;   with a cap: x_t = cap tanh(x_t / cap);   with slopes: x_t -= slopes[h] |p - t|
+ *     out = sum_t softmax_t(x_t) v_t over the t with  from <= t < to,
+ *     from = max(first[row], p + 1 - window, 0),  to = max(p + 1, min(prefix_len[s], L)).
+ * A row that sees nothing (from >= to) gets zeros.
+ *   first is what a document mask is made of: the position of the row's document's first token.  It
+ *     must not descend within a sequence (else SLM_ROWS_LENGTH and that sequence's results are
+ *     meaningless).  first[row] > p without a prefix: the row sees nothing.
+ *   prefix_len: positions that all rows of the sequence see, also those before them (a negative one
+ *     counts as 0).
+ *   window: positions that a row sees at most, its own the last of them.
+ * Where row_start descends (SLM_ROWS_LENGTH), the results of the whole call are meaningless.
+ * Positions before the smallest `from` of a sequence's rows are not read, nor are their page-table
+ * entries: their pages may have been given back.  The other arguments, the requirements, the
+ * workspace and the rounding are those of slm_attention_paged and slm_attention_prompt; non-finite
+ * values at positions that some rows of a sequence see may reach its other rows that see something.
+ * The scores stay fp32, the cap's tanh included.
+ */
+typedef struct {
+    float scale;                /* > 0 and finite; 0: 1 / sqrt(head_dim)                            */
+    float cap;                  /* > 0 and finite; 0: none                                          */
+    const float *slopes;        /* device fp32 [n_heads]; NULL: none                                */
+    const int32_t *prefix_len;  /* device int32 [nseq]; NULL: none                                  */
+    const int32_t *first;       /* device int32 [rows]; NULL: 0                                     */
+    int32_t window;             /* >= 1; 0: none                                                    */
+} slm_scores;
+
+int slm_attention_paged_scored(const slm_kv_cache *cache, const slm_rows *rows, const slm_scores *scores, int32_t n_heads,
+                               const void *q, int64_t q_ld, void *out, int64_t out_ld, void *workspace,
+                               size_t workspace_bytes, int32_t *status, void *stream);
+int slm_attention_prompt_scored(const slm_rows *rows, const slm_scores *scores, int32_t dtype, int32_t n_heads,
+                                int32_t n_kv_heads, int32_t head_dim, const void *q, int64_t q_ld, const void *k,
+                                int64_t k_ld, const void *v, int64_t v_ld, void *out, int64_t out_ld, void *workspace,
+                                size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * slm_sample_rows -- the next token of every row of logits, each with parameters of its own.  A
+ * row's tokens in the order (logit descending, index ascending) are cut to the first top_k, then to
+ * their shortest prefix whose probability (softmax(logit / temperature) over what the first cut
+ * left) reaches top_p, then to those of at least min_p times the first one's probability.  The draw
+ * goes over what is left in index order: the first token whose running sum of probabilities exceeds
+ * uniform times their sum.
+ *   dtype: SLM_F32 or SLM_BF16, the type of logits [rows][ld], device, ld at least vocab (no
+ *     alignment beyond the type's) or 0: all rows draw from the same logits.  vocab in [1, 2^22].  NaN counts as -infinity; a row with no
+ *     other logit gives token 0; where the largest is +infinity, only its equals have probability.
+ *   Device arrays [rows], NULL: the default for every row.  Any value has a meaning:
+ *     temperature  fp32, default 1; not above 0 (or NaN): the first token of the order
+ *     top_k        int32, default 0; not above 0: no cut
+ *     top_p        fp32, default 1; at least 1 (or NaN): no cut; not above 0: the first token
+ *     min_p        fp32, default 0; not above 0 (or NaN): no cut; above 1 counts as 1
+ *   uniforms: device fp32 [rows], in [0, 1) (cut to it; NaN counts as 0).  next_ids: device int32
+ *     [rows].
+ *   Probabilities are added up as whole numbers of 2^-40 of the largest, so the result does not
+ *   depend on the order of the additions.  rows = 0 does nothing.
+ */
+int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const void *logits, int64_t ld, const float *temperature,
+                    const int32_t *top_k, const float *top_p, const float *min_p, const float *uniforms,
+                    int32_t *next_ids, void *stream);
 
 /*
  * slm_debug_rows_faults -- test hook for the abandoned calls of the tensor-core attention (no page

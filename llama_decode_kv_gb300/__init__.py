@@ -53,7 +53,17 @@ class slm_rows(ctypes.Structure):
                 ("rows", ctypes.c_int32)]
 
 
-SLM_ROWS_TIMEOUT, SLM_ROWS_PAGE, SLM_ROWS_LENGTH = 1, 2, 4
+class slm_page_pool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("page_table", "free_pages", "free_count", "seq_len")] + \
+               [(n, ctypes.c_int32) for n in ("nseq", "table_ld", "n_pages", "page_size")]
+
+
+class slm_scores(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("first", ctypes.c_void_p), ("window", ctypes.c_int32)]
+
+
+SLM_ROWS_TIMEOUT, SLM_ROWS_PAGE, SLM_ROWS_LENGTH, SLM_ROWS_POOL = 1, 2, 4, 8
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -92,6 +102,13 @@ _SIGS = {
     "slm_attention_paged": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
     "slm_attention_prompt": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
                                             ctypes.c_size_t, _P, _P]),
+    "slm_rows_plan": (ctypes.c_int, [_P, _P, _I32] + [_P] * 8),
+    "slm_kv_append_axes": (ctypes.c_int, [_P, _P, _I32, _P, _I64, _P, _I64, _P, _I32, _I32, _P, _P, _I64, _I32, _P, _I64,
+                                          _P, _I64, _P, _P]),
+    "slm_attention_paged_scored": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I64, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "slm_attention_prompt_scored": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                                   _P, ctypes.c_size_t, _P, _P]),
+    "slm_sample_rows": (ctypes.c_int, [_I32, _I32, _I32, _P, _I64] + [_P] * 7),
     "slm_debug_rows_faults": (ctypes.c_int, [_I32]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -162,16 +179,18 @@ def attention_decode_noalloc(q, k_cache, v_cache, ctx_len, out, kv_dtype: int, s
 
 _PACK_CACHE = struct.Struct("PPPiiiiii").pack
 _PACK_ROWS = struct.Struct("PPii").pack
-_F32 = _BF16 = _INT = _raw_stream = None  # torch's types and the current stream of a device number
+_PACK_POOL = struct.Struct("PPPPiiii").pack
+_PACK_SCORES = struct.Struct("ffPPPi").pack
+_F32 = _BF16 = _INT = _I64T = _raw_stream = None  # torch's types and the current stream of a device number
 
 
 def _torch_names():
     """Look the names up (torch is not imported before it is needed)."""
-    global _F32, _BF16, _INT, _raw_stream
+    global _F32, _BF16, _INT, _I64T, _raw_stream
     import torch
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda d: torch.cuda.current_stream(d).cuda_stream)
-    _F32, _BF16, _INT = torch.float32, torch.bfloat16, torch.int32
+    _F32, _BF16, _INT, _I64T = torch.float32, torch.bfloat16, torch.int32, torch.int64
 
 
 def _dtype_code(t) -> int:
@@ -228,13 +247,8 @@ def _rows_stream(stream, x):
     return _raw_stream(dev) if stream is None and dev >= 0 else _stream_ptr(stream)
 
 
-def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, rope=None, q=None, q_out=None,
-              stream=None) -> None:
-    """slm_kv_append over torch tensors of the current device: write the packed rows k, v
-    [rows][kv heads][head_dim] into the paged cache [pages][kv heads][page size][head_dim] at
-    positions ctx_len[s] + i (ctx_len None: from 0), rotated by rope [positions][head_dim / 2][2]
-    when given; q [rows][heads][head_dim] is rotated into q_out (the cache's type).  Row strides
-    are free.  status: int32[1] collecting SLM_ROWS_* bits.  Raises SlmError / ValueError."""
+def _append_args(k, v, k_cache, v_cache, page_table, row_start, ctx_len, rope, q, q_out):
+    """What the two appends share: (cache, rows, dtype, k, k_ld, v, v_ld, rope, n_rope), (heads, q, q_ld, q_out, q_out_ld)."""
     shape, dt = k.shape, k.dtype
     code = _dtype_code(dt)
     rows, kv, hd = shape
@@ -260,10 +274,69 @@ def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, ro
             raise ValueError(f"q: {tuple(qs)}, expected ({rows}, heads, {hd})")
         q_ld, o_ld = _heads(q, "q", qs, dt), _heads(q_out, "q_out", qs, k_cache.dtype)
         q_ptr, o_ptr = q.data_ptr(), q_out.data_ptr()
-    rc = slm_kv_append(c, r, code, k.data_ptr(), k_ld, v.data_ptr(), v_ld, rope_ptr, n_rope, heads, q_ptr, q_ld, o_ptr,
-                       o_ld, _ints(status, "status", 1), _rows_stream(stream, k))
+    return (c, r, code, k.data_ptr(), k_ld, v.data_ptr(), v_ld, rope_ptr, n_rope), (heads, q_ptr, q_ld, o_ptr, o_ld)
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, rope=None, q=None, q_out=None,
+              stream=None) -> None:
+    """slm_kv_append over torch tensors of the current device: write the packed rows k, v
+    [rows][kv heads][head_dim] into the paged cache [pages][kv heads][page size][head_dim] at
+    positions ctx_len[s] + i (ctx_len None: from 0), rotated by rope [positions][head_dim / 2][2]
+    when given; q [rows][heads][head_dim] is rotated into q_out (the cache's type).  Row strides
+    are free.  status: int32[1] collecting SLM_ROWS_* bits.  Raises SlmError / ValueError."""
+    a, b = _append_args(k, v, k_cache, v_cache, page_table, row_start, ctx_len, rope, q, q_out)
+    rc = slm_kv_append(*a, *b, _ints(status, "status", 1), _rows_stream(stream, k))
     if rc:
         raise SlmError(rc, "slm_kv_append", slm_last_error(None).decode())
+
+
+def kv_append_axes(k, v, k_cache, v_cache, page_table, row_start, ctx_len, status, rope, axis_of_pair, positions, q=None,
+                   q_out=None, stream=None) -> None:
+    """slm_kv_append_axes over torch tensors of the current device: kv_append whose pair j of a row
+    turns by rope[positions[axis_of_pair[j]][row]][j].  positions: int32 [axes][rows], rows of it at
+    any stride; axis_of_pair: head_dim / 2 whole numbers, -1 for a pair that is not turned.
+    Raises SlmError / ValueError."""
+    if rope is None:
+        raise ValueError("rope is needed")
+    a, b = _append_args(k, v, k_cache, v_cache, page_table, row_start, ctx_len, rope, q, q_out)
+    axes, rows = positions.shape
+    ld, one = positions.stride()
+    if positions.dtype is not _INT or rows != k.shape[0] or (one != 1 and rows > 1):
+        raise ValueError(f"positions: {tuple(positions.shape)} {positions.dtype} (strides {positions.stride()}), expected int32 "
+                         f"[axes][{k.shape[0]}], adjacent in a row")
+    try:
+        pairs = struct.pack(f"{k.shape[2] // 2}b", *axis_of_pair)
+    except struct.error as e:
+        raise ValueError(f"axis_of_pair: {k.shape[2] // 2} axes expected ({e})") from None
+    rc = slm_kv_append_axes(*a, axes, pairs, positions.data_ptr(), ld if axes > 1 else rows, *b, _ints(status, "status", 1),
+                            _rows_stream(stream, k))
+    if rc:
+        raise SlmError(rc, "slm_kv_append_axes", slm_last_error(None).decode())
+
+
+def rows_plan(new_len, seq_len, page_table, page_size, free_pages, free_count, row_start, ctx_len, positions, slots,
+              seq_len_out, free_count_out, status, stream=None) -> None:
+    """slm_rows_plan over torch tensors of the current device: row_start [sequences + 1], ctx_len,
+    positions [rows], slots [rows] (int64) of a step that brings new_len[s] rows after seq_len[s]
+    positions (negative: the sequence ends), page_table [sequences][entries] with the new pages,
+    taken from the stack free_pages [pages] of free_count[0] entries; seq_len_out and
+    free_count_out after the step (they may be seq_len and free_count).  All int32 but slots.
+    Raises SlmError / ValueError."""
+    if _INT is None:
+        _torch_names()
+    nseq, ld = page_table.shape
+    rows = positions.shape[0]
+    if slots.dtype is not _I64T or slots.shape != (rows,) or not slots.is_contiguous():
+        raise ValueError(f"slots: {tuple(slots.shape)} {slots.dtype}, expected contiguous int64 ({rows},)")
+    n_pages = free_pages.shape[0]
+    pool = _PACK_POOL(_ints(page_table, "page_table", nseq, ld), _ints(free_pages, "free_pages", n_pages),
+                      _ints(free_count, "free_count", 1), _ints(seq_len, "seq_len", nseq), nseq, ld, n_pages, page_size)
+    rc = slm_rows_plan(pool, _ints(new_len, "new_len", nseq), rows, _ints(row_start, "row_start", nseq + 1),
+                       _ints(ctx_len, "ctx_len", nseq), _ints(positions, "positions", rows), slots.data_ptr(),
+                       _ints(seq_len_out, "seq_len_out", nseq), _ints(free_count_out, "free_count_out", 1),
+                       _ints(status, "status", 1), _rows_stream(stream, new_len))
+    if rc:
+        raise SlmError(rc, "slm_rows_plan", slm_last_error(None).decode())
 
 
 def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -272,11 +345,8 @@ def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_
     return int(slm_attention_rows_workspace_bytes(_dtype_code(dtype), rows, nseq, n_heads, n_kv_heads, head_dim))
 
 
-def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream=None) -> None:
-    """slm_attention_paged over torch tensors of the current device: out[row][h] = attention of
-    the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
-    already holds the rows' own keys and values).  workspace: uint8 tensor of
-    attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
+def _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream):
+    """(cache, rows), what follows them in a paged attention call, and the sequences."""
     shape, dt = q.shape, k_cache.dtype
     rows, heads, hd = shape
     nseq = page_table.shape[0]
@@ -286,16 +356,12 @@ def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, wo
     r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
                    0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
-    rc = slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace),
-                             _ints(status, "status", 1), _rows_stream(stream, q))
-    if rc:
-        raise SlmError(rc, "slm_attention_paged", slm_last_error(None).decode())
+    return (c, r), (heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace), _ints(status, "status", 1),
+                    _rows_stream(stream, q)), nseq
 
 
-def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) -> None:
-    """slm_attention_prompt over torch tensors of the current device: causal attention of the
-    packed prompts q [rows][heads][head_dim], k, v [rows][kv heads][head_dim] into out.
-    Raises SlmError / ValueError."""
+def _prompt_args(q, k, v, row_start, out, workspace, status, stream):
+    """rows, what follows them in a prompt attention call, and the sequences."""
     shape, ks, dt = q.shape, k.shape, q.dtype
     rows, heads, hd = shape
     if ks[0] != rows or ks[2] != hd:
@@ -304,11 +370,86 @@ def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) ->
     r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1), 0, nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
     k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
-    rc = slm_attention_prompt(r, code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
-                              out.data_ptr(), o_ld, *_workspace(workspace), _ints(status, "status", 1),
-                              _rows_stream(stream, q))
+    return r, (code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(), o_ld,
+               *_workspace(workspace), _ints(status, "status", 1), _rows_stream(stream, q)), nseq
+
+
+def _scores(scale, cap, slopes, window, prefix_len, first, rows: int, heads: int, nseq: int) -> bytes:
+    """The slm_scores of a call."""
+    if slopes is not None and (slopes.dtype is not _F32 or slopes.shape != (heads,) or not slopes.is_contiguous()):
+        raise ValueError(f"slopes: {tuple(slopes.shape)} {slopes.dtype}, expected contiguous float32 ({heads},)")
+    return _PACK_SCORES(scale, cap, 0 if slopes is None else slopes.data_ptr(),
+                        0 if prefix_len is None else _ints(prefix_len, "prefix_len", nseq),
+                        0 if first is None else _ints(first, "first", rows), window)
+
+
+def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream=None) -> None:
+    """slm_attention_paged over torch tensors of the current device: out[row][h] = attention of
+    the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
+    already holds the rows' own keys and values).  workspace: uint8 tensor of
+    attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
+    a, b, _ = _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream)
+    rc = slm_attention_paged(*a, *b)
+    if rc:
+        raise SlmError(rc, "slm_attention_paged", slm_last_error(None).decode())
+
+
+def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) -> None:
+    """slm_attention_prompt over torch tensors of the current device: causal attention of the
+    packed prompts q [rows][heads][head_dim], k, v [rows][kv heads][head_dim] into out.
+    Raises SlmError / ValueError."""
+    r, b, _ = _prompt_args(q, k, v, row_start, out, workspace, status, stream)
+    rc = slm_attention_prompt(r, *b)
     if rc:
         raise SlmError(rc, "slm_attention_prompt", slm_last_error(None).decode())
+
+
+def attention_paged_scored(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, *, scale=0.0,
+                           cap=0.0, slopes=None, window=0, prefix_len=None, first=None, stream=None) -> None:
+    """slm_attention_paged_scored over torch tensors of the current device: attention_paged with
+    scores cap tanh(scale q.k / cap) - slopes[h] |p - t| over the positions from max(first[row],
+    p + 1 - window) on, up to p or prefix_len[s] - 1, whichever is later (scale 0: 1 / sqrt(head_dim);
+    cap 0, window 0, None: without).  slopes: float32 [heads]; prefix_len: int32 [sequences]; first:
+    int32 [rows].  Rows that see nothing get zeros.  Raises SlmError / ValueError."""
+    a, b, nseq = _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream)
+    rc = slm_attention_paged_scored(*a, _scores(scale, cap, slopes, window, prefix_len, first, q.shape[0], b[0], nseq), *b)
+    if rc:
+        raise SlmError(rc, "slm_attention_paged_scored", slm_last_error(None).decode())
+
+
+def attention_prompt_scored(q, k, v, row_start, out, workspace, status, *, scale=0.0, cap=0.0, slopes=None, window=0,
+                            prefix_len=None, first=None, stream=None) -> None:
+    """slm_attention_prompt_scored over torch tensors of the current device: attention_prompt with
+    the scores and masks of attention_paged_scored.  Raises SlmError / ValueError."""
+    r, b, nseq = _prompt_args(q, k, v, row_start, out, workspace, status, stream)
+    rc = slm_attention_prompt_scored(r, _scores(scale, cap, slopes, window, prefix_len, first, q.shape[0], b[1], nseq), *b)
+    if rc:
+        raise SlmError(rc, "slm_attention_prompt_scored", slm_last_error(None).decode())
+
+
+def sample_rows(logits, temperature, top_k, top_p, min_p, uniforms, next_ids, stream=None) -> None:
+    """slm_sample_rows over torch tensors of the current device: the next token of every row of
+    logits [rows][vocab] (float32 or bfloat16, rows at any stride) into next_ids [rows] (int32), with
+    the row's temperature, top_p, min_p (float32 [rows]) and top_k (int32 [rows]), each of them None
+    for the default, and its uniform variate (float32 [rows]).  Raises SlmError / ValueError."""
+    code = _dtype_code(logits.dtype)
+    rows, vocab = logits.shape
+    ld, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError(f"logits: a row's logits must be adjacent (strides {logits.stride()})")
+    ptrs = []
+    for x, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p"), (uniforms, "uniforms")):
+        if x is None and name != "uniforms":
+            ptrs.append(None)
+            continue
+        if x is None or x.dtype is not _F32 or x.shape != (rows,) or not x.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous float32 ({rows},)")
+        ptrs.append(x.data_ptr())
+    rc = slm_sample_rows(rows, vocab, code, logits.data_ptr(), ld, ptrs[0],
+                         None if top_k is None else _ints(top_k, "top_k", rows), ptrs[1], ptrs[2], ptrs[3],
+                         _ints(next_ids, "next_ids", rows), _rows_stream(stream, logits))
+    if rc:
+        raise SlmError(rc, "slm_sample_rows", slm_last_error(None).decode())
 
 
 def sample(logits, temperature: float, top_k: int, top_p: float, uniforms, next_ids, stream=None) -> int:

@@ -19,6 +19,15 @@ struct RowsKv {
     long long k_ld, v_ld;  // packed rows: elements from one row to the next
 };
 
+// Scores and masks besides the plain causal ones (slm_scores); all null and zero: those.
+struct RowsScores {
+    const float *slopes;         // [H]
+    const int *prefix, *first;   // [nseq], [rows]
+    int window;
+    float cap_in, cap_log2;      // scale / cap, cap log2(e)
+    float scale;                 // of q . k
+};
+
 struct RowsArgs {
     const int *row_start, *ctx_len;  // ctx_len null: no cached positions
     int nseq, rows;
@@ -29,7 +38,8 @@ struct RowsArgs {
     long long q_ld, out_ld;          // elements
     RowsKv kv;
     int *status;
-    float scale_log2;                // log2(e) / sqrt(hd)
+    float scale_log2;                // log2(e) / sqrt(hd), or log2(e) times the caller's scale
+    RowsScores sc;
     // partial states (rows_ws_bytes); P = CTAs of the attention launch
     uint8_t *ws;
     int P, slot_rows;
@@ -85,6 +95,145 @@ __device__ __forceinline__ void rows_layout(const RowsArgs &A, SeqRows *seq, lon
     __syncthreads();
 }
 
+// Masked items: the mask of sequence s; `prefix` stands in shared memory, cut to the sequence.
+struct SeqMasks {
+    const SeqRows *seq;
+    const int *prefix, *first;
+    int window;
+    __device__ __forceinline__ RowsMask operator()(int s) const {
+        return RowsMask{first ? first + seq[s].row0 : nullptr, prefix[s], window};
+    }
+};
+typedef MaskedWalk<SeqMasks> RowsMaskedWalk;
+
+// Shared memory that masked_layout takes after seq and wstart.
+struct MaskedShared {
+    RowsStart start;
+    int sums[1];  // prefix[nseq], items before each sequence [nseq + 1]
+};
+__host__ __device__ inline size_t masked_bytes(int nseq) { return (sizeof(RowsStart) + (2 * (size_t)nseq + 1) * 4 + 15) / 16 * 16; }
+
+// rows_layout for masked items: their units are added up one by one, an equal share of them per
+// thread (8,192 rows of 4 heads per kv head are 128 items), and warp 0 looks for the item that this
+// CTA's range begins in.  Ends with a __syncthreads().
+__device__ __forceinline__ void masked_layout(const RowsArgs &A, SeqRows *seq, long long *wstart, MaskedShared *ms,
+                                              RowsMaskedWalk &w, int tid, int threads) {
+    int *prefix = ms->sums, *items = ms->sums + A.nseq;
+    for (int s = tid; s < A.nseq; s += threads) {
+        SeqRows r;
+        const int a = __ldg(A.row_start + s), b = __ldg(A.row_start + s + 1);
+        const int c = A.ctx_len ? __ldg(A.ctx_len + s) : 0;
+        if (!seq_rows(a, b, c, A.rows, A.cap, r) && blockIdx.x == 0) atomicOr(A.status, SLM_ROWS_LENGTH);
+        seq[s] = r;
+        prefix[s] = A.sc.prefix ? min(max(__ldg(A.sc.prefix + s), 0), r.ctx + r.n) : 0;
+        items[s + 1] = r.n > 0 ? item_count(A.geom, r.n) : 0;
+        wstart[s + 1] = 0;
+    }
+    if (tid == 0) wstart[0] = items[0] = 0;
+    __syncthreads();
+    if (tid < 32) {  // inclusive sums of items[1 ..]
+        // Row ranges that overlap (row_start descends somewhere, which has been reported) could claim
+        // any number of items; ranges that do not have at most this many.
+        const long long most = (long long)A.rows / A.geom.PT + A.nseq;
+        long long carry = 0;
+        for (int s0 = 0; s0 < A.nseq; s0 += 32) {
+            const int s = s0 + tid;
+            long long v = s < A.nseq ? items[s + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (tid >= o) v += u;
+            }
+            if (s < A.nseq) items[s + 1] = (int)min(carry + v, most);
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (carry > most) {  // no sequence has rows then: nothing is computed
+            for (int s = tid; s < A.nseq; s += 32) {
+                seq[s].n = 0;
+                items[s + 1] = 0;
+            }
+        }
+    }
+    __syncthreads();
+    w.mask = SeqMasks{seq, prefix, A.sc.first, A.sc.window};
+    const int all = items[A.nseq], share = (all + threads - 1) / threads;
+    const int i1 = min(all, (tid + 1) * share);
+    int i = min(all, tid * share);
+    if (i < i1) {
+        int lo = 0, hi = A.nseq - 1;  // the last s with items[s] <= i
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (items[mid] <= i)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        for (int s = lo; i < i1; s++) {
+            const int stop = min(i1, items[s + 1]);
+            if (i >= stop) continue;
+            const SeqRows r = seq[s];
+            const RowsMask m = w.mask(s);
+            unsigned long long units = 0;
+            for (; i < stop; i++) units += A.geom.cost + item_span(A.geom, r, m, i - items[s]).nb;
+            atomicAdd((unsigned long long *)&wstart[s + 1], units);  // whole numbers: any order
+        }
+    }
+    __syncthreads();
+    if (tid < 32) {
+        long long carry = 0;
+        for (int s0 = 0; s0 < A.nseq; s0 += 32) {
+            const int s = s0 + tid;
+            long long v = s < A.nseq ? wstart[s + 1] * A.KV : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if (tid >= o) v += u;
+            }
+            if (s < A.nseq) wstart[s + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        __syncwarp();
+        const long long total = wstart[A.nseq], x = range_units(total, A.P) * blockIdx.x;
+        if (x < total) {
+            int lo = 0, hi = A.nseq - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (wstart[mid] <= x)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const SeqRows r = seq[lo];
+            const RowsMask m = w.mask(lo);
+            const unsigned long long per = udiv(wstart[lo + 1] - wstart[lo], A.KV), g = udiv(x - wstart[lo], per);
+            long long at = wstart[lo] + (long long)(g * per);  // units before item t0 of this kv head
+            const int T = item_count(A.geom, r.n);
+            for (int t0 = 0; t0 < T; t0 += 32) {
+                const int t = t0 + tid, u = t < T ? A.geom.cost + item_span(A.geom, r, m, t).nb : 0;
+                long long v = u;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+                    if (tid >= o) v += y;
+                }
+                const bool mine = u > 0 && at + v - u <= x && x < at + v;
+                if (mine) ms->start = RowsStart{lo, (int)g, t, at + v - u};
+                if (__any_sync(0xffffffffu, mine)) break;
+                at += __shfl_sync(0xffffffffu, v, 31);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The span that row i of sequence s sees; checks that `first` does not descend.
+__device__ __forceinline__ void row_span(const RowsArgs &A, const RowsMask &m, const SeqRows &r, int i, bool check, int &lo,
+                                         int &hi) {
+    lo = row_from(m, r.ctx, i);
+    hi = row_to(m, r.ctx, i);
+    if (check && m.first && i > 0 && m.first[i] < m.first[i - 1]) atomicOr(A.status, SLM_ROWS_LENGTH);
+}
+
 // What the joining kernel needs to know about the item that this CTA starts and another
 // finishes (p null: none).  unit: units of a range.
 __device__ __forceinline__ void write_join(const RowsArgs &A, int cta, const SeqRows *seq, long long unit,
@@ -131,9 +280,15 @@ int rows_simt_wide_tile(int hd);                        // of the wide one,
 int rows_simt_tile(int rows, int nseq, int G, int hd);  // and of the one that a call takes
 int rows_simt_ctas(int sms, int hd, int R, int nseq);
 cudaError_t rows_simt_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
+cudaError_t rows_simt_scored_launch(const RowsArgs &a, bool bf16, cudaStream_t s);
 
 // Tensor-core attention: bf16, head_dim up to 128; items of two tiles of 128 / G tokens.
 cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s);
+cudaError_t rows_tc_scored_launch_64(const RowsArgs &a, cudaStream_t s);   // head_dim up to 64
+cudaError_t rows_tc_scored_launch_128(const RowsArgs &a, cudaStream_t s);  // from 72 to 128
+
+// What a kernel does beyond the plain causal scores, as bits of a template argument.
+constexpr int kMasked = 1, kCapped = 2, kBiased = 4;
 
 struct AppendArgs {
     const int *row_start, *ctx_len;
@@ -150,5 +305,39 @@ struct AppendArgs {
     int *status;
 };
 cudaError_t rows_append_launch(const AppendArgs &a, bool in_bf16, bool cache_bf16, cudaStream_t s);
+
+// The append whose pairs turn by positions of their own axes.
+constexpr int kMaxAxes = 8;
+struct AxesArgs {
+    AppendArgs a;
+    const int *positions;    // [n_axes][ld]
+    long long ld;
+    int n_axes;
+    uint8_t axis[128];       // of every pair; 0xff: not turned
+};
+cudaError_t rows_append_axes_launch(const AxesArgs &a, bool in_bf16, bool cache_bf16, cudaStream_t s);
+
+// The plan of a step.
+struct StepArgs {
+    const int *new_len, *seq_len, *free_count;
+    int *page_table, *free_pages;
+    int nseq, table_ld, n_pages, page_shift, rows;
+    long long cap;
+    int *row_start, *ctx_len, *positions, *seq_len_out, *free_count_out, *status;
+    long long *slots;
+};
+cudaError_t rows_step_launch(const StepArgs &a, cudaStream_t s);
+
+constexpr int kSampleMaxVocab = 1 << 22;  // weights of 2^40 at most add up below 2^62
+// The draw of the next tokens with every row's own parameters (null: the default).
+struct SampleRowsArgs {
+    const uint8_t *logits;  // [rows][ld] of fp32 or bf16
+    long long ld;
+    int rows, vocab;
+    const float *temperature, *top_p, *min_p, *uniforms;
+    const int *top_k;
+    int *next_ids;
+};
+cudaError_t sample_rows_launch(const SampleRowsArgs &a, bool bf16, cudaStream_t s);
 
 }  // namespace slm

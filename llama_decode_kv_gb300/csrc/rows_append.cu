@@ -7,6 +7,9 @@
 // with (cos, sin) from the caller's fp32 table; it is done in fp32 and rounded once, to the
 // type that is stored.
 //
+// slm_kv_append_axes turns pair j by position positions[axis[j]][r] instead of p; the rest is the
+// same kernel.
+//
 // Bytes bound it: every value is read once and written once, and nothing else is as large.
 // A unit is VEC pairs of one head (two VEC-element loads, VEC (cos, sin), two stores), so that
 // a thread's accesses are 16 bytes wide (8 for bf16 heads of 8 mod 16) and a warp's are
@@ -70,7 +73,8 @@ struct AppendRow {
 };
 
 // Where row r goes; one warp, the answer on lane 0.
-__device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int lane) {
+// rope_len: positions that the rotation by p may take (no rotation by p: all).
+__device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int lane, long long rope_len) {
     AppendRow o{-1, 0};
     int s = 0;  // sequences that end at or before r: the owner's number
     for (int i = lane; i < A.nseq; i += 32) s += __ldg(A.row_start + i + 1) <= r;
@@ -80,7 +84,7 @@ __device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int
     if (r < first || r >= __ldg(A.row_start + s + 1)) return o;  // before the first sequence, or not ascending
     const int ctx = A.ctx_len ? __ldg(A.ctx_len + s) : 0;
     const long long pos = (long long)ctx + ((long long)r - first);
-    if (ctx < 0 || pos >= A.cap || (A.rope && pos >= A.rope_len)) {
+    if (ctx < 0 || pos >= A.cap || pos >= rope_len) {
         atomicOr(A.status, SLM_ROWS_LENGTH);
         return o;
     }
@@ -94,9 +98,39 @@ __device__ __forceinline__ AppendRow resolve_row(const AppendArgs &A, int r, int
     return o;
 }
 
-template <typename TI, typename TC, int VEC>
-__global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __grid_constant__ AppendArgs A, int rpc) {
+// The (cos, sin) of VEC pairs from pair j on, by the positions of their axes.  Sections put all of
+// them on one axis as a rule, and the table row is read 16 bytes at a time as for one position.
+template <int VEC>
+__device__ __forceinline__ void axes_turns(const float *rope, int half, int j, const uint8_t *axis, const int *pos, float *t) {
+    const int a0 = axis[j];
+    bool same = a0 != 0xff;
+#pragma unroll
+    for (int k = 1; k < VEC; k++) same &= axis[j + k] == a0;
+    if (same) {
+        const float *cs = rope + ((size_t)pos[a0] * half + j) * 2;
+#pragma unroll
+        for (int k = 0; k < 2 * VEC; k += 4) *(float4 *)(t + k) = __ldg((const float4 *)(cs + k));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < VEC; k++) {
+        const int a = axis[j + k];
+        const float2 cs = a == 0xff ? make_float2(1.f, 0.f) : __ldg((const float2 *)(rope + ((size_t)pos[a] * half + j + k) * 2));
+        t[2 * k] = cs.x;
+        t[2 * k + 1] = cs.y;
+    }
+}
+
+__host__ __device__ inline const AppendArgs &append_args(const AppendArgs &a) { return a; }
+__host__ __device__ inline const AppendArgs &append_args(const AxesArgs &a) { return a.a; }
+
+template <typename TI, typename TC, int VEC, typename ARGS>
+__global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __grid_constant__ ARGS P, int rpc) {
+    constexpr bool kAxes = sizeof(ARGS) == sizeof(AxesArgs);
+    const AppendArgs &A = append_args(P);
     __shared__ AppendRow rows[8];
+    __shared__ int axis_pos[kAxes ? 8 : 1][kMaxAxes];
+    __shared__ uint8_t axis[kAxes ? 128 : 1];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -110,9 +144,24 @@ __global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __gri
         if (bad) atomicOr(A.status, SLM_ROWS_LENGTH);
     }
     if (warp < nr) {
-        const AppendRow a = resolve_row(A, r0 + warp, lane);
+        AppendRow a = resolve_row(A, r0 + warp, lane, A.rope && !kAxes ? A.rope_len : A.cap);
+        if constexpr (kAxes) {
+            bool off = false;  // an axis' position outside the table: the row is left out
+            const bool row = __shfl_sync(0xffffffffu, (int)(a.cache_row >= 0), 0);
+            if (row && lane < P.n_axes) {
+                const int x = __ldg(P.positions + lane * P.ld + r0 + warp);
+                off = x < 0 || x >= A.rope_len;
+                axis_pos[warp][lane] = off ? 0 : x;
+            }
+            if (__any_sync(0xffffffffu, off)) {
+                if (lane == 0) atomicOr(A.status, SLM_ROWS_LENGTH);
+                a.cache_row = -1;
+            }
+        }
         if (lane == 0) rows[warp] = a;
     }
+    if constexpr (kAxes)
+        for (int j = threadIdx.x; j < A.hd / 2; j += kAppendThreads) axis[j] = P.axis[j];
     __syncthreads();
     const int half = A.hd / 2, ph = half / VEC;        // units of a head
     const int Hq = A.q ? A.H : 0, heads = Hq + 2 * A.KV;
@@ -136,10 +185,14 @@ __global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __gri
         }
         Floats<VEC> a = load_vec<VEC>(src + j), b = load_vec<VEC>(src + j + half);
         if (A.rope && h < Hq + A.KV) {
-            const float *cs = A.rope + ((size_t)R.pos * half + j) * 2;
             float t[2 * VEC];
+            if constexpr (kAxes) {
+                axes_turns<VEC>(A.rope, half, j, axis, axis_pos[i], t);
+            } else {
+                const float *cs = A.rope + ((size_t)R.pos * half + j) * 2;
 #pragma unroll
-            for (int k = 0; k < 2 * VEC; k += 4) *(float4 *)(t + k) = __ldg((const float4 *)(cs + k));
+                for (int k = 0; k < 2 * VEC; k += 4) *(float4 *)(t + k) = __ldg((const float4 *)(cs + k));
+            }
 #pragma unroll
             for (int k = 0; k < VEC; k++) {
                 const float x = a.v[k], y = b.v[k];
@@ -152,8 +205,9 @@ __global__ void __launch_bounds__(kAppendThreads) rows_append_kernel(const __gri
     }
 }
 
-template <typename TI, typename TC>
-static cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
+template <typename TI, typename TC, typename ARGS>
+static cudaError_t launch_append(const ARGS &p, cudaStream_t s) {
+    const AppendArgs &a = append_args(p);
     const int vec = a.hd % 16 == 0 ? 8 : 4;
     const int units = ((a.q ? a.H : 0) + 2 * a.KV) * (a.hd / 2 / vec);
     // One row per CTA, its units spread over grid.y, while the rows alone do not fill the GPU;
@@ -161,13 +215,21 @@ static cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
     const int rpc = a.rows >= 2048 ? 4 : 1;
     const int gy = rpc > 1 ? 1 : std::min((units + kAppendThreads - 1) / kAppendThreads, 65535);
     const dim3 grid((a.rows + rpc - 1) / rpc, gy);
-    return launch_pdl(vec == 8 ? rows_append_kernel<TI, TC, 8> : rows_append_kernel<TI, TC, 4>, grid, dim3(kAppendThreads), 0, s,
-                      a, rpc);
+    return launch_pdl(vec == 8 ? rows_append_kernel<TI, TC, 8, ARGS> : rows_append_kernel<TI, TC, 4, ARGS>, grid,
+                      dim3(kAppendThreads), 0, s, p, rpc);
+}
+
+template <typename ARGS>
+static cudaError_t launch_typed(const ARGS &a, bool in_bf16, bool cache_bf16, cudaStream_t s) {
+    if (in_bf16) return cache_bf16 ? launch_append<__nv_bfloat16, __nv_bfloat16>(a, s) : launch_append<__nv_bfloat16, float>(a, s);
+    return cache_bf16 ? launch_append<float, __nv_bfloat16>(a, s) : launch_append<float, float>(a, s);
 }
 
 cudaError_t rows_append_launch(const AppendArgs &a, bool in_bf16, bool cache_bf16, cudaStream_t s) {
-    if (in_bf16) return cache_bf16 ? launch_append<__nv_bfloat16, __nv_bfloat16>(a, s) : launch_append<__nv_bfloat16, float>(a, s);
-    return cache_bf16 ? launch_append<float, __nv_bfloat16>(a, s) : launch_append<float, float>(a, s);
+    return launch_typed(a, in_bf16, cache_bf16, s);
+}
+cudaError_t rows_append_axes_launch(const AxesArgs &a, bool in_bf16, bool cache_bf16, cudaStream_t s) {
+    return launch_typed(a, in_bf16, cache_bf16, s);
 }
 
 }  // namespace slm

@@ -1,5 +1,5 @@
 // rows_op.cu -- the packed-row operators behind the C ABI (include/slm.h): slm_kv_append,
-// slm_attention_paged, slm_attention_prompt.  Checks of arguments and the choice of kernels;
+// slm_attention_paged, slm_attention_prompt and the calls of a serving step around them.  Checks of arguments and the choice of kernels;
 // nothing here reads the lengths, which live on the device.
 #include <cuda_runtime.h>
 
@@ -80,6 +80,13 @@ static int check_rows(const slm_rows *r) {
     return SLM_OK;
 }
 
+static int check_pages(int page_size, int n_pages, int table_ld) {
+    if (page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)))
+        return attn_fail(SLM_EINVAL, "page_size %d must be a power of two in [16, 2^20]", page_size);
+    if (n_pages < 1 || table_ld < 1) return attn_fail(SLM_EINVAL, "n_pages %d and table_ld %d must be positive", n_pages, table_ld);
+    return SLM_OK;
+}
+
 static int check_cache(const slm_kv_cache *c) {
     if (!c) return attn_fail(SLM_EINVAL, "cache is NULL");
     if (check_dtype(c->kv_dtype, "kv_dtype")) return SLM_EINVAL;
@@ -87,9 +94,7 @@ static int check_cache(const slm_kv_cache *c) {
         return attn_fail(SLM_EINVAL, "n_kv_heads %d outside [1, %d]", c->n_kv_heads, kRowsMaxHeads);
     if (c->head_dim < 8 || c->head_dim % 8 || c->head_dim > 256)
         return attn_fail(SLM_EINVAL, "head_dim %d must be a multiple of 8 in [8, 256]", c->head_dim);
-    if (c->page_size < 16 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)))
-        return attn_fail(SLM_EINVAL, "page_size %d must be a power of two in [16, 2^20]", c->page_size);
-    if (c->n_pages < 1 || c->table_ld < 1) return attn_fail(SLM_EINVAL, "n_pages %d and table_ld %d must be positive", c->n_pages, c->table_ld);
+    if (check_pages(c->page_size, c->n_pages, c->table_ld)) return SLM_EINVAL;
     if (!c->k || !c->v || !c->page_table) return attn_fail(SLM_EINVAL, "k, v and page_table of the cache must be non-NULL");
     if (((uintptr_t)c->k | (uintptr_t)c->v) & 15) return attn_fail(SLM_EINVAL, "the cache's k and v must be 16-byte aligned");
     if ((uintptr_t)c->page_table % 4) return attn_fail(SLM_EINVAL, "page_table must be 4-byte aligned");
@@ -120,9 +125,10 @@ static int log2i(int v) {
 }
 
 // Positions are int32 in the kernels.
-static long long cache_cap(const slm_kv_cache *c) {
-    return std::min<long long>((long long)c->table_ld * c->page_size, 0x7fffff00LL);
+static long long table_cap(int table_ld, int page_size) {
+    return std::min<long long>((long long)table_ld * page_size, 0x7fffff00LL);
 }
+static long long cache_cap(const slm_kv_cache *c) { return table_cap(c->table_ld, c->page_size); }
 
 // Tiling and workspace of an attention call.
 struct RowsTiling {
@@ -173,9 +179,19 @@ static int check_group(int H, int KV, int hd) {
 
 static std::atomic<int> g_lost{0};  // slm_debug_rows_faults
 
-// The part that both attention calls share: workspace, kernel, join.
-static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long longest, void *ws, size_t ws_bytes,
-                         cudaStream_t s) {
+static int check_scores(const slm_scores *s) {
+    if (!s) return attn_fail(SLM_EINVAL, "scores is NULL");
+    if (!(s->scale >= 0.f) || !std::isfinite(s->scale)) return attn_fail(SLM_EINVAL, "scale %g must be finite and not negative", (double)s->scale);
+    if (!(s->cap >= 0.f) || !std::isfinite(s->cap)) return attn_fail(SLM_EINVAL, "cap %g must be finite and not negative", (double)s->cap);
+    if (s->window < 0) return attn_fail(SLM_EINVAL, "window %d is negative", s->window);
+    if (((uintptr_t)s->slopes | (uintptr_t)s->prefix_len | (uintptr_t)s->first) % 4)
+        return attn_fail(SLM_EINVAL, "slopes, prefix_len and first must be 4-byte aligned");
+    return SLM_OK;
+}
+
+// The part that all attention calls share: workspace, kernel, join.
+static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long longest, const slm_scores *sc, void *ws,
+                         size_t ws_bytes, cudaStream_t s) {
     if (!ws || (uintptr_t)ws % 256) return attn_fail(SLM_EINVAL, "workspace must be non-NULL and 256-byte aligned");
     if (ws_bytes < t.ws) return attn_fail(SLM_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, t.ws);
     a.ws = (uint8_t *)ws;
@@ -189,29 +205,48 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     // 21.2.  `longest` is what the caller's table (for prompts: the packed rows) could hold, since the
     // lengths are not known here: a short context under a wide table is cut all the same (one token
     // over 250 positions, table for 32,768: 9.1 us).
+    // A window bounds what an item sees besides.
+    if (sc && sc->window) longest = std::min(longest, (long long)sc->window + t.geom.PT);
     a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
     a.lost = g_lost.load(std::memory_order_relaxed);
     a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)a.hd));
+    if (sc) {
+        const double scale = sc->scale > 0.f ? (double)sc->scale : 1.0 / std::sqrt((double)a.hd);
+        const double most = 3.4028234663852886e38;  // a finite factor: 0 stays 0
+        a.scale_log2 = (float)std::min(1.4426950408889634074 * scale, most);
+        a.sc.slopes = sc->slopes;
+        a.sc.prefix = sc->prefix_len;
+        a.sc.first = sc->first;
+        a.sc.window = sc->window;
+        if (sc->cap > 0.f) {
+            a.sc.cap_in = (float)std::min(scale / sc->cap, most);
+            a.sc.cap_log2 = (float)std::max(std::min(1.4426950408889634074 * sc->cap, most), 1.401298464324817e-45);
+        }
+    }
     const bool bf16 = dtype == SLM_BF16;
     if (a.rows == 1) {  // one row: its stride has no meaning
         a.q_ld = a.out_ld = (long long)a.H * a.hd;
         a.kv.k_ld = a.kv.v_ld = (long long)a.KV * a.hd;
     }
-    cudaError_t e = on_tensor_cores(dtype, a.hd) ? rows_tc_launch(a, s) : rows_simt_launch(a, bf16, s);
+    cudaError_t e;
+    if (!sc)
+        e = on_tensor_cores(dtype, a.hd) ? rows_tc_launch(a, s) : rows_simt_launch(a, bf16, s);
+    else if (on_tensor_cores(dtype, a.hd))
+        e = a.hd <= 64 ? rows_tc_scored_launch_64(a, s) : rows_tc_scored_launch_128(a, s);
+    else
+        e = rows_simt_scored_launch(a, bf16, s);
     if (e == cudaSuccess && a.geom.split) e = rows_join_launch(a, bf16, s);
     if (e != cudaSuccess) return launch_fail("attention", e);
     return SLM_OK;
 }
 
-}  // namespace slm
-
-using namespace slm;
-
-extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
-                             const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_heads,
-                             const void *q, int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status,
-                             void *stream) {
+// Checks and arguments that the two appends share; dev: the current device.  positions: NULL, or the
+// other append's.  SLM_OK with a.rows = 0: nothing to do.
+static int append_common(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
+                         const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_heads, const void *q,
+                         int64_t q_ld, void *q_out, int64_t q_out_ld, const int32_t *positions, int32_t *status,
+                         AppendArgs &a) {
     int rc;
     if ((rc = check_cache(cache)) || (rc = check_rows(rows)) || (rc = check_dtype(dtype, "dtype"))) return rc;
     const int KV = cache->n_kv_heads, hd = cache->head_dim;
@@ -232,10 +267,8 @@ extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, in
     if (sms < 0) return sms;
     const PtrCheck ptrs[] = {{cache->k, "the cache's k"}, {cache->v, "the cache's v"}, {cache->page_table, "page_table"},
                              {rows->row_start, "row_start"}, {rows->ctx_len, "ctx_len"}, {k, "k"}, {v, "v"},
-                             {rope, "rope"}, {q, "q"}, {q_out, "q_out"}, {status, "status"}};
+                             {rope, "rope"}, {q, "q"}, {q_out, "q_out"}, {positions, "positions"}, {status, "status"}};
     if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
-    if (rows->rows == 0) return SLM_OK;
-    AppendArgs a{};
     a.row_start = rows->row_start;
     a.ctx_len = rows->ctx_len;
     a.nseq = rows->nseq;
@@ -261,8 +294,138 @@ extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, in
     a.n_pages = cache->n_pages;
     a.page_shift = log2i(cache->page_size);
     a.status = status;
+    return SLM_OK;
+}
+
+}  // namespace slm
+
+using namespace slm;
+
+extern "C" int slm_kv_append(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k, int64_t k_ld,
+                             const void *v, int64_t v_ld, const float *rope, int32_t rope_len, int32_t n_heads,
+                             const void *q, int64_t q_ld, void *q_out, int64_t q_out_ld, int32_t *status,
+                             void *stream) {
+    AppendArgs a{};
+    if (int rc = append_common(cache, rows, dtype, k, k_ld, v, v_ld, rope, rope_len, n_heads, q, q_ld, q_out, q_out_ld, nullptr,
+                               status, a))
+        return rc;
+    if (a.rows == 0) return SLM_OK;
     const cudaError_t e = rows_append_launch(a, dtype == SLM_BF16, cache->kv_dtype == SLM_BF16, (cudaStream_t)stream);
     if (e != cudaSuccess) return launch_fail("append", e);
+    return SLM_OK;
+}
+
+extern "C" int slm_kv_append_axes(const slm_kv_cache *cache, const slm_rows *rows, int32_t dtype, const void *k,
+                                  int64_t k_ld, const void *v, int64_t v_ld, const float *rope, int32_t rope_len,
+                                  int32_t n_axes, const int8_t *axis_of_pair, const int32_t *positions,
+                                  int64_t positions_ld, int32_t n_heads, const void *q, int64_t q_ld, void *q_out,
+                                  int64_t q_out_ld, int32_t *status, void *stream) {
+    int rc;
+    if ((rc = check_cache(cache)) || (rc = check_rows(rows))) return rc;
+    if (n_axes < 1 || n_axes > kMaxAxes) return attn_fail(SLM_EINVAL, "n_axes %d outside [1, %d]", n_axes, kMaxAxes);
+    if (!axis_of_pair) return attn_fail(SLM_EINVAL, "axis_of_pair is NULL");
+    AxesArgs x{};
+    for (int j = 0; j < cache->head_dim / 2; j++) {
+        if (axis_of_pair[j] < -1 || axis_of_pair[j] >= n_axes)
+            return attn_fail(SLM_EINVAL, "axis_of_pair[%d] = %d outside [-1, %d)", j, (int)axis_of_pair[j], n_axes);
+        x.axis[j] = (uint8_t)axis_of_pair[j];
+    }
+    if (!rope) return attn_fail(SLM_EINVAL, "rope is NULL");
+    if (rows->rows > 0 && (!positions || (uintptr_t)positions % 4))
+        return attn_fail(SLM_EINVAL, "positions must be non-NULL and 4-byte aligned");
+    if (positions_ld < rows->rows || positions_ld > (1LL << 32))
+        return attn_fail(SLM_EINVAL, "positions_ld %lld outside [%d, 2^32]", (long long)positions_ld, rows->rows);
+    if ((rc = append_common(cache, rows, dtype, k, k_ld, v, v_ld, rope, rope_len, n_heads, q, q_ld, q_out, q_out_ld, positions,
+                            status, x.a)))
+        return rc;
+    if (x.a.rows == 0) return SLM_OK;
+    x.positions = positions;
+    x.ld = positions_ld;
+    x.n_axes = n_axes;
+    const cudaError_t e = rows_append_axes_launch(x, dtype == SLM_BF16, cache->kv_dtype == SLM_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return launch_fail("append", e);
+    return SLM_OK;
+}
+
+extern "C" int slm_rows_plan(const slm_page_pool *pool, const int32_t *new_len, int32_t rows, int32_t *row_start,
+                             int32_t *ctx_len, int32_t *positions, int64_t *slots, int32_t *seq_len_out,
+                             int32_t *free_count_out, int32_t *status, void *stream) {
+    if (!pool) return attn_fail(SLM_EINVAL, "pool is NULL");
+    if (pool->nseq < 1 || pool->nseq > kRowsMaxSeqs) return attn_fail(SLM_EINVAL, "nseq %d outside [1, %d]", pool->nseq, kRowsMaxSeqs);
+    if (rows < 0 || rows > kRowsMaxRows) return attn_fail(SLM_EINVAL, "rows %d outside [0, 2^30]", rows);
+    int rc;
+    if ((rc = check_pages(pool->page_size, pool->n_pages, pool->table_ld))) return rc;
+    const PtrCheck ptrs[] = {{pool->page_table, "page_table"}, {pool->free_pages, "free_pages"}, {pool->free_count, "free_count"},
+                             {pool->seq_len, "seq_len"}, {new_len, "new_len"}, {row_start, "row_start"}, {ctx_len, "ctx_len"},
+                             {seq_len_out, "seq_len_out"}, {free_count_out, "free_count_out"}, {status, "status"},
+                             {positions, "positions"}, {slots, "slots"}};
+    constexpr int n = sizeof ptrs / sizeof *ptrs;
+    for (int i = 0; i < n; i++) {
+        if (!ptrs[i].p && i < n - 2) return attn_fail(SLM_EINVAL, "%s is NULL", ptrs[i].name);
+        const int size = i == n - 1 ? 8 : 4;
+        if ((uintptr_t)ptrs[i].p % size) return attn_fail(SLM_EINVAL, "%s must be %d-byte aligned", ptrs[i].name, size);
+    }
+    int dev = 0;
+    if ((rc = current_sms(dev)) < 0) return rc;
+    if ((rc = check_pointers(dev, ptrs, n))) return rc;
+    StepArgs a{};
+    a.new_len = new_len;
+    a.seq_len = pool->seq_len;
+    a.free_count = pool->free_count;
+    a.page_table = pool->page_table;
+    a.free_pages = pool->free_pages;
+    a.nseq = pool->nseq;
+    a.table_ld = pool->table_ld;
+    a.n_pages = pool->n_pages;
+    a.page_shift = log2i(pool->page_size);
+    a.rows = rows;
+    a.cap = table_cap(pool->table_ld, pool->page_size);
+    a.row_start = row_start;
+    a.ctx_len = ctx_len;
+    a.positions = positions;
+    a.slots = (long long *)slots;
+    a.seq_len_out = seq_len_out;
+    a.free_count_out = free_count_out;
+    a.status = status;
+    const cudaError_t e = rows_step_launch(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return launch_fail("plan", e);
+    return SLM_OK;
+}
+
+extern "C" int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const void *logits, int64_t ld,
+                               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                               const float *uniforms, int32_t *next_ids, void *stream) {
+    int rc;
+    if (rows < 0 || rows > kRowsMaxRows) return attn_fail(SLM_EINVAL, "rows %d outside [0, 2^30]", rows);
+    if (vocab < 1 || vocab > kSampleMaxVocab) return attn_fail(SLM_EINVAL, "vocab %d outside [1, 2^22]", vocab);
+    if ((rc = check_dtype(dtype, "dtype"))) return rc;
+    if (rows > 1 && ld != 0 && (ld < vocab || ld > (1LL << 32)))
+        return attn_fail(SLM_EINVAL, "logits: row stride %lld is neither 0 nor in [%d, 2^32]", (long long)ld, vocab);
+    const PtrCheck ptrs[] = {{logits, "logits"}, {uniforms, "uniforms"}, {next_ids, "next_ids"}, {temperature, "temperature"},
+                             {top_k, "top_k"}, {top_p, "top_p"}, {min_p, "min_p"}};
+    constexpr int n = sizeof ptrs / sizeof *ptrs;
+    for (int i = 0; i < n && rows > 0; i++) {
+        if (!ptrs[i].p && i < 3) return attn_fail(SLM_EINVAL, "%s is NULL", ptrs[i].name);
+        const int size = i == 0 ? elem_size(dtype) : 4;
+        if ((uintptr_t)ptrs[i].p % size) return attn_fail(SLM_EINVAL, "%s must be %d-byte aligned", ptrs[i].name, size);
+    }
+    int dev = 0;
+    if ((rc = current_sms(dev)) < 0) return rc;
+    if ((rc = check_pointers(dev, ptrs, n))) return rc;
+    if (rows == 0) return SLM_OK;
+    SampleRowsArgs a{};
+    a.logits = (const uint8_t *)logits;
+    a.ld = rows > 1 ? ld : vocab;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.uniforms = uniforms;
+    a.next_ids = next_ids;
+    const cudaError_t e = sample_rows_launch(a, dtype == SLM_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return launch_fail("sample", e);
     return SLM_OK;
 }
 
@@ -276,9 +439,10 @@ extern "C" size_t slm_attention_rows_workspace_bytes(int32_t dtype, int32_t rows
     return sms < 0 ? 0 : rows_tiling(sms, dtype, rows, nseq, n_heads, n_kv_heads, head_dim).ws;
 }
 
-extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q,
-                                   int64_t q_ld, void *out, int64_t out_ld, void *workspace, size_t workspace_bytes,
-                                   int32_t *status, void *stream) {
+// sc: NULL for plain causal scores.
+static int paged_attention(const slm_kv_cache *cache, const slm_rows *rows, const slm_scores *sc, int32_t n_heads, const void *q,
+                           int64_t q_ld, void *out, int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
+                           void *stream) {
     int rc;
     if ((rc = check_cache(cache)) || (rc = check_rows(rows))) return rc;
     const int KV = cache->n_kv_heads, hd = cache->head_dim, dtype = cache->kv_dtype;
@@ -291,7 +455,8 @@ extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *ro
     if (sms < 0) return sms;
     const PtrCheck ptrs[] = {{cache->k, "the cache's k"}, {cache->v, "the cache's v"}, {cache->page_table, "page_table"},
                              {rows->row_start, "row_start"}, {rows->ctx_len, "ctx_len"}, {q, "q"}, {out, "out"},
-                             {workspace, "workspace"}, {status, "status"}};
+                             {workspace, "workspace"}, {status, "status"}, {sc ? sc->slopes : nullptr, "slopes"},
+                             {sc ? sc->prefix_len : nullptr, "prefix_len"}, {sc ? sc->first : nullptr, "first"}};
     if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
     if (rows->rows == 0) return SLM_OK;
     RowsArgs a{};
@@ -314,14 +479,14 @@ extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *ro
     a.kv.n_pages = cache->n_pages;
     a.kv.page_shift = log2i(cache->page_size);
     a.status = status;
-    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, KV, hd), dtype, a.cap, workspace,
-                         workspace_bytes, (cudaStream_t)stream);
+    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, KV, hd), dtype, a.cap, sc,
+                         workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
-extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, int32_t n_kv_heads,
-                                    int32_t head_dim, const void *q, int64_t q_ld, const void *k, int64_t k_ld,
-                                    const void *v, int64_t v_ld, void *out, int64_t out_ld, void *workspace,
-                                    size_t workspace_bytes, int32_t *status, void *stream) {
+static int prompt_attention(const slm_rows *rows, const slm_scores *sc, int32_t dtype, int32_t n_heads, int32_t n_kv_heads,
+                            int32_t head_dim, const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v,
+                            int64_t v_ld, void *out, int64_t out_ld, void *workspace, size_t workspace_bytes,
+                            int32_t *status, void *stream) {
     int rc;
     if ((rc = check_rows(rows)) || (rc = check_dtype(dtype, "dtype")) || (rc = check_heads(n_heads, n_kv_heads, head_dim)) ||
         (rc = check_group(n_heads, n_kv_heads, head_dim)))
@@ -336,7 +501,8 @@ extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t
     const int sms = current_sms(dev);
     if (sms < 0) return sms;
     const PtrCheck ptrs[] = {{rows->row_start, "row_start"}, {q, "q"}, {k, "k"}, {v, "v"}, {out, "out"},
-                             {workspace, "workspace"}, {status, "status"}};
+                             {workspace, "workspace"}, {status, "status"}, {sc ? sc->slopes : nullptr, "slopes"},
+                             {sc ? sc->prefix_len : nullptr, "prefix_len"}, {sc ? sc->first : nullptr, "first"}};
     if ((rc = check_pointers(dev, ptrs, sizeof ptrs / sizeof *ptrs))) return rc;
     if (rows->rows == 0) return SLM_OK;
     RowsArgs a{};
@@ -356,8 +522,39 @@ extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t
     a.kv.k_ld = k_ld;
     a.kv.v_ld = v_ld;
     a.status = status;
-    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows,
+    return run_attention(a, rows_tiling(sms, dtype, rows->rows, rows->nseq, n_heads, n_kv_heads, head_dim), dtype, rows->rows, sc,
                          workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" int slm_attention_paged(const slm_kv_cache *cache, const slm_rows *rows, int32_t n_heads, const void *q,
+                                   int64_t q_ld, void *out, int64_t out_ld, void *workspace, size_t workspace_bytes,
+                                   int32_t *status, void *stream) {
+    return paged_attention(cache, rows, nullptr, n_heads, q, q_ld, out, out_ld, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" int slm_attention_paged_scored(const slm_kv_cache *cache, const slm_rows *rows, const slm_scores *scores,
+                                          int32_t n_heads, const void *q, int64_t q_ld, void *out, int64_t out_ld,
+                                          void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
+    if (int rc = check_scores(scores)) return rc;
+    return paged_attention(cache, rows, scores, n_heads, q, q_ld, out, out_ld, workspace, workspace_bytes, status, stream);
+}
+
+extern "C" int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, int32_t n_kv_heads,
+                                    int32_t head_dim, const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                                    const void *v, int64_t v_ld, void *out, int64_t out_ld, void *workspace,
+                                    size_t workspace_bytes, int32_t *status, void *stream) {
+    return prompt_attention(rows, nullptr, dtype, n_heads, n_kv_heads, head_dim, q, q_ld, k, k_ld, v, v_ld, out, out_ld,
+                            workspace, workspace_bytes, status, stream);
+}
+
+extern "C" int slm_attention_prompt_scored(const slm_rows *rows, const slm_scores *scores, int32_t dtype, int32_t n_heads,
+                                           int32_t n_kv_heads, int32_t head_dim, const void *q, int64_t q_ld,
+                                           const void *k, int64_t k_ld, const void *v, int64_t v_ld, void *out,
+                                           int64_t out_ld, void *workspace, size_t workspace_bytes, int32_t *status,
+                                           void *stream) {
+    if (int rc = check_scores(scores)) return rc;
+    return prompt_attention(rows, scores, dtype, n_heads, n_kv_heads, head_dim, q, q_ld, k, k_ld, v, v_ld, out, out_ld,
+                            workspace, workspace_bytes, status, stream);
 }
 
 extern "C" int slm_debug_rows_faults(int32_t lost) {

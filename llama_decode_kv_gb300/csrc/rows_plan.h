@@ -116,10 +116,14 @@ SLM_HD long long range_units(long long total, int P) {
     return total > 0 ? (long long)udiv((unsigned long long)total + P - 1, (unsigned long long)P) : 1;
 }
 
-// One piece of one item: blocks [kb0, kb1) of its nb.
+// One piece of one item: blocks [kb0, kb1) of its [b0, b0 + nb).
 struct RowsPiece {
     int s, g, t, nb, kb0, kb1;
     long long base;  // the item's first unit
+    int b0;          // 0 but for masked items
+
+    SLM_HD bool begins() const { return kb0 == b0; }
+    SLM_HD bool ends() const { return kb1 == b0 + nb; }
 };
 
 // Walks the pieces of the units [from, to).  seq: the checked sequences; wstart[s]: units of
@@ -203,6 +207,7 @@ struct RowsWalk {
             p.t = t;
             p.nb = nb;
             p.base = base;
+            p.b0 = 0;
             p.kb0 = x > first ? (int)(x - first) : 0;
             p.kb1 = hi > first ? (int)(hi - first) : 0;
             x = hi;
@@ -215,6 +220,111 @@ struct RowsWalk {
 
 // A CTA has at most two pieces that are not whole items: one that starts inside an item
 // (its first) and one that starts an item and does not finish it (its last).
-SLM_HD int piece_slot(int cta, const RowsPiece &p) { return 2 * cta + (p.kb0 > 0 ? 0 : 1); }
+SLM_HD int piece_slot(int cta, const RowsPiece &p) { return 2 * cta + (p.begins() ? 1 : 0); }
 
+// ---- items whose rows do not see all positions up to their own
+//
+// Row i of a sequence, at position p = ctx + i, sees [lo, hi): lo = max(first, p + 1 - window, 0),
+// hi = max(p + 1, prefix).  first does not descend within a sequence, so an item's span begins at
+// its first row's lo and ends at its last row's hi, and has blocks [b0, b0 + nb) of its own (none
+// where the span is empty: such an item still counts its `cost` units, and writes its rows).  There
+// is no closed form for their sum: the units of all items are added up one by one (masked_start).
+
+// The mask of one sequence: its first packed row's entry of `first` (null: none), its prefix cut to
+// [0, ctx + n], the window (0: none).
+struct RowsMask {
+    const int *first;
+    int prefix, window;
+};
+
+SLM_HD int row_from(const RowsMask &m, int ctx, int i) {
+    int lo = m.first ? m.first[i] : 0;
+    lo = lo > 0 ? lo : 0;
+    const int w = m.window ? ctx + i + 1 - m.window : 0;
+    return lo > w ? lo : w;
+}
+SLM_HD int row_to(const RowsMask &m, int ctx, int i) { return ctx + i + 1 > m.prefix ? ctx + i + 1 : m.prefix; }
+
+struct RowsSpan {
+    int lo, hi, b0, nb;
+};
+SLM_HD RowsSpan item_span(const RowsGeom &g, const SeqRows &r, const RowsMask &m, int t) {
+    const int i0 = t * g.PT, i1 = r.n - i0 < g.PT ? r.n : i0 + g.PT;
+    RowsSpan s{row_from(m, r.ctx, i0), row_to(m, r.ctx, i1 - 1), 0, 0};
+    if (s.lo < s.hi) {
+        s.b0 = s.lo >> g.shift;
+        s.nb = (int)(((unsigned)s.hi + (1u << g.shift) - 1) >> g.shift) - s.b0;
+    }
+    return s;
+}
+
+// The item that holds a unit of the line.
+struct RowsStart {
+    int s, g, t;
+    long long base;
+};
+
+// RowsWalk over masked items.  mask(s): the mask of sequence s.
+template <typename MASK> struct MaskedWalk {
+    long long x, end, base;
+    int s, g, t;
+    RowsSpan span;
+    MASK mask;
+
+    SLM_HD void open(const SeqRows *seq, const RowsGeom &G) { span = item_span(G, seq[s], mask(s), t); }
+
+    SLM_HD bool advance(const SeqRows *seq, int nseq, const RowsGeom &G) {
+        base += G.cost + span.nb;
+        t++;
+        if ((long long)t * G.PT >= seq[s].n) {
+            t = 0;
+            if (++g == G.KV) {
+                g = 0;
+                s++;
+                while (s < nseq && seq[s].n == 0) s++;
+            }
+        }
+        if (s >= nseq) return false;
+        open(seq, G);
+        return true;
+    }
+
+    // at: the item that holds unit `from` (not looked at where the range is empty).
+    SLM_HD void begin(const SeqRows *seq, long long total, int nseq, const RowsGeom &G, long long from, long long to,
+                      const RowsStart &at) {
+        x = from;
+        end = to < total ? to : total;
+        if (x >= end) return;
+        s = at.s;
+        g = at.g;
+        t = at.t;
+        base = at.base;
+        open(seq, G);
+        if (!G.split && base < x) {  // the item belongs to the range that it begins in
+            if (!advance(seq, nseq, G)) end = x;
+            x = base;
+        }
+    }
+
+    // The next piece: at least one block, or the whole of an item without any.
+    SLM_HD bool next(const SeqRows *seq, int nseq, const RowsGeom &G, RowsPiece &p) {
+        while (x < end) {
+            const long long first = base + G.cost, stop = first + span.nb;
+            const long long hi = end < stop && G.split ? end : stop;
+            const bool empty = span.nb == 0 && x == base;
+            p.s = s;
+            p.g = g;
+            p.t = t;
+            p.nb = span.nb;
+            p.base = base;
+            p.b0 = span.b0;
+            p.kb0 = span.b0 + (x > first ? (int)(x - first) : 0);
+            p.kb1 = span.b0 + (hi > first ? (int)(hi - first) : 0);
+            x = hi;
+            if (x >= stop && !advance(seq, nseq, G)) end = x;
+            if (p.kb1 > p.kb0 || empty) return true;
+        }
+        return false;
+    }
+};
 }  // namespace slm
