@@ -25,7 +25,9 @@ struct RowsScores {
     const int *prefix, *first;   // [nseq], [rows]
     int window;
     float cap_in, cap_log2;      // scale / cap, cap log2(e)
-    float scale;                 // of q . k
+    // the tensor-core kernel's tanh (rows_attention_tc.cuh): |q . k| up to half the cap and up to it, and the
+    // polynomials' coefficients of powers of (q . k)^2
+    float half_cap, one_cap, poly3[3], poly5[5];
 };
 
 struct RowsArgs {
@@ -106,19 +108,20 @@ struct SeqMasks {
 };
 typedef MaskedWalk<SeqMasks> RowsMaskedWalk;
 
-// Shared memory that masked_layout takes after seq and wstart.
+// Shared memory that masked_layout takes after seq and wstart; besides, nseq + 1 ints of scratch that
+// it is done with at its end.
 struct MaskedShared {
     RowsStart start;
-    int sums[1];  // prefix[nseq], items before each sequence [nseq + 1]
+    int prefix[1];  // [nseq]
 };
-__host__ __device__ inline size_t masked_bytes(int nseq) { return (sizeof(RowsStart) + (2 * (size_t)nseq + 1) * 4 + 15) / 16 * 16; }
+__host__ __device__ inline size_t masked_bytes(int nseq) { return (sizeof(RowsStart) + (size_t)nseq * 4 + 15) / 16 * 16; }
 
 // rows_layout for masked items: their units are added up one by one, an equal share of them per
 // thread (8,192 rows of 4 heads per kv head are 128 items), and warp 0 looks for the item that this
 // CTA's range begins in.  Ends with a __syncthreads().
 __device__ __forceinline__ void masked_layout(const RowsArgs &A, SeqRows *seq, long long *wstart, MaskedShared *ms,
-                                              RowsMaskedWalk &w, int tid, int threads) {
-    int *prefix = ms->sums, *items = ms->sums + A.nseq;
+                                              int *items, RowsMaskedWalk &w, int tid, int threads) {
+    int *prefix = ms->prefix;
     for (int s = tid; s < A.nseq; s += threads) {
         SeqRows r;
         const int a = __ldg(A.row_start + s), b = __ldg(A.row_start + s + 1);

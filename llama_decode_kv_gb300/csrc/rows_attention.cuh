@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
     std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk> w;
     if constexpr (kSpans) {
         MaskedShared *ms = (MaskedShared *)(((uintptr_t)(lrow + R) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, w, tid, kSimtThreads);
+        masked_layout(A, seq, wstart, ms, (int *)kv, w, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
         w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
     } else {
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
     std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk> w;
     if constexpr (kSpans) {
         MaskedShared *ms = (MaskedShared *)(((uintptr_t)(ps + R * PLD) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, w, tid, kSimtThreads);
+        masked_layout(A, seq, wstart, ms, (int *)kv, w, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
         w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
     } else {

@@ -52,6 +52,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "device_common.cuh"
@@ -60,7 +61,10 @@
 
 namespace slm {
 
-constexpr int kTcThreads = 320;
+// Threads of a CTA: ten warps; scored calls twelve (two of them idle), so that their softmax groups can
+// take registers over from the other roles: 2 x 128 x 208 + 128 x 88 = 384 x 168, what such a CTA is
+// launched with.
+__host__ __device__ constexpr int tc_threads(int score) { return score ? 384 : 320; }
 constexpr int kTcBlk = 128;                 // positions per block
 constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]
 constexpr int kTcCols = 512;                // tensor memory columns
@@ -68,6 +72,7 @@ constexpr float kTcSlack = 8.0f;            // log2 growth of a maximum that O i
 
 struct RowsTcArgs {
     CUtensorMap q, k, v;
+    CUtensorMap q_few;  // queries of 32 / G tokens (split items)
     RowsArgs a;
     int TT;      // tokens per tile
     int box;     // positions per key / value box
@@ -78,6 +83,7 @@ struct RowsTcArgs {
 struct TcBars {
     uint64_t kv_full[16], kv_empty[16];
     uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_ready[2], o_full[2], drain;
+    uint64_t quarter[2];      // split items: the four warps of a group have handed something over
     uint64_t x_full, x_free;  // twin items: group 1's statistics stand in shared memory; group 0 is done
     uint32_t tmem;
     int stop;
@@ -216,9 +222,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Keys from `lim` on become -infinity.  `all` (at most any lane's lim): no lane's key before it does,
 // so groups of 16 below it are left alone (two instructions an element at half rate: a diagonal
 // block took twice as long as the others).
-__device__ __forceinline__ void mask64(uint32_t (&s)[64], int lim, int all) {
+template <int N> __device__ __forceinline__ void mask64(uint32_t (&s)[N], int lim, int all) {
 #pragma unroll
-    for (int k0 = 0; k0 < 64; k0 += 16)
+    for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 + 16 > all) {
 #pragma unroll
             for (int k = k0; k < k0 + 16; k++)
@@ -226,19 +232,19 @@ __device__ __forceinline__ void mask64(uint32_t (&s)[64], int lim, int all) {
         }
 }
 
-__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
+template <int N> __device__ __forceinline__ float max64(const uint32_t (&s)[N]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int k = 0; k < 64; k += 8)
+    for (int k = 0; k < N; k += 8)
 #pragma unroll
         for (int q = 0; q < 4; q++) m[q] = max3(m[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
 // Keys before `low` become -infinity.  `all`: at least any lane's low.
-__device__ __forceinline__ void mask64_low(uint32_t (&s)[64], int low, int all) {
+template <int N> __device__ __forceinline__ void mask64_low(uint32_t (&s)[N], int low, int all) {
 #pragma unroll
-    for (int k0 = 0; k0 < 64; k0 += 16)
+    for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 < all) {
 #pragma unroll
             for (int k = k0; k < k0 + 16; k++)
@@ -246,78 +252,111 @@ __device__ __forceinline__ void mask64_low(uint32_t (&s)[64], int low, int all) 
         }
 }
 
-__device__ __forceinline__ float absmax64(const uint32_t (&s)[64]) {
+template <int N> __device__ __forceinline__ float absmax64(const uint32_t (&s)[N]) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 64; k += 8)
+    for (int k = 0; k < N; k += 8)
 #pragma unroll
         for (int q = 0; q < 4; q++)
             m[q] = max3(m[q], fabsf(__uint_as_float(s[k + 2 * q])), fabsf(__uint_as_float(s[k + 2 * q + 1])));
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// tanh(y) = y (1 + z Q(z)), z = y^2, for |y| <= 1: Q of degree 4 with the least largest relative error
-// on [0, 1] (reweighted least squares), 6.7e-7 = 2^-20.5.  Beyond, 1 - 2 / (1 + e^(2 |y|)) with the
-// SFU's exponential and reciprocal, 2^-22 off.  A relative error, so the cap may be as large as it
-// likes.
-constexpr float kTanh0 = -0.3333028f, kTanh1 = 0.1328849f, kTanh2 = -0.05176828f, kTanh3 = 0.0169064f, kTanh4 = -0.00312657f;
+// Capped scores.  tanh(y) = y (1 + z Q(z)), z = y^2: with Q of degree 2 where |y| <= 1/2 and of degree 4
+// where |y| <= 1 (least largest relative error, by reweighted least squares: 2^-20.5 both), and beyond
+// 1 - 2 / (1 + e^(2 |y|)) with the SFU's exponential and reciprocal, 2^-22 off.  A relative error, so the
+// cap may be as large as it likes.  Scale, cap and log2(e) are multiplied into the polynomial's
+// coefficients (RowsScores), so that a score is s P(s^2) + off of the product s = q . k.
 __device__ __forceinline__ float tanh_large(float y) {
     float e = fast_exp2(2.8853900817779268f * fabsf(y)), r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return copysignf(fmaf(-2.0f, r, 1.0f), y);
 }
-__device__ __forceinline__ uint64_t tanh2_small(uint64_t y) {
-    const uint64_t z = mul2(y, y);
-    uint64_t q = fma2(z, pack2(kTanh4, kTanh4), pack2(kTanh3, kTanh3));
-    q = fma2(z, q, pack2(kTanh2, kTanh2));
-    q = fma2(z, q, pack2(kTanh1, kTanh1));
-    q = fma2(z, q, pack2(kTanh0, kTanh0));
-    return fma2(mul2(y, z), q, y);
+// 0: every |s| of the warp is below half the cap (in its units), 1: below it, 2: some are above.
+__device__ __forceinline__ int cap_tier(const RowsScores &sc, float most) {
+    return __all_sync(0xffffffffu, most <= sc.half_cap) ? 0 : __all_sync(0xffffffffu, most <= sc.one_cap) ? 1 : 2;
 }
-__device__ __forceinline__ float tanh_any(float y) {
+template <int TIER> __device__ __forceinline__ uint64_t cap_poly(const RowsScores &sc, float c, uint64_t v) {
+    const uint64_t z = mul2(v, v);
+    uint64_t q;
+    if (TIER == 0) {
+        q = pack2(sc.poly3[2], sc.poly3[2]);
+#pragma unroll
+        for (int i = 1; i >= 0; i--) q = fma2(z, q, pack2(sc.poly3[i], sc.poly3[i]));
+    } else {
+        q = pack2(sc.poly5[4], sc.poly5[4]);
+#pragma unroll
+        for (int i = 3; i >= 0; i--) q = fma2(z, q, pack2(sc.poly5[i], sc.poly5[i]));
+    }
+    return fma2(z, q, pack2(c, c));  // of s
+}
+__device__ __forceinline__ float cap_any(const RowsScores &sc, float c, float v) {
+    if (fabsf(v) > sc.one_cap) return sc.cap_log2 * tanh_large(v * sc.cap_in);
     float a, b;
-    unpack2(tanh2_small(pack2(y, y)), a, b);
-    return fabsf(y) <= 1.0f ? a : tanh_large(y);
+    unpack2(cap_poly<1>(sc, c, pack2(v, v)), a, b);
+    return v * a;
 }
 
-// The scores of 64 keys in the log2 domain, from q . k.  d0: the first key's position minus the
-// row's, as a float; sl: slope log2(e); small: no |q . k| of this warp's is above the cap; both: some
-// key may stand behind its row.
-template <int SCORE> __device__ __forceinline__ void scores64(uint32_t (&s)[64], const RowsScores &sc, float c, float sl, float d0,
-                                                              bool small, bool both) {
-    const uint64_t in2 = pack2(sc.cap_in, sc.cap_in), out2 = pack2(sc.cap_log2, sc.cap_log2), c2 = pack2(c, c);
-    const uint64_t sl2 = pack2(sl, sl), nsl2 = pack2(-sl, -sl);
-    const uint64_t d2 = pack2(d0, d0);
+// The scores of N keys in the log2 domain plus `off`, from q . k.  d0: the first key's position minus
+// the row's; sl: slope log2(e); both: some key may stand behind its row.
+template <int SCORE, int TIER, int N>
+__device__ __forceinline__ void score_pairs(uint32_t (&s)[N], const RowsScores &sc, float c, float sl, float d0, bool both,
+                                            float off) {
+    const float base = SCORE & kBiased ? fmaf(sl, d0, off) : off;
+    const uint64_t c2 = pack2(c, c), sl2 = pack2(sl, sl), base2 = pack2(base, base);
 #pragma unroll
-    for (int k = 0; k < 64; k += 2) {
-        uint64_t v = pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), f = c2;
+    for (int k = 0; k < N; k += 2) {
+        float a = __uint_as_float(s[k]), b = __uint_as_float(s[k + 1]);
+        uint64_t v = pack2(a, b), f = c2, add = base2;
         if (SCORE & kCapped) {
-            v = mul2(v, in2);
-            if (small) {
-                v = tanh2_small(v);
+            if (TIER == 2) {
+                v = pack2(cap_any(sc, c, a), cap_any(sc, c, b));
+                f = pack2(1.f, 1.f);
             } else {
-                float a, b;
-                unpack2(v, a, b);
-                v = pack2(tanh_any(a), tanh_any(b));
+                f = cap_poly<TIER>(sc, c, v);
             }
-            f = out2;
         }
         if (SCORE & kBiased) {
-            uint64_t d = add2(d2, pack2((float)k, (float)(k + 1)));  // t - p
-            if (both) {
-                float a, b;
-                unpack2(d, a, b);
-                v = fma2(v, f, mul2(nsl2, pack2(fabsf(a), fabsf(b))));
-            } else {
-                v = fma2(v, f, mul2(sl2, d));
-            }
-        } else {
-            v = mul2(v, f);
+            if (both)  // -sl |d|
+                add = pack2(fmaf(-sl, fabsf(d0 + (float)k), off), fmaf(-sl, fabsf(d0 + (float)(k + 1)), off));
+            else       // d <= 0 wherever it counts
+                add = fma2(pack2((float)k, (float)(k + 1)), sl2, base2);
         }
-        float a, b;
-        unpack2(v, a, b);
+        unpack2(fma2(v, f, add), a, b);
         s[k] = __float_as_uint(a);
         s[k + 1] = __float_as_uint(b);
+    }
+}
+template <int SCORE, int N>
+__device__ __forceinline__ void scores(uint32_t (&s)[N], const RowsScores &sc, float c, float sl, float d0, int tier, bool both,
+                                       float off) {
+    if (!(SCORE & kCapped) || tier == 0)
+        score_pairs<SCORE, 0>(s, sc, c, sl, d0, both, off);
+    else if (tier == 1)
+        score_pairs<SCORE, 1>(s, sc, c, sl, d0, both, off);
+    else
+        score_pairs<SCORE, 2>(s, sc, c, sl, d0, both, off);
+}
+
+// The most that a distance's term comes to in the 64 keys from d0 (their first position minus the row's) on.
+__device__ __forceinline__ float bias_most(float sl, float d0) {
+    const float a = fabsf(d0), b = fabsf(d0 + 63.f), far = fmaxf(a, b);
+    const float near = d0 > 0.f || d0 < -63.f ? fminf(a, b) : 0.f;
+    return -sl * (sl > 0.f ? near : far);
+}
+
+// P = 2^S of 64 keys: added to the sums, and as bf16 pairs to tensor memory.
+__device__ __forceinline__ void exps64(const uint32_t (&s)[64], uint64_t (&sum)[2], uint32_t addr) {
+#pragma unroll
+    for (int k0 = 0; k0 < 64; k0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            const float a = fast_exp2(__uint_as_float(s[k0 + k])), b = fast_exp2(__uint_as_float(s[k0 + k + 1]));
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+            pk[k / 2] = pack_bf16x2(a, b);
+        }
+        tmem_st16(addr + k0 / 2, pk);
     }
 }
 
@@ -378,7 +417,7 @@ __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, int *sta
 // The blocks of a piece that softmax group i works on, and its tokens: its own tile's, or (twin)
 // every second block of tile 0's.
 struct TileView {
-    bool twin;
+    bool twin, split;
     int n, tok0, ntok;  // blocks; first token in the sequence; tokens
     int first, step;    // block j is first + j step
 };
@@ -388,6 +427,7 @@ __device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece
     TileView v;
     const int left = sr.n - p.t * PT;  // tokens from the item's first on, at least 1
     v.twin = TWIN && left <= TT;
+    v.split = false;
     if (v.twin) {
         v.tok0 = p.t * PT;
         v.ntok = left;
@@ -408,14 +448,15 @@ inline size_t tc_lengths_bytes(int nseq, bool spans) {
     return (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 + (spans ? masked_bytes(nseq) + 16 : 0);
 }
 
-__host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages) {
-    return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16 + (HDP == 64 ? 1024 : 0);
+__host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool spans) {
+    return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16 +
+           (HDP == 64 ? 1024 + (spans ? 3072 : 0) : 0);
 }
 
 // ------------------------------------------------------------------ the kernel
 
 template <int HDP, bool PAGED, int SCORE>
-__global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
+__global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
     constexpr int NP = HDP / 64;  // 64-column panels of a [128][head_dim] operand
     // Tensor memory columns: S 128 i, O 256 + HDP i.  P (64 columns) has its own where O leaves
     // room, else the upper half of S, which the softmax holds in registers by then.
@@ -433,9 +474,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     uint8_t *base = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sq = base;                             // [2 tiles][NP][128][64]
     uint8_t *ring = base + 2 * NP * kPanel;         // [stages][NP][128][64]
+    // Split items (kSpans) put their weights where the second tile's queries go: of group i from
+    // kSplitP i on, [2 panels of 64 keys][32 rows], swizzled like the other operands.
+    constexpr int kSplitP = 8192;
+    uint8_t *split_p = sq + NP * kPanel;
     TcBars *B = (TcBars *)(ring + (size_t)T.stages * NP * kPanel);
     float *xm = (float *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);  // [128] maxima, [128] sums
-    long long *wstart = (long long *)(xm + (kTwin ? 256 : 0));
+    // split items: of each group maxima [2][4 warps][32] and sums [4][32]; 128-wide heads have one group,
+    // and its numbers behind its weights
+    float *split_x = kTwin ? xm + 256 : (float *)(split_p + 24576);
+    long long *wstart = (long long *)(xm + (kTwin ? 256 + (kSpans ? 2 * 384 : 0) : 0));
     SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
     volatile int *stop = &B->stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -457,6 +505,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             mbar_init(&B->o_full[i], o_arrivals);
         }
         mbar_init(&B->drain, 1);
+        mbar_init(&B->quarter[0], 4);
+        mbar_init(&B->quarter[1], 4);
         mbar_init(&B->x_full, 4);
         mbar_init(&B->x_free, 4);
         B->stop = 0;
@@ -474,12 +524,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     Walk w;
     if constexpr (kSpans) {
         MaskedShared *ms = (MaskedShared *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, w, tid, kTcThreads);
+        masked_layout(A, seq, wstart, ms, (int *)ring, w, tid, tc_threads(SCORE));
         const long long unit = range_units(wstart[A.nseq], A.P);
         w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
     } else {
-        rows_layout(A, seq, wstart, tid, kTcThreads);  // ends with a __syncthreads()
+        rows_layout(A, seq, wstart, tid, tc_threads(SCORE));  // ends with a __syncthreads()
     }
+    // an item of at most 32 rows is split by keys over the four warps of a group
+    auto view = [&](const SeqRows &sr, const RowsPiece &p, int i, int prefix) {
+        TileView v = tile_view<kTwin>(sr, p, TT, PT, i, prefix);
+        if (kSpans) v.split = (sr.n - p.t * PT) * G <= 32;
+        return v;
+    };
     auto prefix_of = [&](int s) {  // positions that all rows of the sequence see
         if constexpr (kSpans)
             return w.mask.prefix[s];
@@ -504,25 +560,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     RowsPiece p;
 
     if (warp < 8) {
+        if constexpr (kSpans) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------------------------- softmax, a thread per row
         const int i = warp >> 2, r = tid & 127;                 // tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + 128 * i, tP = tmem + lanes + kP + kPStep * i, tO = tmem + lanes + kO + HDP * i;
-        const int tok = r / G, head = r - tok * G;
+        const int tile_tok = r / G, few_tok = lane / G;  // the row's token; in a split item
         const float c = A.scale_log2;
         const float mu = kX ? 1.0f : c;   // of m, to the log2 domain
         uint32_t sp = 0, op = 0, xp = 0;  // phases of s_full; of both o_full (bit i); of x_full, x_free
         bool lent = false;                // group 1: group 0 may still read O and xm, xl of a twin item
         bool joined = false;
+        const int wq = warp & 3;  // split items: the warp's quarter of a block's keys
+        uint32_t hp = 0;          // phase of `quarter`
         RowsPiece ahead;  // the next piece, found while the tensor core finishes this one
         bool more = w.next(seq, A.nseq, A.geom, ahead);
         while (more) {
             p = ahead;
             const SeqRows sr = seq[p.s];
             const int pre = prefix_of(p.s);
-            const TileView v = tile_view<kTwin>(sr, p, TT, PT, i, pre);
+            const TileView v = view(sr, p, i, pre);
             const bool whole = p.begins() && p.ends();
-            const bool valid = tok < v.ntok && r < TT * G;
+            const int tok = kSpans && v.split ? few_tok : tile_tok, head = (kSpans && v.split ? lane : r) - tok * G;
+            const bool valid = tok < v.ntok && (kSpans && v.split ? lane < v.ntok * G : r < TT * G);
             const bool busy = __any_sync(0xffffffffu, valid);    // else only the hand-offs
             const int pos = sr.ctx + v.tok0 + tok;
             int from = 0, seen = pos + 1;  // the row sees positions [from, seen)
@@ -539,7 +599,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             if (v.twin) {
                 op ^= p.kb1 - p.kb0 > 1 ? 3u : (uint32_t)(!kSpans || p.kb1 > p.kb0);
             } else {
-                const TileView u = tile_view<kTwin>(sr, p, TT, PT, 1 - i, pre);
+                const TileView u = view(sr, p, 1 - i, pre);
                 op ^= (uint32_t)(v.n > 0) << i | (uint32_t)(u.n > 0) << (1 - i);
             }
             if (i == 1 && lent && v.n > 0) {
@@ -554,6 +614,92 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             for (int j = 0; j < v.n; j++) {
                 if (!(ok = tc_wait(&B->s_full[i], sp, A.status, stop))) break;
                 sp ^= 1;
+                if (kSpans && v.split) {
+                    // The four warps hold the same 32 rows, and each works on 32 keys of the block: their
+                    // maxima and, at the end, sums meet in shared memory, and so do their weights, which
+                    // the tensor core takes from there.
+                    tc_after();
+                    __syncwarp();
+                    float *xs = split_x + 384 * i;
+                    const int t0 = (v.first + j * v.step) * kTcBlk + 32 * wq;
+                    uint32_t x[32];
+                    tmem_ld32(tS + 32 * wq, x);
+                    const int lim = seen - t0, low = from - t0;
+                    int tier = 0;
+                    if (kCap) tier = cap_tier(A.sc, absmax64(x));
+                    if (kX) scores<SCORE>(x, A.sc, c, sl, (float)(t0 - pos), tier, kBias && pre > 0, 0.f);
+                    const int all = __reduce_min_sync(0xffffffffu, lim), low_all = __reduce_max_sync(0xffffffffu, low);
+                    if (all < 32) mask64(x, lim, all);
+                    if (low_all > 0) mask64_low(x, low, low_all);
+                    xs[(j & 1) * 128 + 32 * wq + lane] = max64(x);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&B->quarter[i]);
+                    if (!(ok = tc_wait(&B->quarter[i], hp, A.status, stop))) break;
+                    hp ^= 1;
+                    const float *xr = xs + (j & 1) * 128 + lane;
+                    const float mb = fmaxf(fmaxf(xr[0], xr[32]), fmaxf(xr[64], xr[96]));
+                    if (j == 0) {
+                        m = mb;
+                    } else {
+                        const bool grow = m == -INFINITY ? mb > m : (mb - m) * mu > kTcSlack;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float f = grow ? fast_exp2((m - mb) * mu) : 1.0f;
+                            if (grow) m = mb;
+                            l *= f;
+                            if (wq == 0) {
+#pragma unroll 1
+                                for (int d = 0; d < HDP; d += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32(tO + d, o);
+#pragma unroll
+                                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                    tmem_st32(tO + d, o);
+                                }
+                                tmem_wait_st();
+                            }
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.f : m * mu;
+                    const uint64_t c2 = pack2(mu, mu), mc2 = pack2(-mc, -mc);
+                    uint64_t sum[2] = {0, 0};
+                    // row `lane`, 16-byte chunk 4 (wq & 1) + q of its 128 bytes in panel wq >> 1
+                    const uint32_t dst = smem_addr(split_p) + kSplitP * i + 4096 * (wq >> 1) + 128 * lane;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            float a, b;
+                            unpack2(fma2(pack2(__uint_as_float(x[8 * q + k]), __uint_as_float(x[8 * q + k + 1])), c2, mc2), a, b);
+                            a = fast_exp2(a);
+                            b = fast_exp2(b);
+                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+                            w[k / 2] = pack_bf16x2(a, b);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((4 * (wq & 1) + q) ^ (lane & 7)) << 4)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    float a, b;
+                    unpack2(add2(sum[0], sum[1]), a, b);
+                    l += a + b;
+                    if (j == v.n - 1) {  // before the last weights go: then this memory may be the producer's
+                        xs[256 + 32 * wq + lane] = l;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&B->quarter[i]);
+                        if (!(ok = tc_wait(&B->quarter[i], hp, A.status, stop))) break;
+                        hp ^= 1;
+                        l = (xs[256 + lane] + xs[288 + lane]) + (xs[320 + lane] + xs[352 + lane]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&B->p_half[i]);
+                        mbar_arrive(&B->p_ready[i]);
+                    }
+                    continue;
+                }
                 if (busy) {
                     tc_after();
                     __syncwarp();
@@ -576,23 +722,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                         if (cut_low) mask64_low(hi, low - 64, low_all - 64);
                     };
                     float mb;
-                    // scores: the distance of the block's first key; whether keys may stand behind rows
+                    // the distance of the block's first key; whether keys may stand behind rows
                     float d0 = 0.f;
-                    bool both = false, small = true;
-                    if constexpr (kX) {
+                    bool both = false;
+                    int tier = 0;
+                    if constexpr (kBias) {
                         const int t0 = (v.first + j * v.step) * kTcBlk;
                         d0 = (float)(t0 - pos);
-                        both = kBias && pre > 0 && __any_sync(0xffffffffu, t0 + kTcBlk - 1 > pos);
+                        both = pre > 0 && __any_sync(0xffffffffu, t0 + kTcBlk - 1 > pos);
+                    }
+                    if constexpr (kX) {
+                        // Of the products, the largest: tanh is monotone, and a distance's term is at most
+                        // bias_most.  That bound of the maximum is at most 63 |sl| above it (96 where it is
+                        // taken, so that weights of 2^-24 of the largest stay normal numbers); steeper
+                        // slopes have their scores worked out for it.
+                        const bool steep = kBias && __any_sync(0xffffffffu, fabsf(sl) > 96.f / 63.f);
+                        float most = 0.f;
+                        auto largest = [&](uint32_t (&x)[64], float d) {
+                            float y = max64(x);
+                            if (y == -INFINITY) return y;
+                            y = kCap ? cap_any(A.sc, c, y) : y * c;
+                            return kBias ? y + bias_most(sl, d) : y;
+                        };
                         tmem_ld64(tS, lo);
-                        if (kCap) small = __all_sync(0xffffffffu, absmax64(lo) * A.sc.cap_in <= 1.0f);
-                        scores64<SCORE>(lo, A.sc, c, sl, d0, small, both);
+                        if (kCap) most = absmax64(lo);
                         mask_lo();
-                        mb = max64(lo);
+                        mb = largest(lo, d0);
                         tmem_ld64(tS + 64, hi);
-                        const bool small_hi = kCap && __all_sync(0xffffffffu, absmax64(hi) * A.sc.cap_in <= 1.0f);
-                        scores64<SCORE>(hi, A.sc, c, sl, d0 + 64.f, small_hi, both);
+                        if (kCap) {
+                            most = fmaxf(most, absmax64(hi));
+                            tier = cap_tier(A.sc, most);
+                        }
                         mask_hi();
-                        mb = fmaxf(mb, max64(hi));
+                        mb = fmaxf(mb, largest(hi, d0 + 64.f));
+                        if (steep) {
+                            scores<SCORE>(lo, A.sc, c, sl, d0, tier, both, 0.f);
+                            mask_lo();
+                            mb = max64(lo);
+                            tmem_ld64(tS + 64, lo);
+                            scores<SCORE>(lo, A.sc, c, sl, d0 + 64.f, tier, both, 0.f);
+                            if (cut) mask64(lo, lim - 64, all - 64);
+                            if (cut_low) mask64_low(lo, low - 64, low_all - 64);
+                            mb = fmaxf(mb, max64(lo));
+                        }
                     } else {
                         tmem_ld64(tS, lo);
                         mask_lo();
@@ -622,16 +794,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     const float mc = m == -INFINITY ? 0.f : m * mu;
                     const uint64_t c2 = pack2(mu, mu), mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {0, 0};  // two packed pairs of fp32 zeros
-                    weights64(hi, c2, mc2, sum, tP + 32);
+                    if constexpr (kX) {
+                        scores<SCORE>(hi, A.sc, c, sl, d0 + 64.f, tier, both, -mc);
+                        mask_hi();
+                        exps64(hi, sum, tP + 32);
+                    } else {
+                        weights64(hi, c2, mc2, sum, tP + 32);
+                    }
                     tmem_wait_st();  // keys 64-127: the tensor core can begin
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&B->p_half[i]);
                     __syncwarp();
                     tmem_ld64(tS, lo);
-                    if constexpr (kX) scores64<SCORE>(lo, A.sc, c, sl, d0, small, both);
-                    mask_lo();
-                    weights64(lo, c2, mc2, sum, tP);
+                    if constexpr (kX) {
+                        scores<SCORE>(lo, A.sc, c, sl, d0, tier, both, -mc);
+                        mask_lo();
+                        exps64(lo, sum, tP);
+                    } else {
+                        mask_lo();
+                        weights64(lo, c2, mc2, sum, tP);
+                    }
                     float a, b;
                     unpack2(add2(sum[0], sum[1]), a, b);
                     l += a + b;
@@ -650,8 +833,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             const bool both = v.twin && p.kb1 - p.kb0 > 1;
             float f0 = 1.0f, f1 = 0.0f;
             if (both && i == 1) {
-                xm[r] = m;
-                xm[128 + r] = l;
+                if (!kSpans || !v.split || wq == 0) {
+                    xm[r] = m;
+                    xm[128 + r] = l;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->x_full);
                 lent = true;
@@ -668,7 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 l = l * f0 + xm[128 + r] * f1;
                 m = M;
             }
-            if (!busy || (v.twin && i == 1)) {
+            if (!busy || (v.twin && i == 1) || (kSpans && v.split && wq > 0)) {
                 __syncwarp();
                 if (both && lane == 0) mbar_arrive(&B->x_free);
                 continue;
@@ -740,7 +925,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             if (both && lane == 0) mbar_arrive(&B->x_free);
         }
         if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
+    } else if (kSpans && warp >= 10) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     } else if (warp == 8) {
+        if constexpr (kSpans) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- tensor core
         constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
         const int ksteps = (A.hd + 15) / 16;
@@ -772,9 +960,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             for (int k = 0; k < 4; k++)
                 mma_ts(tmem + kO + HDP * i, a + 8 * (4 * half + k), b + (4 * half + k) * 128, idO, !(first && k == 0));
         };
+        auto issue_split_o = [&](int i, bool first) {  // O_i (+)= P_i V, all keys, P_i in shared memory
+            const uint32_t b = dv + vs * (NP * kPanel / 16), a = desc_lo(split_p + kSplitP * i, 16);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                mma_ss(tmem + kO + HDP * i, a + (k >> 2) * (4096 / 16) + (k & 3) * 2, b + k * 128, idO, !(first && k == 0));
+        };
         // P_i V for one block of group i; `last`: O_i is complete
-        auto weigh = [&](int i, bool first, bool last) {
+        auto weigh = [&](int i, bool first, bool last, bool split) {
             if (!tc_wait(&B->p_half[i], pph >> i & 1, A.status, stop)) return false;
+            if (kSpans && split) {
+                if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
+                pph ^= 1u << i;
+                tc_after();
+                if (elect_one()) {
+                    issue_split_o(i, first);
+                    if (last) tc_commit(&B->o_full[i]);
+                }
+                return true;
+            }
             tc_after();
             if (elect_one()) issue_o(i, 1, first);
             if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
@@ -823,7 +1027,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             const int tail = p.ends() ? item_to(sr, p) - (p.kb1 - 1) * kTcBlk : kTcBlk;  // of the last block
             const int head = kSpans && p.begins() ? item_from(sr, p) - p.kb0 * kTcBlk : 0;  // of the first one
             const int pre = prefix_of(p.s);
-            const TileView v0 = tile_view<kTwin>(sr, p, TT, PT, 0, pre);
+            const TileView v0 = view(sr, p, 0, pre);
+            if (kSpans && v0.split) {  // the second tile's place holds weights
+                if (!(ok = tc_wait(&B->q_full[1], qph >> 1 & 1, A.status, stop))) break;
+                qph ^= 2;
+            }
             if (v0.twin) {
                 // one tile: block b belongs to group b & 1
                 auto score = [&](int b) {
@@ -843,13 +1051,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = score(0)) || (n > 1 && !(ok = score(1)))) break;
                 another = w.next(seq, A.nseq, A.geom, ahead);
                 for (int b = 0; b < n; b++) {
-                    if (!(ok = take_v(b == 0 ? head : 0, b == n - 1 ? tail : kTcBlk)) || !(ok = weigh(b & 1, b < 2, b + 2 >= n))) break;
+                    if (!(ok = take_v(b == 0 ? head : 0, b == n - 1 ? tail : kTcBlk)) || !(ok = weigh(b & 1, b < 2, b + 2 >= n, v0.split))) break;
                     drop_v();
                     if (b + 2 < n && !(ok = score(b + 2))) break;
                 }
+                if (kSpans && ok && v0.split && elect_one()) tc_commit(&B->q_empty[1]);
                 continue;
             }
-            const int nt[2] = {v0.n, tile_view<kTwin>(sr, p, TT, PT, 1, pre).n};
+            const int nt[2] = {v0.n, view(sr, p, 1, pre).n};
             if (!(ok = tc_wait(&B->kv_full[ks], kph, A.status, stop))) break;
 #pragma unroll
             for (int i = 0; i < 2; i++) {
@@ -872,7 +1081,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 const bool more = j + 1 < n;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    if (j < nt[i] && !(ok = weigh(i, j == 0, j == nt[i] - 1))) break;
+                    if (j < nt[i] && !(ok = weigh(i, j == 0, j == nt[i] - 1, v0.split))) break;
                     if (i == 1) drop_v();
                     if (i == 0 && more) {
                         if (!(ok = tc_wait(&B->kv_full[ks], kph, A.status, stop))) break;
@@ -887,6 +1096,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!ok) break;
                 if (more) drop_k();
             }
+            if (kSpans && ok && v0.split && elect_one()) tc_commit(&B->q_empty[1]);
         }
         // What was issued has run, and its commits have arrived, before the CTA gives up its tensor and
         // shared memory -- in an abandoned call too, whoever gives up and however late.
@@ -898,7 +1108,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp == 9) {
+        if constexpr (kSpans) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- TMA producer
+        if constexpr (kSpans) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // masked_layout's scratch
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
         uint32_t qn[2] = {0, 0};              // query tiles loaded so far
         bool ok = true;
@@ -948,7 +1160,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     if (kb == p.kb0 && is_v == 0) {  // the queries, behind the first keys
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
-                            const TileView v = tile_view<kTwin>(sr, p, TT, PT, i, pre);
+                            const TileView v = view(sr, p, i, pre);
+                            if (kSpans && v.split) {
+                                if (qn[i] > 0 && !(ok = tc_wait(&B->q_empty[i], (qn[i] - 1) & 1, A.status, stop))) break;
+                                qn[i]++;
+                                if (i == 1) {  // lent to the weights
+                                    if (lane == 0) mbar_arrive(&B->q_full[1]);
+                                } else if (lane == 0) {  // the rows once for each warp
+                                    const int few = 32 / G;
+                                    mbar_expect_tx(&B->q_full[0], (uint32_t)(NP * 4 * few * G * 128));
+#pragma unroll
+                                    for (int pn = 0; pn < NP; pn++)
+#pragma unroll
+                                        for (int q = 0; q < 4; q++)
+                                            tma_3d(sq + (size_t)pn * kPanel + q * 4096, &T.q_few, pn * 64, p.g * G, sr.row0 + v.tok0,
+                                                   &B->q_full[0]);
+                                }
+                                __syncwarp();
+                                continue;
+                            }
                             if (v.n == 0 || (v.twin && i == 1)) continue;
                             if (qn[i] > 0 && !(ok = tc_wait(&B->q_empty[i], (qn[i] - 1) & 1, A.status, stop))) break;
                             qn[i]++;
@@ -993,7 +1223,7 @@ static int tc_stages(int hd, int nseq, bool spans) {
     // sequences: 20 KB)
     const int HDP = hd <= 64 ? 64 : 128;
     int n = HDP == 64 ? 10 : 5;
-    while (tc_fixed_bytes(HDP, n) + tc_lengths_bytes(nseq, spans) > kSmemLimit) n--;
+    while (tc_fixed_bytes(HDP, n, spans) + tc_lengths_bytes(nseq, spans) > kSmemLimit) n--;
     return n;
 }
 
@@ -1002,12 +1232,13 @@ static int tc_stages(int hd, int nseq, bool spans) {
 // without one.
 template <int HDP, bool PAGED, int SCORE> static cudaError_t launch_tc(RowsTcArgs &t, cudaStream_t s) {
     const RowsArgs &a = t.a;
-    const size_t smem = tc_fixed_bytes(HDP, t.stages) + tc_lengths_bytes(a.nseq, SCORE != 0);
+    const size_t smem = tc_fixed_bytes(HDP, t.stages, SCORE != 0) + tc_lengths_bytes(a.nseq, SCORE != 0);
     cudaError_t e = allow_smem((const void *)rows_tc_kernel<HDP, PAGED, SCORE>);
     const uint64_t hb = (uint64_t)a.hd * 2;  // bytes of a head
     const uint64_t qd[] = {(uint64_t)a.hd, (uint64_t)a.H, (uint64_t)a.rows}, qs[] = {hb, (uint64_t)a.q_ld * 2};
-    const uint32_t qb[] = {64, (uint32_t)a.G, (uint32_t)t.TT};
+    const uint32_t qb[] = {64, (uint32_t)a.G, (uint32_t)t.TT}, qf[] = {64, (uint32_t)a.G, (uint32_t)std::max(1, 32 / a.G)};
     if (e == cudaSuccess) e = make_bf16_map_nd(&t.q, a.q, 3, qd, qs, qb);
+    if (e == cudaSuccess && SCORE) e = make_bf16_map_nd(&t.q_few, a.q, 3, qd, qs, qf);
     if (PAGED) {
         const uint64_t page = 1ull << a.kv.page_shift;
         t.box = page < kTcBlk ? (int)page : kTcBlk;
@@ -1025,7 +1256,7 @@ template <int HDP, bool PAGED, int SCORE> static cudaError_t launch_tc(RowsTcArg
         if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 3, d, vs, b);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(kTcThreads), smem, s, t);
+    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(tc_threads(SCORE)), smem, s, t);
 }
 
 static RowsTcArgs tc_args(const RowsArgs &a, bool spans) {

@@ -222,6 +222,18 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
         if (sc->cap > 0.f) {
             a.sc.cap_in = (float)std::min(scale / sc->cap, most);
             a.sc.cap_log2 = (float)std::max(std::min(1.4426950408889634074 * sc->cap, most), 1.401298464324817e-45);
+            // products whose square stays finite
+            a.sc.half_cap = (float)std::min(0.5 * sc->cap / scale, 1e15);
+            a.sc.one_cap = (float)std::min(sc->cap / scale, 1e15);
+            // tanh(y) = y (1 + y^2 Q(y^2)) (rows_attention_tc.cuh), of q . k
+            static const double q3[3] = {-0.333281593, 0.132053596, -0.044750641}, q5[5] = {-0.333302797, 0.132884901, -0.051768282, 0.0169064046, -0.00312657604};
+            const double in = scale / sc->cap;
+            double f = 1.4426950408889634074 * scale;
+            for (int i = 0; i < 5; i++) {
+                f *= in * in;
+                if (i < 3) a.sc.poly3[i] = (float)std::max(-most, std::min(f * q3[i], most));
+                a.sc.poly5[i] = (float)std::max(-most, std::min(f * q5[i], most));
+            }
         }
     }
     const bool bf16 = dtype == SLM_BF16;
