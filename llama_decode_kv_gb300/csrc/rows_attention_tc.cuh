@@ -298,12 +298,11 @@ __device__ __forceinline__ float cap_any(const RowsScores &sc, float c, float v)
 }
 
 // The scores of N keys in the log2 domain plus `off`, from q . k.  d0: the first key's position minus
-// the row's; sl: slope log2(e); both: some key may stand behind its row.
-template <int SCORE, int TIER, int N>
-__device__ __forceinline__ void score_pairs(uint32_t (&s)[N], const RowsScores &sc, float c, float sl, float d0, bool both,
-                                            float off) {
+// the row's; sl: slope log2(e); BOTH: some key may stand behind its row.
+template <int SCORE, int TIER, bool BOTH, int N>
+__device__ __forceinline__ void score_pairs(uint32_t (&s)[N], const RowsScores &sc, float c, float sl, float d0, float off) {
     const float base = SCORE & kBiased ? fmaf(sl, d0, off) : off;
-    const uint64_t c2 = pack2(c, c), sl2 = pack2(sl, sl), base2 = pack2(base, base);
+    const uint64_t c2 = pack2(c, c), base2 = pack2(base, base);
 #pragma unroll
     for (int k = 0; k < N; k += 2) {
         float a = __uint_as_float(s[k]), b = __uint_as_float(s[k + 1]);
@@ -317,10 +316,10 @@ __device__ __forceinline__ void score_pairs(uint32_t (&s)[N], const RowsScores &
             }
         }
         if (SCORE & kBiased) {
-            if (both)  // -sl |d|
+            if (BOTH)  // -sl |d|
                 add = pack2(fmaf(-sl, fabsf(d0 + (float)k), off), fmaf(-sl, fabsf(d0 + (float)(k + 1)), off));
             else       // d <= 0 wherever it counts
-                add = fma2(pack2((float)k, (float)(k + 1)), sl2, base2);
+                add = pack2(fmaf((float)k, sl, base), fmaf((float)(k + 1), sl, base));
         }
         unpack2(fma2(v, f, add), a, b);
         s[k] = __float_as_uint(a);
@@ -330,12 +329,20 @@ __device__ __forceinline__ void score_pairs(uint32_t (&s)[N], const RowsScores &
 template <int SCORE, int N>
 __device__ __forceinline__ void scores(uint32_t (&s)[N], const RowsScores &sc, float c, float sl, float d0, int tier, bool both,
                                        float off) {
-    if (!(SCORE & kCapped) || tier == 0)
-        score_pairs<SCORE, 0>(s, sc, c, sl, d0, both, off);
-    else if (tier == 1)
-        score_pairs<SCORE, 1>(s, sc, c, sl, d0, both, off);
+    // the branches stand outside the loops: within, both sides of them would be computed for every key
+    auto tiers = [&](auto b) {
+        constexpr bool BOTH = decltype(b)::value;
+        if (!(SCORE & kCapped) || tier == 0)
+            score_pairs<SCORE, 0, BOTH>(s, sc, c, sl, d0, off);
+        else if (tier == 1)
+            score_pairs<SCORE, 1, BOTH>(s, sc, c, sl, d0, off);
+        else
+            score_pairs<SCORE, 2, BOTH>(s, sc, c, sl, d0, off);
+    };
+    if ((SCORE & kBiased) && both)
+        tiers(std::true_type{});
     else
-        score_pairs<SCORE, 2>(s, sc, c, sl, d0, both, off);
+        tiers(std::false_type{});
 }
 
 // The most that a distance's term comes to in the 64 keys from d0 (their first position minus the row's) on.
@@ -422,11 +429,11 @@ struct TileView {
     int first, step;    // block j is first + j step
 };
 // prefix: positions that all rows see (masked items).
-template <bool TWIN>
-__device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece &p, int TT, int PT, int i, int prefix = 0) {
+__device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece &p, int TT, int PT, int i, int prefix,
+                                              bool twin) {
     TileView v;
     const int left = sr.n - p.t * PT;  // tokens from the item's first on, at least 1
-    v.twin = TWIN && left <= TT;
+    v.twin = twin && left <= TT;
     v.split = false;
     if (v.twin) {
         v.tok0 = p.t * PT;
@@ -450,7 +457,7 @@ inline size_t tc_lengths_bytes(int nseq, bool spans) {
 
 __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool spans) {
     return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16 +
-           (HDP == 64 ? 1024 + (spans ? 3072 : 0) : 0);
+           (HDP == 64 ? 1024 + (spans ? 3072 : 0) : spans ? 256 : 0);
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -479,11 +486,12 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     constexpr int kSplitP = 8192;
     uint8_t *split_p = sq + NP * kPanel;
     TcBars *B = (TcBars *)(ring + (size_t)T.stages * NP * kPanel);
-    float *xm = (float *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);  // [128] maxima, [128] sums
-    // split items: of each group maxima [2][4 warps][32] and sums [4][32]; 128-wide heads have one group,
-    // and its numbers behind its weights
+    float *xm = (float *)((uint8_t *)B + (sizeof(TcBars) + 15) / 16 * 16);  // maxima and sums of a twin item's rows
+    // split items: of each group maxima [2][4 warps][32] and sums [4][32]; for 128-wide heads behind the
+    // weights
     float *split_x = kTwin ? xm + 256 : (float *)(split_p + 24576);
-    long long *wstart = (long long *)(xm + (kTwin ? 256 + (kSpans ? 2 * 384 : 0) : 0));
+    constexpr int kXm = kTwin ? 128 : 32;  // rows of a twin item
+    long long *wstart = (long long *)(xm + (kTwin ? 256 + (kSpans ? 2 * 384 : 0) : kSpans ? 2 * kXm : 0));
     SeqRows *seq = (SeqRows *)(wstart + A.nseq + 1);
     volatile int *stop = &B->stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -530,10 +538,12 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     } else {
         rows_layout(A, seq, wstart, tid, tc_threads(SCORE));  // ends with a __syncthreads()
     }
-    // an item of at most 32 rows is split by keys over the four warps of a group
+    // an item of at most 32 rows is split by keys over the four warps of a group, and worked on twice
+    // over whatever its heads' width
     auto view = [&](const SeqRows &sr, const RowsPiece &p, int i, int prefix) {
-        TileView v = tile_view<kTwin>(sr, p, TT, PT, i, prefix);
-        if (kSpans) v.split = (sr.n - p.t * PT) * G <= 32;
+        const bool split = kSpans && (sr.n - p.t * PT) * G <= 32;
+        TileView v = tile_view(sr, p, TT, PT, i, prefix, kTwin || split);
+        v.split = split;
         return v;
     };
     auto prefix_of = [&](int s) {  // positions that all rows of the sequence see
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
             if (both && i == 1) {
                 if (!kSpans || !v.split || wq == 0) {
                     xm[r] = m;
-                    xm[128 + r] = l;
+                    xm[kXm + r] = l;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&B->x_full);
@@ -847,11 +857,13 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                 if (!tc_wait(&B->o_full[1], op0 >> 1 & 1, A.status, stop)) break;
                 if (!tc_wait(&B->x_full, xp, A.status, stop)) break;
                 xp ^= 1;
-                const float m1 = xm[r], M = fmaxf(m, m1);
-                f0 = m == -INFINITY ? 0.f : fast_exp2((m - M) * mu);
-                f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - M) * mu);
-                l = l * f0 + xm[128 + r] * f1;
-                m = M;
+                if (!kSpans || !v.split || wq == 0) {
+                    const float m1 = xm[r], M = fmaxf(m, m1);
+                    f0 = m == -INFINITY ? 0.f : fast_exp2((m - M) * mu);
+                    f1 = m1 == -INFINITY ? 0.f : fast_exp2((m1 - M) * mu);
+                    l = l * f0 + xm[kXm + r] * f1;
+                    m = M;
+                }
             }
             if (!busy || (v.twin && i == 1) || (kSpans && v.split && wq > 0)) {
                 __syncwarp();
