@@ -97,132 +97,133 @@ __device__ __forceinline__ void rows_layout(const RowsArgs &A, SeqRows *seq, lon
     __syncthreads();
 }
 
-// Masked items: the mask of sequence s; `prefix` stands in shared memory, cut to the sequence.
+// Masked items: the mask of sequence s, its prefix cut to the sequence.
 struct SeqMasks {
     const SeqRows *seq;
-    const int *prefix, *first;
+    const int *prefixes, *first;
     int window;
+    __device__ __forceinline__ int prefix(int s) const {
+        return prefixes ? min(max(__ldg(prefixes + s), 0), seq[s].ctx + seq[s].n) : 0;
+    }
     __device__ __forceinline__ RowsMask operator()(int s) const {
-        return RowsMask{first ? first + seq[s].row0 : nullptr, prefix[s], window};
+        return RowsMask{first ? first + seq[s].row0 : nullptr, prefix(s), window};
     }
 };
 typedef MaskedWalk<SeqMasks> RowsMaskedWalk;
 
-// Shared memory that masked_layout takes after seq and wstart; besides, nseq + 1 ints of scratch that
-// it is done with at its end.
-struct MaskedShared {
-    RowsStart start;
-    int prefix[1];  // [nseq]
-};
-__host__ __device__ inline size_t masked_bytes(int nseq) { return (sizeof(RowsStart) + (size_t)nseq * 4 + 15) / 16 * 16; }
+// Shared memory that masked_layout takes after seq and wstart (aligned to 16 bytes); besides, nseq + 1
+// ints of scratch that it is done with at its end.
+__host__ __device__ inline size_t masked_bytes() { return sizeof(RowsStart) + 16; }
 
-// rows_layout for masked items: their units are added up one by one, an equal share of them per
-// thread (8,192 rows of 4 heads per kv head are 128 items), and warp 0 looks for the item that this
-// CTA's range begins in.  Ends with a __syncthreads().
-__device__ __forceinline__ void masked_layout(const RowsArgs &A, SeqRows *seq, long long *wstart, MaskedShared *ms,
-                                              int *items, RowsMaskedWalk &w, int tid, int threads) {
-    int *prefix = ms->prefix;
+// The last s with a[s] <= x, of n.
+template <typename T> __device__ __forceinline__ int last_upto(const T *a, int n, T x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (a[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// a[1 .. n] become their inclusive sums times `times`, none above `most`; the last sum, uncut.  One warp.
+template <typename T> __device__ __forceinline__ long long running_sums(T *a, int n, long long times, long long most, int lane) {
+    long long carry = 0;
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        const int s = s0 + lane;
+        long long v = s < n ? a[s + 1] * times : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (s < n) a[s + 1] = (T)min(carry + v, most);
+        carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    return carry;
+}
+
+// rows_layout for masked items.  A sequence of one item has its units at once (a decode step); those of
+// several are added up item by item, an equal share of them per thread (8,192 rows of 4 heads per kv
+// head are 128 items).  Warp 0 looks for the item that this CTA's range begins in.  Ends with a
+// __syncthreads().
+__device__ __forceinline__ void masked_layout(const RowsArgs &A, SeqRows *seq, long long *wstart, RowsStart *start, int *items,
+                                              RowsMaskedWalk &w, int tid, int threads) {
+    w.mask = SeqMasks{seq, A.sc.prefix, A.sc.first, A.sc.window};
+    bool several = false;
     for (int s = tid; s < A.nseq; s += threads) {
         SeqRows r;
         const int a = __ldg(A.row_start + s), b = __ldg(A.row_start + s + 1);
         const int c = A.ctx_len ? __ldg(A.ctx_len + s) : 0;
         if (!seq_rows(a, b, c, A.rows, A.cap, r) && blockIdx.x == 0) atomicOr(A.status, SLM_ROWS_LENGTH);
         seq[s] = r;
-        prefix[s] = A.sc.prefix ? min(max(__ldg(A.sc.prefix + s), 0), r.ctx + r.n) : 0;
-        items[s + 1] = r.n > 0 ? item_count(A.geom, r.n) : 0;
-        wstart[s + 1] = 0;
+        const int n = r.n > 0 ? item_count(A.geom, r.n) : 0;
+        several |= n > 1;
+        items[s + 1] = n;
+        wstart[s + 1] = n == 1 ? A.geom.cost + item_span(A.geom, r, w.mask(s), 0).nb : 0;
     }
     if (tid == 0) wstart[0] = items[0] = 0;
-    __syncthreads();
-    if (tid < 32) {  // inclusive sums of items[1 ..]
-        // Row ranges that overlap (row_start descends somewhere, which has been reported) could claim
-        // any number of items; ranges that do not have at most this many.
-        const long long most = (long long)A.rows / A.geom.PT + A.nseq;
-        long long carry = 0;
-        for (int s0 = 0; s0 < A.nseq; s0 += 32) {
-            const int s = s0 + tid;
-            long long v = s < A.nseq ? items[s + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (tid >= o) v += u;
-            }
-            if (s < A.nseq) items[s + 1] = (int)min(carry + v, most);
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
-        if (carry > most) {  // no sequence has rows then: nothing is computed
-            for (int s = tid; s < A.nseq; s += 32) {
-                seq[s].n = 0;
-                items[s + 1] = 0;
+    if (__syncthreads_or(several)) {
+        if (tid < 32) {
+            // Row ranges that overlap (row_start descends somewhere, which has been reported) could
+            // claim any number of items; ranges that do not have at most this many.
+            const long long most = (long long)A.rows / A.geom.PT + A.nseq;
+            if (running_sums(items, A.nseq, 1, most, tid) > most) {  // nobody has rows then
+                __syncwarp();
+                for (int s = tid; s < A.nseq; s += 32) {
+                    seq[s].n = 0;
+                    items[s + 1] = 0;
+                    wstart[s + 1] = 0;
+                }
             }
         }
+        __syncthreads();
+        const int all = items[A.nseq], share = (all + threads - 1) / threads;
+        const int i1 = min(all, (tid + 1) * share);
+        int i = min(all, tid * share);
+        if (i < i1)
+            for (int s = last_upto(items, A.nseq, i); i < i1; s++) {
+                const int stop = min(i1, items[s + 1]);
+                if (i >= stop) continue;
+                const SeqRows r = seq[s];
+                const RowsMask m = w.mask(s);
+                unsigned long long units = 0;
+                const bool one = items[s + 1] - items[s] == 1;  // has its units
+                for (; i < stop; i++)
+                    if (!one) units += A.geom.cost + item_span(A.geom, r, m, i - items[s]).nb;
+                if (!one) atomicAdd((unsigned long long *)&wstart[s + 1], units);  // whole numbers: any order
+            }
+        __syncthreads();
     }
-    __syncthreads();
-    w.mask = SeqMasks{seq, prefix, A.sc.first, A.sc.window};
-    const int all = items[A.nseq], share = (all + threads - 1) / threads;
-    const int i1 = min(all, (tid + 1) * share);
-    int i = min(all, tid * share);
-    if (i < i1) {
-        int lo = 0, hi = A.nseq - 1;  // the last s with items[s] <= i
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (items[mid] <= i)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        for (int s = lo; i < i1; s++) {
-            const int stop = min(i1, items[s + 1]);
-            if (i >= stop) continue;
-            const SeqRows r = seq[s];
-            const RowsMask m = w.mask(s);
-            unsigned long long units = 0;
-            for (; i < stop; i++) units += A.geom.cost + item_span(A.geom, r, m, i - items[s]).nb;
-            atomicAdd((unsigned long long *)&wstart[s + 1], units);  // whole numbers: any order
-        }
-    }
-    __syncthreads();
     if (tid < 32) {
-        long long carry = 0;
-        for (int s0 = 0; s0 < A.nseq; s0 += 32) {
-            const int s = s0 + tid;
-            long long v = s < A.nseq ? wstart[s + 1] * A.KV : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if (tid >= o) v += u;
-            }
-            if (s < A.nseq) wstart[s + 1] = carry + v;
-            carry += __shfl_sync(0xffffffffu, v, 31);
-        }
+        running_sums(wstart, A.nseq, A.KV, 0x7fffffffffffffffLL, tid);
         __syncwarp();
         const long long total = wstart[A.nseq], x = range_units(total, A.P) * blockIdx.x;
         if (x < total) {
-            int lo = 0, hi = A.nseq - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (wstart[mid] <= x)
-                    lo = mid;
-                else
-                    hi = mid - 1;
-            }
-            const SeqRows r = seq[lo];
-            const RowsMask m = w.mask(lo);
-            const unsigned long long per = udiv(wstart[lo + 1] - wstart[lo], A.KV), g = udiv(x - wstart[lo], per);
-            long long at = wstart[lo] + (long long)(g * per);  // units before item t0 of this kv head
+            const int s = last_upto(wstart, A.nseq, x);
+            const SeqRows r = seq[s];
+            const RowsMask m = w.mask(s);
+            const unsigned long long per = udiv(wstart[s + 1] - wstart[s], A.KV), g = udiv(x - wstart[s], per);
+            long long at = wstart[s] + (long long)(g * per);  // units before item t0 of this kv head
             const int T = item_count(A.geom, r.n);
-            for (int t0 = 0; t0 < T; t0 += 32) {
-                const int t = t0 + tid, u = t < T ? A.geom.cost + item_span(A.geom, r, m, t).nb : 0;
-                long long v = u;
+            if (T == 1) {
+                if (tid == 0) *start = RowsStart{s, (int)g, 0, at};
+            } else {
+                for (int t0 = 0; t0 < T; t0 += 32) {
+                    const int t = t0 + tid, u = t < T ? A.geom.cost + item_span(A.geom, r, m, t).nb : 0;
+                    long long v = u;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, v, o);
-                    if (tid >= o) v += y;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+                        if (tid >= o) v += y;
+                    }
+                    const bool mine = u > 0 && at + v - u <= x && x < at + v;
+                    if (mine) *start = RowsStart{s, (int)g, t, at + v - u};
+                    if (__any_sync(0xffffffffu, mine)) break;
+                    at += __shfl_sync(0xffffffffu, v, 31);
                 }
-                const bool mine = u > 0 && at + v - u <= x && x < at + v;
-                if (mine) ms->start = RowsStart{lo, (int)g, t, at + v - u};
-                if (__any_sync(0xffffffffu, mine)) break;
-                at += __shfl_sync(0xffffffffu, v, 31);
             }
         }
     }

@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
     constexpr bool kSpans = SCORED;
     std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk> w;
     if constexpr (kSpans) {
-        MaskedShared *ms = (MaskedShared *)(((uintptr_t)(lrow + R) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, (int *)kv, w, tid, kSimtThreads);
+        RowsStart *start = (RowsStart *)(((uintptr_t)(lrow + R) + 15) & ~(uintptr_t)15);
+        masked_layout(A, seq, wstart, start, (int *)kv, w, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
-        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
+        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), *start);
     } else {
         rows_layout(A, seq, wstart, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kSimtThreads) rows_simt_kernel(const __grid_co
         int L = sr.ctx + tok0 + ntok, from = 0;  // the item sees positions [from, L)
         if constexpr (kSpans) {
             from = row_from(w.mask(p.s), sr.ctx, tok0);
-            L = max(L, w.mask.prefix[p.s]);
+            L = max(L, w.mask.prefix(p.s));
         }
         __syncthreads();  // the last piece is done with every buffer
         // queries, times log2(e) / sqrt(hd)
@@ -405,10 +405,10 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
     constexpr bool kSpans = SCORED;
     std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk> w;
     if constexpr (kSpans) {
-        MaskedShared *ms = (MaskedShared *)(((uintptr_t)(ps + R * PLD) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, (int *)kv, w, tid, kSimtThreads);
+        RowsStart *start = (RowsStart *)(((uintptr_t)(ps + R * PLD) + 15) & ~(uintptr_t)15);
+        masked_layout(A, seq, wstart, start, (int *)kv, w, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
-        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
+        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), *start);
     } else {
         rows_layout(A, seq, wstart, tid, kSimtThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
         int L = sr.ctx + tok0 + ntok, from = 0;  // the item sees positions [from, L)
         if constexpr (kSpans) {
             from = row_from(w.mask(p.s), sr.ctx, tok0);
-            L = max(L, w.mask.prefix[p.s]);
+            L = max(L, w.mask.prefix(p.s));
         }
         __syncthreads();  // the last piece is done with every buffer
         // keys and values of block kb into buffer b; rows that no row of the item sees are zero
@@ -607,14 +607,14 @@ __global__ void __launch_bounds__(kSimtThreads, HDP == 64 ? 2 : 1) rows_fma_kern
 // ---- launch
 
 template <int HDP, bool SCORED> static cudaError_t launch_fma(const RowsArgs &a, cudaStream_t s) {
-    const size_t smem = simt_smem<float, HDP, 64>(a.nseq) + (SCORED ? masked_bytes(a.nseq) + 16 : 0);
+    const size_t smem = simt_smem<float, HDP, 64>(a.nseq) + (SCORED ? masked_bytes() : 0);
     const cudaError_t e = allow_smem((const void *)rows_fma_kernel<HDP, SCORED>);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_fma_kernel<HDP, SCORED>, dim3(a.P), dim3(kSimtThreads), smem, s, a);
 }
 
 template <typename T, int HDP, int R, bool SCORED> static cudaError_t launch_simt(const RowsArgs &a, cudaStream_t s) {
-    const size_t smem = simt_smem<T, HDP, R>(a.nseq) + (SCORED ? masked_bytes(a.nseq) + 16 : 0);
+    const size_t smem = simt_smem<T, HDP, R>(a.nseq) + (SCORED ? masked_bytes() : 0);
     const cudaError_t e = allow_smem((const void *)rows_simt_kernel<T, HDP, R, SCORED>);
     if (e != cudaSuccess) return e;
     return launch_pdl(rows_simt_kernel<T, HDP, R, SCORED>, dim3(a.P), dim3(kSimtThreads), smem, s, a);

@@ -452,7 +452,7 @@ __device__ __forceinline__ TileView tile_view(const SeqRows &sr, const RowsPiece
 }
 
 inline size_t tc_lengths_bytes(int nseq, bool spans) {
-    return (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 + (spans ? masked_bytes(nseq) + 16 : 0);
+    return (size_t)nseq * sizeof(SeqRows) + (size_t)(nseq + 1) * 8 + (spans ? masked_bytes() : 0);
 }
 
 __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool spans) {
@@ -531,10 +531,10 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     pdl_trigger();
     Walk w;
     if constexpr (kSpans) {
-        MaskedShared *ms = (MaskedShared *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, ms, (int *)ring, w, tid, tc_threads(SCORE));
+        RowsStart *start = (RowsStart *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
+        masked_layout(A, seq, wstart, start, (int *)ring, w, tid, tc_threads(SCORE));
         const long long unit = range_units(wstart[A.nseq], A.P);
-        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), ms->start);
+        w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), *start);
     } else {
         rows_layout(A, seq, wstart, tid, tc_threads(SCORE));  // ends with a __syncthreads()
     }
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     };
     auto prefix_of = [&](int s) {  // positions that all rows of the sequence see
         if constexpr (kSpans)
-            return w.mask.prefix[s];
+            return w.mask.prefix(s);
         else
             return 0;
     };

@@ -427,7 +427,7 @@ extern "C" int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const
     if (rows == 0) return SLM_OK;
     SampleRowsArgs a{};
     a.logits = (const uint8_t *)logits;
-    a.ld = rows > 1 ? ld : vocab;
+    a.ld = rows > 1 ? ld : 0;
     a.rows = rows;
     a.vocab = vocab;
     a.temperature = temperature;

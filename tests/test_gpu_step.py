@@ -355,6 +355,7 @@ def test_sample_odd_logits(slm, vocab):  # noqa: F811
         if T != inf:
             assert last[:7] == [0, 0, 1 if greedy else 3, 4, 2, 3, 0], (T, last)
         assert ids[7] == 0 and last[7] == (0 if greedy else vocab - 1 if k == 0 else 1 if T == inf else [0, 1, 3][k - 1])
+    assert sample(slm, x[7:], [1.0], [0], [nan], [nan], [1.0 - 2.0 ** -24]) == [vocab - 1]  # neither cut
     # uniforms outside [0, 1): cut to it
     z = torch.zeros(4, vocab, device="cuda")
     assert sample(slm, z, None, None, None, None, [-3.0, nan, 1.0, 7.0]) == [0, 0, vocab - 1, vocab - 1]
@@ -378,6 +379,59 @@ def test_sample_many_rows(slm):  # noqa: F811
         want.append(b)
     assert sample(slm, x, T, k, p, m, u) == want
     assert sample(slm, x, T, k, p, m, u) == want
+
+
+@pytest.mark.parametrize("k,p", [(0, 0.5), (0, 0.99), (700, 1.0), (3000, 0.9), (1, 0.5), (5000, 0.2)])
+def test_sample_ties(slm, k, p):  # noqa: F811
+    """Thousands of equal logits next to the border: the lowest indices come first, whichever way finds them."""
+    vocab, rng = 20000, np.random.default_rng(2)
+    for values in ([0.0], [0.0, 1.0], [0.0, 0.001], [-3.0, 0.0, 0.1]):
+        x = torch.from_numpy(rng.choice(values, vocab)).float().cuda()
+        ids, w = kept(x.double().cpu().numpy(), 1.0, k, np.float64(np.float32(p)), 0.0)
+        got = draws(ids, w, rng, 8)
+        assert sample(slm, x.expand(8, vocab), [1.0] * 8, [k] * 8, [p] * 8, [0.0] * 8, [g[0] for g in got]) == [g[1] for g in got]
+
+
+def test_sample_largest_vocabulary(slm):  # noqa: F811
+    vocab = 1 << 22
+    x = torch.randn(2, vocab, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * 3
+    x[:, 4000000] = 16.0
+    rng = np.random.default_rng(4)
+    for T, k, p in ((0.0, 0, 1.0), (1.0, 30, 1.0), (0.7, 0, 0.8), (1.0, 0, 1.0)):
+        u, want = [], []
+        for r in x.double().cpu().numpy():
+            if T == 0:
+                u.append(0.3)
+                want.append(int(r.argmax()))
+                continue
+            ids, w = kept(r, np.float64(np.float32(T)), k, np.float64(np.float32(p)), 0.0)
+            c = np.cumsum(w) / w.sum()  # millions of borders: the middle of a token's part, the largest of some
+            i = int(np.argmax(w * (rng.random(w.size) < 0.2)))
+            a = np.float32((c[i] + (c[i - 1] if i else 0.0)) / 2)
+            u.append(a)
+            want.append(int(ids[i]))
+        assert sample(slm, x, [T] * 2, [k] * 2, [p] * 2, None, u) == want
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_sample_alignment(slm, dtype, offset):  # noqa: F811
+    """Rows that begin anywhere."""
+    vocab, rng = 5003, np.random.default_rng(offset)
+    buf = torch.full((7, vocab + 9), float("inf"), device="cuda", dtype=dtype)
+    x = buf[:, offset:offset + vocab]
+    x.copy_(torch.randn(7, vocab, device="cuda") * 2)
+    params = [(0.0, 0, 1.0), (1.0, 12, 1.0), (1.0, 0, 0.9), (1.0, 0, 1.0), (0.5, 900, 0.7), (2.0, 0, 0.3), (1.0, 5000, 1.0)]
+    u, want = [], []
+    for r, (T, k, p) in zip(x.double().cpu().numpy(), params):
+        if T == 0:
+            u.append(0.1)
+            want.append(int(np.lexsort((np.arange(vocab), -r))[0]))
+            continue
+        (a, b), = draws(*kept(r, T, k, np.float64(np.float32(p)), 0.0), rng, 1)
+        u.append(a)
+        want.append(b)
+    assert sample(slm, x, [q[0] for q in params], [q[1] for q in params], [q[2] for q in params], None, u) == want
 
 
 def test_sample_distribution(slm):  # noqa: F811
