@@ -342,6 +342,6 @@ struct SampleRowsArgs {
     const int *top_k;
     int *next_ids;
 };
-cudaError_t sample_rows_launch(const SampleRowsArgs &a, bool bf16, cudaStream_t s);
+cudaError_t sample_rows_launch(const SampleRowsArgs &a, bool bf16, int sms, cudaStream_t s);
 
 }  // namespace slm

@@ -422,7 +422,8 @@ extern "C" int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const
         if ((uintptr_t)ptrs[i].p % size) return attn_fail(SLM_EINVAL, "%s must be %d-byte aligned", ptrs[i].name, size);
     }
     int dev = 0;
-    if ((rc = current_sms(dev)) < 0) return rc;
+    const int sms = current_sms(dev);
+    if (sms < 0) return sms;
     if ((rc = check_pointers(dev, ptrs, n))) return rc;
     if (rows == 0) return SLM_OK;
     SampleRowsArgs a{};
@@ -436,7 +437,7 @@ extern "C" int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const
     a.min_p = min_p;
     a.uniforms = uniforms;
     a.next_ids = next_ids;
-    const cudaError_t e = sample_rows_launch(a, dtype == SLM_BF16, (cudaStream_t)stream);
+    const cudaError_t e = sample_rows_launch(a, dtype == SLM_BF16, sms, (cudaStream_t)stream);
     if (e != cudaSuccess) return launch_fail("sample", e);
     return SLM_OK;
 }

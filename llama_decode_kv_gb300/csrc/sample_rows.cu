@@ -9,25 +9,27 @@
 //     top-k:  the k-th number.   top-p:  where the running sum of W first reaches p times the whole.
 //     min-p:  w_i >= m.          draw:   the first i in index order with sum_{j <= i} W_j > u sum W.
 //
-// HBM bounds a batch: its logits are read once.  A CTA has a row, and reads it for the largest logit of
-// every group of 16 tokens; the other steps read only groups that can matter, from the L2:
+// HBM bounds a batch: its logits are read once.  A row has one CTA, or a cluster of up to eight where
+// there are few rows, each with a slice of the row; it reads it for the largest logit of every group
+// of 16 tokens; the other steps read only groups that can matter, from the L2:
 //   greedy        the first group with the largest logit;
-//   top-k         groups whose maximum is among the k largest (at least k tokens are no smaller than the
-//                 k-th largest maximum, and hardly more): their tokens make a list, and each token of it
-//                 finds its rank and the sum before it by looking at the others;
-//   top-p alone   a histogram of the weights, 8 bins an octave, in cut whole numbers, says in which bin
+//   top-k         256 bins of the groups' maxima give a value that at least k of them reach, and few
+//                 more: the tokens that do make a list, which is sorted, cut, and
+//                 sorted by index;
+//   top-p alone   a histogram of the weights, 32 bins an octave, in cut whole numbers, says in which bin
 //                 (or two) the sum is reached; the sum above it is then exact, the bin's tokens make a
 //                 list, and a few rounds of 256 bins find the last one of them to be kept;
 //   the draw      the sum of every 1,024 tokens, the segment that holds the target, its tokens.
 // A list that overflows (a top-k of a good part of the vocabulary, thousands of equal logits next to the
-// border) leaves the row to the general way: a threshold by its four bytes in turn, over all tokens.
+// border) or an infinite logit leaves the row to the general way: a threshold by its eight bytes in turn,
+// over all tokens.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "device_common.cuh"
 #include "rows.cuh"
@@ -35,10 +37,13 @@
 namespace slm {
 
 typedef unsigned long long u64;
-constexpr int kSrList = 2048;    // tokens of a list
-constexpr int kSrGroups = 16384; // groups of a row at most
-constexpr int kSrBins = 352;     // 44 octaves of 8 bins: weights of 2^-41 and less are 0
+constexpr int kSrThreads = 256;
+constexpr int kSrResident = 3;    // CTAs per SM
+constexpr int kSrList = 2048;     // tokens of a list
+constexpr int kSrGroups = 16384;  // groups of a slice at most
+constexpr int kSrBins = 1344;     // 42 octaves of 32 bins: weights of 2^-41 and less are 0
 constexpr int kSrSegment = 1024;
+constexpr int kSrCluster = 8;     // slices of a row at most
 
 // Monotone map of a float to an unsigned key; NaN goes where -infinity is, and -0 where 0.
 __device__ __forceinline__ uint32_t sr_key(float f) {
@@ -49,23 +54,25 @@ __device__ __forceinline__ float sr_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// Four consecutive logits from i on; -infinity behind the row.  `wide`: rows begin on boundaries of four
+// Four consecutive logits from i on; -infinity from n on.  `wide`: rows begin on boundaries of four
 // elements.
-__device__ __forceinline__ float4 sr_load4(const float *x, int i, int V, bool wide) {
-    if (wide && i + 3 < V) return __ldg((const float4 *)(x + i));
+__device__ __forceinline__ float4 sr_wide4(const float *x, int i) { return __ldg((const float4 *)(x + i)); }
+__device__ __forceinline__ float4 sr_wide4(const uint16_t *x, int i) {
+    const uint2 w = __ldg((const uint2 *)(x + i));
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+__device__ __forceinline__ float4 sr_load4(const float *x, int i, int n, bool wide) {
+    if (wide && i + 3 < n) return sr_wide4(x, i);
     float4 v;
-    v.x = i < V ? __ldg(x + i) : -INFINITY;
-    v.y = i + 1 < V ? __ldg(x + i + 1) : -INFINITY;
-    v.z = i + 2 < V ? __ldg(x + i + 2) : -INFINITY;
-    v.w = i + 3 < V ? __ldg(x + i + 3) : -INFINITY;
+    v.x = i < n ? __ldg(x + i) : -INFINITY;
+    v.y = i + 1 < n ? __ldg(x + i + 1) : -INFINITY;
+    v.z = i + 2 < n ? __ldg(x + i + 2) : -INFINITY;
+    v.w = i + 3 < n ? __ldg(x + i + 3) : -INFINITY;
     return v;
 }
-__device__ __forceinline__ float4 sr_load4(const uint16_t *x, int i, int V, bool wide) {
-    if (wide && i + 3 < V) {
-        const uint2 w = __ldg((const uint2 *)(x + i));
-        return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
-    }
-    auto at = [&](int j) { return j < V ? __uint_as_float((uint32_t)__ldg(x + j) << 16) : -INFINITY; };
+__device__ __forceinline__ float4 sr_load4(const uint16_t *x, int i, int n, bool wide) {
+    if (wide && i + 3 < n) return sr_wide4(x, i);
+    auto at = [&](int j) { return j < n ? __uint_as_float((uint32_t)__ldg(x + j) << 16) : -INFINITY; };
     return make_float4(at(i), at(i + 1), at(i + 2), at(i + 3));
 }
 __device__ __forceinline__ float sr_load(const float *x, int i) { return __ldg(x + i); }
@@ -85,40 +92,93 @@ __device__ __forceinline__ u64 warp_total(u64 v) {
     return v;
 }
 
-struct SrToken {
-    u64 at, w;  // place in the order; weight
-};
-
-// What a row's CTA shares.
+// What a slice's CTA shares; list and found of slice 0 are the row's in the end.
 struct SrShared {
-    u64 warp[32], bins[256], found[2];
-    uint32_t hist[kSrBins];
-    int n, id, lo, hi;
-    uint32_t kmin, kmax;
-    SrToken list[kSrList];
+    u64 warp[kSrThreads / 32], found[2];
+    u64 slices[2][kSrCluster];  // a number of every slice, two sets in turn
+    int n, lo, hi;
+    u64 bins[256], sums[256];
+    union {
+        struct {
+            uint32_t hist[kSrBins], merged[kSrBins];
+        };
+        uint32_t by_index[kSrList];  // draw_list
+    };
+    u64 list[kSrList], sorted[kSrList];  // places in the order
 };
 
-template <typename T, int NT> struct SrRow {
+// Weights on their way into a sum: whole numbers of 2^-20 and of 2^-40, apart until flush(), which has to
+// come before 4,096 of them are in.
+struct SrSum {
+    u64 sum = 0;
+    uint32_t hi = 0;
+    int lo = 0;
+    __device__ __forceinline__ void add(float w) {
+        constexpr float kMagic = 12582912.0f;  // 1.5 2^23: what is added to it is rounded to a whole number
+        const float a = w * 1048576.0f, h = a + kMagic, l = fmaf(a - (h - kMagic), 1048576.0f, kMagic);
+        hi += __float_as_uint(h) - 0x4b400000u;
+        lo += (int)(__float_as_uint(l) - 0x4b400000u);
+    }
+    __device__ __forceinline__ u64 flush() {
+        sum += ((u64)hi << 20) + (u64)(long long)lo;
+        hi = 0;
+        lo = 0;
+        return sum;
+    }
+};
+
+template <typename T, bool CL> struct SrRow {
+    static constexpr int NT = kSrThreads;
     const T *x;
-    int V, shift;      // tokens of a group: 2^shift
+    int V, i0, i1;     // tokens of the row; the slice [i0, i1)
+    int slices, rank;
+    int shift;         // tokens of a group: 2^shift
     bool wide;
-    uint32_t *gm;      // [groups] keys of the maxima
-    u64 *seg;          // [segments] sums
+    uint32_t *gm;      // [groups of the slice] keys of the maxima
+    u64 *seg;          // [segments of the slice] sums
     SrShared *S;
     int tid, lane, warp;
-    uint32_t top;      // key of the largest logit
-    float vmax, scale; // it, and log2(e) / T
+    int set;           // of S->slices
+    float vmax, scale; // the largest logit, log2(e) / T
     float minp;
+    int *out;
 
-    __device__ __forceinline__ float exponent(uint32_t key) const {  // log2 of the weight
-        const float d = sr_value(key) - vmax;
-        return key == top ? 0.0f : d == -INFINITY ? -INFINITY : d * scale;
+    // All threads of the row.
+    __device__ __forceinline__ void sync() const {
+        if (CL) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
     }
-    static __device__ __forceinline__ u64 whole(float w) { return (u64)__float2ull_rn(w * 1099511627776.0f); }
-    __device__ __forceinline__ int groups() const { return (V + (1 << shift) - 1) >> shift; }
+    // The same place in slice r's shared memory.
+    template <typename P> __device__ __forceinline__ P *at_slice(P *p, int r) const {
+        if (!CL) return p;
+        P *q;
+        asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(r));
+        return q;
+    }
+    // Every slice's number to all slices: afterwards S->slices[returned][.] holds them.  The two sets
+    // take turns, so that a set is written again only behind a barrier that its readers have reached.
+    __device__ __forceinline__ int share(u64 v) {
+        const int k = set;
+        set ^= 1;
+        if (tid < slices) at_slice(S, tid)->slices[k][rank] = v;
+        sync();
+        return k;
+    }
+
+    __device__ __forceinline__ float exponent(float v) const { return fmaxf((v - vmax) * scale, -200.0f); }  // log2 of the weight; NaN: nothing
+    static __device__ __forceinline__ u64 whole(float w) {  // w 2^40, to the nearest
+        SrSum a;
+        a.add(w);
+        return a.flush();
+    }
+    __device__ __forceinline__ int groups() const { return (i1 - i0 + (1 << shift) - 1) >> shift; }
     static __device__ __forceinline__ u64 place(uint32_t key, int i) { return (u64)key << 32 | (0xffffffffu - (uint32_t)i); }
 
-    // Inclusive running sum over the CTA, in order of the threads; the whole sum in warp[NT / 32 - 1].
+    // Inclusive running sum over the CTA, in order of the threads, and the whole.
     __device__ __forceinline__ u64 scan(u64 v, u64 &total) const {
         v = warp_scan(v, lane);
         __syncthreads();  // the last call's sums have been read
@@ -133,7 +193,7 @@ template <typename T, int NT> struct SrRow {
         }
         return before + v;
     }
-    __device__ __forceinline__ u64 total_of(u64 v) const {
+    __device__ __forceinline__ u64 cta_total(u64 v) const {
         v = warp_total(v);
         __syncthreads();
         if (lane == 0) S->warp[warp] = v;
@@ -143,158 +203,274 @@ template <typename T, int NT> struct SrRow {
         for (int i = 0; i < NT / 32; i++) t += S->warp[i];
         return t;
     }
-
-    // f(key, index) of the tokens of those groups that pass(maximum's key), 128 tokens a warp at a time;
-    // done() after each segment's, if any.
-    template <typename P, typename F, typename D> __device__ __forceinline__ void each(P pass, F f, D done) const {
-        for (int s0 = warp * kSrSegment; s0 < V; s0 += NT / 32 * kSrSegment) {
-#pragma unroll 2
-            for (int c = s0; c < min(V, s0 + kSrSegment); c += 128) {
-                const int i = c + 4 * lane;
-                const bool mine = i < V && pass(gm[i >> shift]);
-                if (!__any_sync(0xffffffffu, mine)) continue;
-                if (mine) {
-                    const float4 v = sr_load4(x, i, V, wide);
-                    f(sr_key(v.x), i);
-                    f(sr_key(v.y), i + 1);
-                    f(sr_key(v.z), i + 2);
-                    f(sr_key(v.w), i + 3);
-                }
+    __device__ __forceinline__ u64 total_of(u64 v) {
+        u64 t = cta_total(v);
+        if (CL) {
+            const int k = share(t);
+            t = 0;
+            for (int r = 0; r < slices; r++) t += S->slices[k][r];
+        }
+        return t;
+    }
+    __device__ __forceinline__ u64 most_of(u64 v) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+        __syncthreads();
+        if (lane == 0) S->warp[warp] = v;
+        __syncthreads();
+        u64 t = 0;
+#pragma unroll 8
+        for (int i = 0; i < NT / 32; i++) t = max(t, S->warp[i]);
+        if (CL) {
+            const int k = share(t);
+            for (int r = 0; r < slices; r++) t = max(t, S->slices[k][r]);
+        }
+        return t;
+    }
+    // to[b] = the slices' from[b], added up: an equal part of them by each slice, for all.
+    template <typename N> __device__ __forceinline__ void merge(const N *from, N *to, int n) const {
+        sync();
+        if (CL) {
+            const int part = (n + slices - 1) / slices, b0 = rank * part;
+            for (int b = b0 + tid; b < min(n, b0 + part); b += NT) {
+                N v[kSrCluster], t = 0;
+#pragma unroll
+                for (int r = 0; r < kSrCluster; r++) v[r] = at_slice(from, min(r, slices - 1))[b];
+#pragma unroll
+                for (int r = 0; r < kSrCluster; r++) t += r < slices ? v[r] : 0;
+#pragma unroll
+                for (int r = 0; r < kSrCluster; r++)
+                    if (r < slices) at_slice(to, r)[b] = t;
             }
-            done(s0 / kSrSegment);
+        } else {
+            for (int b = tid; b < n; b += NT) to[b] = from[b];
+        }
+        sync();
+    }
+
+    // f(four logits, index) of the slice's tokens of those groups that pass(maximum), 512 tokens a warp at
+    // a time so that four loads are in flight; done(segment) after each segment's.  Behind the slice's
+    // end the logits are -infinity.
+    template <typename P, typename F, typename D> __device__ __forceinline__ void each(P pass, F f, D done) const {
+        for (int s0 = i0 + warp * kSrSegment; s0 < i1; s0 += NT / 32 * kSrSegment) {
+#pragma unroll 1
+            for (int c = s0; c < min(i1, s0 + kSrSegment); c += 512) {
+                bool mine[4];
+                float4 v[4];
+                bool any = false;
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    const int i = c + 128 * q + 4 * lane;
+                    mine[q] = i < i1 && pass(sr_value(gm[(i - i0) >> shift]));
+                    any |= mine[q];
+                }
+                if (!__any_sync(0xffffffffu, any)) continue;
+                if (wide && c + 512 <= i1) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        v[q] = mine[q] ? sr_wide4(x, c + 128 * q + 4 * lane) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (mine[q]) v[q] = sr_load4(x, c + 128 * q + 4 * lane, i1, wide);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    if (mine[q]) f(v[q], c + 128 * q + 4 * lane);
+            }
+            done((s0 - i0) / kSrSegment);
         }
     }
-    __device__ __forceinline__ void append(u64 at, u64 w) const {
+    __device__ __forceinline__ void append(u64 at) const {  // to the slice's list
         const int n = atomicAdd(&S->n, 1);
-        if (n < kSrList) S->list[n] = SrToken{at, w};
+        if (n < kSrList) S->list[n] = at;
+    }
+    __device__ __forceinline__ float weight_at(u64 at) const { return fast_exp2(exponent(sr_value((uint32_t)(at >> 32)))); }
+    // The slices' lists, one behind the other, to slice 0's; how many tokens they are (more than kSrList:
+    // an overflow, and nothing is moved).
+    __device__ __forceinline__ int gather() {
+        __syncthreads();
+        const int mine = S->n;
+        if (!CL) return mine;
+        const int k = share((u64)mine);
+        int before = 0, all = 0;
+        for (int r = 0; r < slices; r++) {
+            if (r == rank) before = all;
+            all += (int)S->slices[k][r];
+        }
+        if (all > kSrList) return all;
+        if (rank > 0) {
+            u64 *to = at_slice(S, 0)->list + before;
+            for (int c = tid; c < mine; c += NT) to[c] = S->list[c];
+        }
+        sync();
+        return all;
     }
 
-    // The first index with the key `top`.
-    __device__ __forceinline__ int first_top() const {
-        if (tid == 0) S->id = V;
-        __syncthreads();
+    // Greedy: the first index with the largest logit.
+    __device__ __forceinline__ void first_top() {
         const int n = groups();
-        int g = 0x7fffffff;
-        for (int i = tid; i < n; i += NT)
-            if (gm[i] == top) {
-                g = i;
+        const uint32_t top = sr_key(vmax);
+        u64 first = 0;  // complemented: larger is earlier
+        for (int g = tid; g < n; g += NT)
+            if (gm[g] == top) {
+                first = 0xffffffffull - (uint32_t)g;
                 break;
             }
-        g = (int)__reduce_min_sync(0xffffffffu, (unsigned)g);
-        if (lane == 0 && g < n) atomicMin(&S->id, g);
+        // the slice's first group, then its first token, then the first slice's
+#pragma unroll
+        for (int o = 16; o; o >>= 1) first = max(first, __shfl_xor_sync(0xffffffffu, first, o));
         __syncthreads();
-        g = S->id;
+        if (lane == 0) S->warp[warp] = first;
         __syncthreads();
-        if (tid == 0) S->id = V;
-        __syncthreads();
-        for (int i = (g << shift) + tid; i < min(V, (g + 1) << shift); i += NT)
-            if (sr_key(sr_load(x, i)) == top) atomicMin(&S->id, i);
-        __syncthreads();
-        return S->id;
+        for (int w = 0; w < NT / 32; w++) first = max(first, S->warp[w]);
+        u64 best = 0;
+        if (first) {
+            const int c = i0 + (int)((0xffffffffu - (uint32_t)first) << shift);
+            for (int i = c + tid; i < min(i1, c + (1 << shift)); i += NT)
+                if (sr_key(sr_load(x, i)) == top) best = max(best, 0xffffffffull - (uint32_t)i);
+        }
+        best = most_of(best);
+        if (rank == 0 && tid == 0) *out = (int)(0xffffffffu - (uint32_t)best);
     }
 
-    // A key that at least k of the groups' maxima reach, and not many more.
-    __device__ __forceinline__ uint32_t kth_maximum(int k) const {
+    // 256 bins of equal width between the largest logit and the groups' smallest maximum; the bin that
+    // the k-th largest of all maxima is in.
+    __device__ __forceinline__ int kth_bin(int k, float &width) {
         const int n = groups();
-        uint32_t prefix = 0, mask = 0;
-        int above = 0;
-        for (int d = 24; d >= 0; d -= 8) {
-            for (int b = tid; b < 256; b += NT) S->hist[b] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += NT)
-                if ((gm[i] & mask) == prefix) atomicAdd(&S->hist[gm[i] >> d & 255u], 1u);
-            __syncthreads();
-            if (warp == 0) {  // lane l has bins 255 - 8 l down to 248 - 8 l
-                int t = 0;
+        uint32_t least = 0xffffffffu;
+        for (int g = tid; g < n; g += NT)
+            if (sr_value(gm[g]) > -INFINITY) least = min(least, gm[g]);
+        const float low = sr_value(0xffffffffu - (uint32_t)most_of(0xffffffffu - least));
+        const float range = vmax - low;
+        width = range > 1e-30f ? 255.0f / range : 0.0f;
+        for (int b = tid; b < 256; b += NT) S->hist[b] = 0;
+        __syncthreads();
+        for (int g = tid; g < n; g += NT) atomicAdd(&S->hist[bin_of_value(sr_value(gm[g]), width)], 1u);
+        merge(S->hist, S->merged, 256);
+        if (warp == 0) {  // lane l has bins 8 l to 8 l + 7
+            int t = 0;
 #pragma unroll
-                for (int q = 0; q < 8; q++) t += (int)S->hist[255 - 8 * lane - q];
-                const int upto = (int)warp_scan((u64)t, lane);
-                int a = above + upto - t;
-                if (a < k && k <= a + t) {
-                    int q = 0;
-                    while (q < 7 && a + (int)S->hist[255 - 8 * lane - q] < k) a += (int)S->hist[255 - 8 * lane - q++];
-                    S->lo = 255 - 8 * lane - q;
-                    S->hi = a;
-                }
+            for (int q = 0; q < 8; q++) t += (int)S->merged[8 * lane + q];
+            int a = (int)warp_scan((u64)t, lane) - t;
+            if (a < k && k <= a + t) {
+                int b = 8 * lane;
+                while ((a += (int)S->merged[b]) < k) b++;
+                S->lo = b;
             }
-            __syncthreads();
-            prefix |= (uint32_t)S->lo << d;
-            mask |= 255u << d;
-            above = S->hi;
-            const int reach = above + (int)S->hist[S->lo];
-            __syncthreads();
-            if (reach <= k + k / 8 + 16) break;
-        }
-        return prefix;
-    }
-
-    // The list's tokens after top-k (k = 0: all of them), top-p and min-p; the draw.  The list holds the
-    // first k tokens of the row at least.
-    __device__ __forceinline__ int draw_list(int n, int k, float p, float u) const {
-        constexpr int E = kSrList / NT;
-        u64 before[E], w[E], at[E], mass = 0;
-        bool in[E];
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-            const int c = tid + e * NT;
-            in[e] = false;
-            if (c < n) {
-                at[e] = S->list[c].at;
-                w[e] = S->list[c].w;
-                before[e] = 0;
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < n; j++)
-                    if (S->list[j].at > at[e]) {
-                        rank++;
-                        before[e] += S->list[j].w;
-                    }
-                in[e] = k == 0 || rank < k;
-                if (in[e]) mass += w[e];
-            }
-        }
-        u64 M = total_of(mass);
-        const u64 want = p < 1.0f ? max((u64)1, (u64)ceil((double)fmaxf(p, 0.0f) * (double)M)) : ~0ull;
-        mass = 0;
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-            const int c = tid + e * NT;
-            if (c >= n) continue;
-            const uint32_t key = (uint32_t)(at[e] >> 32);
-            in[e] = in[e] && before[e] < want && !(exp2f(exponent(key)) < minp);
-            if (!in[e]) S->list[c].w = w[e] = 0;
-            mass += w[e];
-        }
-        M = total_of(mass);  // (its barriers order the list too)
-        const u64 target = target_of(u, M);
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-            const int c = tid + e * NT;
-            if (c >= n || w[e] == 0) continue;
-            const uint32_t idx = (uint32_t)at[e];  // complemented: larger is earlier
-            u64 upto = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; j++)
-                if ((uint32_t)S->list[j].at >= idx) upto += S->list[j].w;
-            if (upto > target && upto - w[e] <= target) S->id = (int)(0xffffffffu - idx);
         }
         __syncthreads();
-        return S->id;
+        return S->lo;
+    }
+    __device__ __forceinline__ int bin_of_value(float v, float width) const {
+        return (int)fminf((vmax - v) * width, 255.0f);
     }
 
     static __device__ __forceinline__ u64 target_of(float u, u64 M) {
         u = u >= 0.f ? fminf(u, 1.0f) : 0.f;
         return min((u64)((double)u * (double)M), M - 1);
     }
+    static __device__ __forceinline__ u64 share_of(float p, u64 M) {  // p M, at least 1
+        return max((u64)1, (u64)ceil((double)fmaxf(p, 0.0f) * (double)M));
+    }
+
+    // By slice 0: the list's tokens after top-k (k = 0: all of them), top-p and min-p; the draw.  The
+    // list holds the first k tokens of the row at least.
+    __device__ __forceinline__ void draw_list(int n, int k, float p, float u) const {
+        sort(S->list, n, [&](int rank, u64 at) { S->sorted[rank] = at; });
+        // every cut keeps a prefix: adjacent tokens a thread, and the sum before each
+        const int per = (n + NT - 1) / NT, c0 = min(n, tid * per), c1 = min(k > 0 ? min(n, k) : n, c0 + per);
+        u64 mass = 0, M;
+        for (int c = c0; c < c1; c++) mass += whole(weight_at(S->sorted[c]));
+        u64 before = scan(mass, M) - mass;
+        const u64 want = p < 1.0f ? share_of(p, M) : ~0ull;
+        u64 left = 0;
+        for (int c = c0; c < c1; c++) {
+            const float w = weight_at(S->sorted[c]);
+            left += before < want && !(w < minp);
+            before += whole(w);
+        }
+        const int m = (int)cta_total(left);
+        for (int c = tid; c < m; c += NT) S->list[c] = S->sorted[c] << 32 | (uint32_t)c;  // complemented index first
+        __syncthreads();
+        sort(S->list, m, [&](int rank, u64 at) { S->by_index[rank] = (uint32_t)at; });
+        const int share = (m + NT - 1) / NT, d0 = min(m, tid * share), d1 = min(m, d0 + share);
+        mass = 0;
+        for (int d = d0; d < d1; d++) mass += whole(weight_at(S->sorted[S->by_index[d]]));
+        const u64 upto = scan(mass, M), target = target_of(u, M);
+        if (upto > target && upto - mass <= target) {
+            u64 a = upto - mass;
+            for (int d = d0; d < d1; d++) {
+                const u64 at = S->sorted[S->by_index[d]];
+                a += whole(weight_at(at));
+                if (a > target) {
+                    *out = (int)(0xffffffffu - (uint32_t)at);
+                    break;
+                }
+            }
+        }
+    }
+    // put(rank, value) of n different values, the largest first.  A warp sorts 64 at a time, two a lane (a
+    // bitonic network); a value's rank is its place there plus the larger ones of every other 64.
+    template <typename P> __device__ __forceinline__ void sort(u64 *a, int n, P put) const {
+        for (int c = 64 * warp; c < n; c += 64 * (NT / 32)) {
+            u64 x = c + lane < n ? a[c + lane] : 0, y = c + 32 + lane < n ? a[c + 32 + lane] : 0;
+#pragma unroll
+            for (int size = 2; size <= 64; size <<= 1)
+#pragma unroll
+                for (int stride = size >> 1; stride > 0; stride >>= 1) {
+                    if (stride == 32) {
+                        const u64 hi = max(x, y);
+                        y = min(x, y);
+                        x = hi;
+                    } else {
+                        const u64 u = __shfl_xor_sync(0xffffffffu, x, stride), v = __shfl_xor_sync(0xffffffffu, y, stride);
+                        const bool first = (lane & stride) == 0;
+                        x = first == ((lane & size) == 0) ? max(x, u) : min(x, u);
+                        y = first == (((lane + 32) & size) == 0) ? max(y, v) : min(y, v);
+                    }
+                }
+            if (c + lane < n) a[c + lane] = x;
+            if (c + 32 + lane < n) a[c + 32 + lane] = y;
+        }
+        __syncthreads();
+        for (int i = tid; i < n; i += NT) {
+            const u64 me = a[i];
+            const int mine = i & ~63;
+            int rank = i & 63;
+#pragma unroll 4
+            for (int c = 0; c < n; c += 64) {
+                if (c == mine) continue;
+                int lo = 0;  // how many of the 64 are larger
+#pragma unroll
+                for (int step = 64; step; step >>= 1)
+                    if (lo + step <= 64 && c + lo + step <= n && a[c + lo + step - 1] > me) lo += step;
+                rank += lo;
+            }
+            put(rank, me);
+        }
+        __syncthreads();
+    }
 
     // The draw from the tokens from `least` on, by the segments' sums.
-    __device__ __forceinline__ int draw_segments(u64 least, float u) const {
-        const int n = (V + kSrSegment - 1) / kSrSegment, per = (n + NT - 1) / NT;
+    __device__ __forceinline__ void draw_segments(u64 least, float u) {
+        const int n = (i1 - i0 + kSrSegment - 1) / kSrSegment, per = (n + NT - 1) / NT;
         const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
-        u64 mine = 0, M;
+        u64 mine = 0, M, base = 0;
         for (int s = s0; s < s1; s++) mine += seg[s];
-        const u64 upto = scan(mine, M);
+        u64 upto = scan(mine, M);
+        if (CL) {
+            const int k = share(M);
+            M = 0;
+            for (int r = 0; r < slices; r++) {
+                if (r == rank) base = M;
+                M += S->slices[k][r];
+            }
+        }
         const u64 target = target_of(u, M);
+        if (tid == 0) S->lo = -1;
+        __syncthreads();
+        upto += base;
         if (upto > target && upto - mine <= target) {
             u64 a = upto - mine;
             int s = s0;
@@ -303,150 +479,170 @@ template <typename T, int NT> struct SrRow {
             S->found[0] = a;
         }
         __syncthreads();
-        if (warp == 0) {
-            u64 a = S->found[0];
-            const int c0 = S->lo * kSrSegment;
-            for (int c = c0; c < min(V, c0 + kSrSegment); c += 128) {
-                const int i = c + 4 * lane;
-                const float4 v = sr_load4(x, i, V, wide);
-                const float f[4] = {v.x, v.y, v.z, v.w};
-                u64 w[4], sum = 0;
+        if (warp > 0 || S->lo < 0) return;
+        u64 a = S->found[0];
+        const int c0 = i0 + S->lo * kSrSegment;
+        for (int c = c0; c < min(i1, c0 + kSrSegment); c += 128) {
+            const int i = c + 4 * lane;
+            const float4 v = sr_load4(x, i, i1, wide);
+            const float f[4] = {v.x, v.y, v.z, v.w};
+            u64 w[4], sum = 0;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float r = fast_exp2(exponent(f[q]));
+                w[q] = i + q < i1 && place(sr_key(f[q]), i + q) >= least && !(r < minp) ? whole(r) : 0;
+                sum += w[q];
+            }
+            const u64 to = a + warp_scan(sum, lane);
+            const bool here = to > target && to - sum <= target;
+            if (here) {
+                u64 b = to - sum;
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
-                    const uint32_t key = sr_key(f[q]);
-                    const float r = exp2f(exponent(key));
-                    w[q] = i + q < V && place(key, i + q) >= least && !(r < minp) ? whole(r) : 0;
-                    sum += w[q];
+                    if (b <= target && b + w[q] > target) *out = i + q;
+                    b += w[q];
                 }
-                const u64 upto = a + warp_scan(sum, lane);
-                const bool here = upto > target && upto - sum <= target;
-                if (here) {
-                    u64 b = upto - sum;
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        if (b <= target && b + w[q] > target) S->id = i + q;
-                        b += w[q];
-                    }
-                }
-                if (__any_sync(0xffffffffu, here)) break;
-                a = __shfl_sync(0xffffffffu, upto, 31);
             }
+            if (__any_sync(0xffffffffu, here)) break;
+            a = __shfl_sync(0xffffffffu, to, 31);
         }
-        __syncthreads();
-        return S->id;
     }
 
-    // Sums of the segments over tokens from `least` on.
-    __device__ __forceinline__ void sum_segments(u64 least) const {
-        u64 sum = 0;
-        each([&](uint32_t m) {
-                 const float r = exp2f(exponent(m));
-                 return (u64)m >= least >> 32 && !(r < minp) && r > 0.f;
+    // Sums of the segments, min-p applied.
+    __device__ __forceinline__ void sum_segments() const {
+        SrSum sum;
+        each([&](float m) {
+                 const float e = exponent(m);
+                 return e > -42.0f && !(fast_exp2(e) < minp);
              },
-             [&](uint32_t key, int i) {
-                 const float r = exp2f(exponent(key));
-                 if (i < V && place(key, i) >= least && !(r < minp)) sum += whole(r);
+             [&](float4 v, int) {
+#pragma unroll
+                 for (int q = 0; q < 4; q++) {
+                     const float w = fast_exp2(exponent(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w));
+                     sum.add(w < minp ? 0.0f : w);
+                 }
              },
              [&](int s) {
-                 sum = warp_total(sum);
-                 if (lane == 0) seg[s] = sum;
-                 sum = 0;
+                 const u64 t = warp_total(sum.flush());
+                 if (lane == 0) seg[s] = t;
+                 sum.sum = 0;
              });
         __syncthreads();
     }
 
-    __device__ __forceinline__ int bin_of(float e) const { return (int)fminf(e * -8.0f, (float)(kSrBins - 1)); }
+    // The bin of a weight's exponent: the nearest whole number to -32 e.
+    static __device__ __forceinline__ int bin_of(float e) {
+        return (int)(__float_as_uint(fmaf(e, -32.0f, 12582912.0f)) - 0x4b400000u);
+    }
 
     // The place in the order of the last token of the shortest prefix that reaches p of the whole mass,
-    // and the sums of the segments over that prefix (min-p applied to them).  false: a list overflowed.
-    __device__ __forceinline__ bool nucleus(float p, u64 &least) const {
-        // bits of a weight in the histogram: 13, less where the vocabulary could overflow 32
+    // and the sums of the segments over that prefix (min-p applied to them).  false: the list overflowed.
+    __device__ __forceinline__ bool nucleus(float p, u64 &least) {
+        // bits of a weight in the histogram: 13, less where a bin of the whole vocabulary could overflow
         int bits = 13;
         for (int v = V; v > (1 << 18); v >>= 1) bits--;
         for (int b = tid; b < kSrBins; b += NT) S->hist[b] = 0;
         if (tid == 0) S->n = 0;
         __syncthreads();
-        u64 mass = 0;
-        each([&](uint32_t m) { return exponent(m) > -42.0f; },
-             [&](uint32_t key, int) {
-                 const float e = exponent(key);
-                 const u64 w = whole(exp2f(e));
-                 if (w == 0) return;
-                 mass += w;
-                 const int b = bin_of(e), cut = 40 - bits - (b >> 3);
-                 atomicAdd(&S->hist[b], (uint32_t)(cut >= 0 ? w >> cut : w << -cut));
+        SrSum mass;
+        each([&](float m) { return exponent(m) > -42.0f; },
+             [&](float4 v, int) {
+#pragma unroll
+                 for (int q = 0; q < 4; q++) {
+                     const float e = exponent(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w), w = fast_exp2(e);
+                     if (e <= -41.0f) continue;
+                     mass.add(w);
+                     const int b = bin_of(e);  // w 2^floor(b / 32) is between 2^-1.01 and 2^0.02
+                     atomicAdd(&S->hist[b],
+                               __float2uint_rz(__uint_as_float(__float_as_uint(w) + ((uint32_t)(bits + (b >> 5)) << 23))));
+                 }
+                 mass.flush();
              },
              [](int) {});
-        const u64 M = total_of(mass);
-        const u64 want = max((u64)1, (u64)ceil((double)fmaxf(p, 0.0f) * (double)M));
-        if (warp == 0) {  // 11 bins a lane; a cut weight is at most 2^(2 - bits) below the weight
-            constexpr int B = kSrBins / 32;
-            u64 a[B], t = 0;
+        merge(S->hist, S->merged, kSrBins);
+        const u64 M = total_of(mass.sum), want = share_of(p, M);
+        // Cutting took less than 2^(2 - bits) of every weight, and the whole numbers of 2^-40 have half of
+        // one a token besides.  Adjacent bins a thread: the first of all that may reach the share, and the
+        // first that must.
+        if (tid == 0) S->lo = S->hi = kSrBins - 1;
+        constexpr int B = (kSrBins + NT - 1) / NT;
+        u64 a[B], t = 0, all;
 #pragma unroll
-            for (int q = 0; q < B; q++) {
-                const int b = B * lane + q, cut = 40 - bits - (b >> 3);
-                a[q] = cut >= 0 ? (u64)S->hist[b] << cut : (u64)S->hist[b] >> -cut;
-                t += a[q];
-            }
-            u64 c = warp_scan(t, lane) - t;
-            int b1 = kSrBins, b2 = kSrBins;
+        for (int q = 0; q < B; q++) {
+            const int b = B * tid + q, sh = 40 - bits - (b >> 5);
+            const u64 h = b < kSrBins ? S->merged[b] : 0;
+            a[q] = sh >= 0 ? h << sh : h >> -sh;
+            t += a[q];
+        }
+        u64 c = scan(t, all) - t;
+        bool may = false, must = false;
 #pragma unroll
-            for (int q = 0; q < B; q++) {
-                c += a[q];
-                if (b1 == kSrBins && c + (c >> (bits - 2)) + 1 >= want) b1 = B * lane + q;
-                if (b2 == kSrBins && c >= want) b2 = B * lane + q;
+        for (int q = 0; q < B; q++) {
+            c += a[q];
+            if (!may && c + (c >> (bits - 2)) + (u64)V >= want) {
+                atomicMin(&S->lo, B * tid + q);
+                may = true;
             }
-            b1 = (int)__reduce_min_sync(0xffffffffu, (unsigned)b1);
-            b2 = (int)__reduce_min_sync(0xffffffffu, (unsigned)b2);
-            if (lane == 0) {
-                S->lo = min(b1, kSrBins - 1);
-                S->hi = min(b2, kSrBins - 1);
-                S->kmin = 0xffffffffu;
-                S->kmax = 0;
+            if (!must && c >= want + (u64)V) {
+                atomicMin(&S->hi, B * tid + q);
+                must = true;
             }
         }
         __syncthreads();
         const int b1 = S->lo, b2 = S->hi;
-        u64 above = 0, sum = 0;
-        each([&](uint32_t m) { return exponent(m) > -42.0f && bin_of(exponent(m)) <= b2; },
-             [&](uint32_t key, int i) {
-                 const float e = exponent(key), r = exp2f(e);
-                 const u64 w = whole(r);
-                 if (w == 0) return;
-                 const int b = bin_of(e);
-                 if (b < b1) {
-                     above += w;
-                     if (!(r < minp)) sum += w;
-                 } else if (b <= b2) {
-                     append(place(key, i), w);
+        u64 above = 0;
+        SrSum sum, cut_off;  // what min-p leaves, and takes, above the list
+        each([&](float m) { return exponent(m) > -42.0f && bin_of(exponent(m)) <= b2; },
+             [&](float4 v, int i) {
+#pragma unroll
+                 for (int q = 0; q < 4; q++) {
+                     const float f = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w, e = exponent(f), w = fast_exp2(e);
+                     if (e <= -41.0f) continue;
+                     const int b = bin_of(e);
+                     if (b < b1) {
+                         sum.add(w < minp ? 0.0f : w);
+                         if (minp > 0.0f) cut_off.add(w < minp ? w : 0.0f);
+                     } else if (b <= b2) {
+                         append(place(sr_key(f), i + q));
+                     }
                  }
              },
              [&](int s) {
-                 sum = warp_total(sum);
-                 if (lane == 0) seg[s] = sum;
-                 sum = 0;
+                 const u64 mine = sum.flush();
+                 above += mine + cut_off.flush();
+                 cut_off.sum = 0;
+                 const u64 t = warp_total(mine);
+                 if (lane == 0) seg[s] = t;
+                 sum.sum = 0;
              });
         above = total_of(above);
-        const int n = S->n;
+        const int n = gather();
         if (n > kSrList) return false;
-        // The tokens of the list up to the one that reaches `rest`: rounds of 256 bins of their keys, each
-        // within the bin that the last one found, until few tokens are left in it.
-        u64 rest = want - above;
+        if (rank == 0) last_of_list(n, want - above);
+        sync();
+        least = S->found[1];
+        return true;
+    }
+
+    // By slice 0: the list's tokens up to the one that reaches `rest`, which all slices are told, added to
+    // their segments.  Rounds of 256 bins of their keys, each within the bin that the last one found,
+    // until few tokens are left in it.
+    __device__ __forceinline__ void last_of_list(int n, u64 rest) {
         uint32_t from = 0xffffffffu, to = 0;
         for (int c = tid; c < n; c += NT) {
-            const uint32_t key = (uint32_t)(S->list[c].at >> 32);
+            const uint32_t key = (uint32_t)(S->list[c] >> 32);
             from = min(from, key);
             to = max(to, key);
         }
         from = __reduce_min_sync(0xffffffffu, from);
         to = __reduce_max_sync(0xffffffffu, to);
-        if (lane == 0) {
-            atomicMin(&S->kmin, from);
-            atomicMax(&S->kmax, to);
-        }
         __syncthreads();
-        from = S->kmin;
-        to = S->kmax;
+        if (lane == 0) S->warp[warp] = (u64)from << 32 | to;
+        __syncthreads();
+        for (int w = 0; w < NT / 32; w++) {
+            from = min(from, (uint32_t)(S->warp[w] >> 32));
+            to = max(to, (uint32_t)S->warp[w]);
+        }
         int left = n;
         while (left > 64 && from < to) {
             const int sh = max(0, 24 - __clz(to - from));
@@ -456,25 +652,13 @@ template <typename T, int NT> struct SrRow {
             }
             __syncthreads();
             for (int c = tid; c < n; c += NT) {
-                const uint32_t key = (uint32_t)(S->list[c].at >> 32);
+                const uint32_t key = (uint32_t)(S->list[c] >> 32);
                 if (key < from || key > to) continue;
-                atomicAdd(&S->bins[(key - from) >> sh], S->list[c].w);
+                atomicAdd(&S->bins[(key - from) >> sh], whole(fast_exp2(exponent(sr_value(key)))));
                 atomicAdd(&S->hist[(key - from) >> sh], 1u);
             }
             __syncthreads();
-            if (warp == 0) {
-                u64 t = 0;
-#pragma unroll
-                for (int q = 0; q < 8; q++) t += S->bins[255 - 8 * lane - q];
-                const u64 upto = warp_scan(t, lane);
-                if (upto >= rest && upto - t < rest) {
-                    u64 a = upto - t;
-                    int b = 255 - 8 * lane;
-                    while (a + S->bins[b] < rest) a += S->bins[b--];
-                    S->lo = b;
-                    S->found[0] = a;
-                }
-            }
+            if (warp == 0) top_bin(S->bins, rest);
             __syncthreads();
             rest -= S->found[0];
             left = (int)S->hist[S->lo];
@@ -483,54 +667,71 @@ template <typename T, int NT> struct SrRow {
             __syncthreads();
         }
         // the last one: the tokens before it within [from, to] do not reach `rest`, with it they do
+        if (tid == 0) S->n = 0;
+        __syncthreads();
         for (int c = tid; c < n; c += NT) {
-            const u64 at = S->list[c].at;
-            const uint32_t key = (uint32_t)(at >> 32);
-            if (key < from || key > to) continue;
+            const uint32_t key = (uint32_t)(S->list[c] >> 32);
+            if (key >= from && key <= to) S->sorted[atomicAdd(&S->n, 1)] = S->list[c];
+        }
+        __syncthreads();
+        left = S->n;
+        for (int c = tid; c < left; c += NT) {
+            const u64 at = S->sorted[c];
             u64 before = 0;
-            for (int j = 0; j < n; j++) {
-                const u64 o = S->list[j].at;
-                if (o > at && (uint32_t)(o >> 32) <= to) before += S->list[j].w;
+            for (int j = 0; j < left; j++) {
+                const u64 o = S->sorted[j];
+                if (o > at) before += whole(weight_at(o));
             }
-            if (before < rest && before + S->list[c].w >= rest) S->found[1] = at;
+            if (before < rest && before + whole(weight_at(at)) >= rest)
+                for (int r = 0; r < slices; r++) at_slice(S, r)->found[1] = at;
         }
         __syncthreads();
-        least = S->found[1];
+        const u64 least = S->found[1];
+        const int len = i1 - i0;  // of slice 0, so of all but the last
         for (int c = tid; c < n; c += NT) {
-            const u64 at = S->list[c].at;
-            if (at < least || exp2f(exponent((uint32_t)(at >> 32))) < minp) continue;
-            atomicAdd(&seg[(0xffffffffu - (uint32_t)at) / kSrSegment], S->list[c].w);
+            const u64 at = S->list[c];
+            const float w = weight_at(at);
+            if (at < least || w < minp) continue;
+            const int i = (int)(0xffffffffu - (uint32_t)at), r = CL ? i / len : 0;
+            atomicAdd(&at_slice(seg, r)[(i - r * len) / kSrSegment], whole(w));
         }
-        __syncthreads();
-        return true;
     }
 
-    // The general cut: `least` moved up to the shortest prefix of what it keeps with a sum of at least
-    // `want` of amount(key); every token is looked at, a byte of the key and then of the index at a time.
+    // By one warp: the first bin from the top at which the sum of a[0 .. 255] reaches `want` (S->lo), and
+    // the sum above it (S->found[0]).
+    __device__ __forceinline__ void top_bin(const u64 *a, u64 want) const {
+        u64 t = 0;
+#pragma unroll
+        for (int q = 0; q < 8; q++) t += a[255 - 8 * lane - q];
+        const u64 upto = warp_scan(t, lane);
+        if (upto >= want && upto - t < want) {
+            u64 c = upto - t;
+            int b = 255 - 8 * lane;
+            while (c + a[b] < want) c += a[b--];
+            S->lo = b;
+            S->found[0] = c;
+        }
+    }
+
+    // The general way: weights of keys, with every infinity in its place.
+    __device__ __forceinline__ float any_weight(float v) const {
+        const float d = fmaxf(v, -INFINITY) - vmax;
+        return fmaxf(v, -INFINITY) == vmax ? 1.0f : d == -INFINITY ? 0.0f : fast_exp2(d * scale);
+    }
+    // `least` moved up to the shortest prefix of what it keeps with a sum of at least `want` of
+    // amount(logit), a byte at a time.
     template <typename A> __device__ __forceinline__ void cut(u64 &least, u64 want, A amount) const {
         u64 prefix = 0, mask = 0;
         for (int d = 56; d >= 0; d -= 8) {
             for (int b = tid; b < 256; b += NT) S->bins[b] = 0;
             __syncthreads();
-            for (int i = tid; i < V; i += NT) {
-                const uint32_t key = sr_key(sr_load(x, i));
-                const u64 at = place(key, i);
-                if ((at & mask) == prefix && at >= least) atomicAdd(&S->bins[at >> d & 255u], amount(key));
+            for (int i = i0 + tid; i < i1; i += NT) {
+                const float v = sr_load(x, i);
+                const u64 at = place(sr_key(v), i);
+                if ((at & mask) == prefix && at >= least) atomicAdd(&S->bins[at >> d & 255u], amount(v));
             }
-            __syncthreads();
-            if (warp == 0) {
-                u64 t = 0;
-#pragma unroll
-                for (int q = 0; q < 8; q++) t += S->bins[255 - 8 * lane - q];
-                const u64 upto = warp_scan(t, lane);
-                if (upto >= want && upto - t < want) {
-                    u64 a = upto - t;
-                    int b = 255 - 8 * lane;
-                    while (a + S->bins[b] < want) a += S->bins[b--];
-                    S->lo = b;
-                    S->found[0] = a;
-                }
-            }
+            merge(S->bins, S->sums, 256);
+            if (warp == 0) top_bin(S->sums, want);
             __syncthreads();
             prefix |= (u64)S->lo << d;
             mask |= (u64)255 << d;
@@ -539,124 +740,201 @@ template <typename T, int NT> struct SrRow {
         }
         least = prefix;
     }
+    __device__ __forceinline__ void general(int k, float p, float u) {
+        u64 least = 0;
+        if (k > 0) cut(least, (u64)k, [](float) { return (u64)1; });
+        if (p < 1.0f) {
+            u64 mass = 0;
+            for (int i = i0 + tid; i < i1; i += NT) {
+                const float v = sr_load(x, i);
+                if (place(sr_key(v), i) >= least) mass += whole(any_weight(v));
+            }
+            const u64 M = total_of(mass);
+            cut(least, share_of(p, M), [&](float v) { return whole(any_weight(v)); });
+        }
+        // The draw, token by token: a thread's are adjacent.
+        const int per = (i1 - i0 + NT - 1) / NT, lo = min(i1, i0 + tid * per), hi = min(i1, lo + per);
+        auto weight = [&](int i) {
+            const float v = sr_load(x, i), w = any_weight(v);
+            return place(sr_key(v), i) >= least && !(w < minp) ? whole(w) : 0;
+        };
+        u64 mine = 0, M, base = 0;
+        for (int i = lo; i < hi; i++) mine += weight(i);
+        u64 upto = scan(mine, M);
+        if (CL) {
+            const int q = share(M);
+            M = 0;
+            for (int r = 0; r < slices; r++) {
+                if (r == rank) base = M;
+                M += S->slices[q][r];
+            }
+        }
+        upto += base;
+        const u64 target = target_of(u, M);
+        if (upto > target && upto - mine <= target) {
+            u64 a = upto - mine;
+            for (int i = lo; i < hi; i++) {
+                a += weight(i);
+                if (a > target) {
+                    *out = i;
+                    break;
+                }
+            }
+        }
+    }
 };
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) sample_rows_kernel(const __grid_constant__ SampleRowsArgs A, int shift) {
+// Apart from the kernel, whose registers its loops would take.
+template <typename R> __device__ __noinline__ void sample_general(R row, int k, float p, float u) { row.general(k, p, u); }
+
+template <typename T, bool CL>
+__global__ void __launch_bounds__(kSrThreads, kSrResident) sample_rows_kernel(const __grid_constant__ SampleRowsArgs A, int slices, int shift) {
+    constexpr int NT = kSrThreads;
     extern __shared__ __align__(16) uint8_t smem[];
-    SrRow<T, NT> R;
+    SrRow<T, CL> R;
     R.V = A.vocab;
+    R.slices = CL ? slices : 1;
+    R.rank = CL ? blockIdx.x % slices : 0;
+    // slices are whole segments, the last ones may be shorter or empty
+    const int len = (A.vocab + R.slices * kSrSegment - 1) / (R.slices * kSrSegment) * kSrSegment;
+    R.i0 = min(A.vocab, R.rank * len);
+    R.i1 = min(A.vocab, R.i0 + len);
     R.shift = shift;
     R.S = (SrShared *)smem;
     R.seg = (u64 *)(R.S + 1);
-    R.gm = (uint32_t *)(R.seg + (A.vocab + kSrSegment - 1) / kSrSegment);
+    R.gm = (uint32_t *)(R.seg + len / kSrSegment);
     R.tid = threadIdx.x;
     R.lane = R.tid & 31;
     R.warp = R.tid >> 5;
+    R.set = 0;
     R.wide = ((uintptr_t)A.logits | (uintptr_t)(A.ld * (long long)sizeof(T))) % (4 * sizeof(T)) == 0;
     SrShared *S = R.S;
     const int V = A.vocab, tid = R.tid, lane = R.lane;
     pdl_wait();
     pdl_trigger();
-    for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
-        const T *x = R.x = (const T *)A.logits + row * A.ld;
+    const int step = gridDim.x / R.slices;
+    for (long long row = blockIdx.x / R.slices; row < A.rows; row += step) {
+        R.x = (const T *)A.logits + row * A.ld;
+        R.out = A.next_ids + row;
         const float temp = A.temperature ? __ldg(A.temperature + row) : 1.0f;
         int k = A.top_k ? __ldg(A.top_k + row) : 0;
         k = k > 0 && k < V ? k : 0;
         const float p = A.top_p ? __ldg(A.top_p + row) : 1.0f, u = __ldg(A.uniforms + row);
         const float m = A.min_p ? __ldg(A.min_p + row) : 0.0f;
         R.minp = m > 0.f ? fminf(m, 1.0f) : 0.0f;
-        __syncthreads();  // the last row is done with the shared memory
+        R.sync();  // the last row is done with the shared memory
         if (shift > 4) {
             for (int g = tid; g < R.groups(); g += NT) R.gm[g] = 0;
             __syncthreads();
         }
         // the largest logit of every 16 tokens (four lanes), four loads in flight
         float most = -INFINITY;
-        for (int c = R.warp * 512; c < V; c += NT / 32 * 512) {
+        for (int c = R.i0 + R.warp * 512; c < R.i1; c += NT / 32 * 512) {
             float4 v[4];
+            if (R.wide && c + 512 <= R.i1) {
 #pragma unroll
-            for (int q = 0; q < 4; q++) v[q] = sr_load4(x, c + 128 * q + 4 * lane, V, R.wide);
+                for (int q = 0; q < 4; q++) v[q] = sr_wide4(R.x, c + 128 * q + 4 * lane);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; q++) v[q] = sr_load4(R.x, c + 128 * q + 4 * lane, R.i1, R.wide);
+            }
 #pragma unroll
             for (int q = 0; q < 4; q++) {
-                float m = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                most = fmaxf(most, m);
+                float g = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
+                g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+                g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+                most = fmaxf(most, g);
                 const int i = c + 128 * q + 4 * lane;
-                if ((lane & 3) == 0 && i < V) {
+                if ((lane & 3) == 0 && i < R.i1) {
                     if (shift == 4)
-                        R.gm[i >> 4] = sr_key(m);
+                        R.gm[(i - R.i0) >> 4] = sr_key(g);
                     else
-                        atomicMax(&R.gm[i >> shift], sr_key(m));
+                        atomicMax(&R.gm[(i - R.i0) >> shift], sr_key(g));
                 }
             }
         }
-        const uint32_t mine = __reduce_max_sync(0xffffffffu, sr_key(most));
-        if (lane == 0) S->warp[R.warp] = mine;
         if (tid == 0) S->n = 0;
-        __syncthreads();
-        uint32_t top = 0;
-#pragma unroll 8
-        for (int w = 0; w < NT / 32; w++) top = max(top, (uint32_t)S->warp[w]);
-        R.top = top;
-        R.vmax = sr_value(top);
-        int id = 0;
+        R.vmax = sr_value((uint32_t)R.most_of(sr_key(most)));
         if (R.vmax == -INFINITY) {
-            id = 0;
-        } else if (!(temp > 0.f) || k == 1) {
-            id = R.first_top();
-        } else {
-            R.scale = 1.4426950408889634f / temp;
-            bool done = false;
-            if (V <= kSrList / 2 || (k > 0 && k <= min(R.groups(), kSrList / 2))) {
-                const uint32_t least = V <= kSrList / 2 ? 0u : R.kth_maximum(k);
-                R.each([&](uint32_t m) { return m >= least; },
-                       [&](uint32_t key, int i) {
-                           if (i < V && key >= least) R.append(R.place(key, i), R.whole(exp2f(R.exponent(key))));
+            if (R.rank == 0 && tid == 0) *R.out = 0;
+            continue;
+        }
+        if (!(temp > 0.f) || k == 1) {
+            R.first_top();
+            continue;
+        }
+        R.scale = fminf(1.4426950408889634f / temp, FLT_MAX);
+        if (R.vmax < INFINITY) {
+            if (V <= kSrList / 2 || (k > 0 && k <= min((V + (1 << shift) - 1) >> shift, kSrList / 2))) {
+                float width = 0.0f;
+                const int last = V <= kSrList / 2 ? 255 : R.kth_bin(k, width);
+                // tokens of -infinity have no weight and come last in the order: never listed
+                R.each([&](float g) { return g > -INFINITY && R.bin_of_value(g, width) <= last; },
+                       [&](float4 v, int i) {
+#pragma unroll
+                           for (int q = 0; q < 4; q++) {
+                               const float f = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
+                               if (f > -INFINITY && R.bin_of_value(f, width) <= last)
+                                   R.append(R.place(sr_key(f), i + q));
+                           }
                        },
                        [](int) {});
-                __syncthreads();
-                done = S->n <= kSrList;
-                if (done) id = R.draw_list(S->n, k, p, u);
+                const int n = R.gather();
+                if (n <= kSrList) {
+                    if (R.rank == 0) R.draw_list(n, k, p, u);
+                    continue;
+                }
             } else if (k == 0 && p < 1.0f) {
                 u64 least;
-                done = R.nucleus(p, least);
-                if (done) id = R.draw_segments(least, u);
-            }
-            if (!done) {
-                u64 least = 0;
-                if (k > 0) R.cut(least, (u64)k, [](uint32_t) { return (u64)1; });
-                if (p < 1.0f) {
-                    u64 mass = 0;
-                    for (int i = tid; i < V; i += NT) {
-                        const uint32_t key = sr_key(sr_load(x, i));
-                        if (R.place(key, i) >= least) mass += R.whole(exp2f(R.exponent(key)));
-                    }
-                    const u64 M = R.total_of(mass);
-                    R.cut(least, max((u64)1, (u64)ceil((double)fmaxf(p, 0.0f) * (double)M)),
-                          [&](uint32_t key) { return R.whole(exp2f(R.exponent(key))); });
+                if (R.nucleus(p, least)) {
+                    R.draw_segments(least, u);
+                    continue;
                 }
-                R.sum_segments(least);
-                id = R.draw_segments(least, u);
+            } else if (k == 0) {
+                R.sum_segments();
+                R.draw_segments(0, u);
+                continue;
             }
         }
-        if (tid == 0) A.next_ids[row] = id;
+        sample_general(R, k, p, u);
+        R.set = 0;
     }
+    R.sync();  // nobody leaves while another slice may still look into its shared memory
 }
 
-template <typename T, int NT> static cudaError_t launch_sample(const SampleRowsArgs &a, cudaStream_t s) {
+template <typename T, bool CL> static cudaError_t launch_sample(const SampleRowsArgs &a, int slices, cudaStream_t s) {
+    const int len = (a.vocab + slices * kSrSegment - 1) / (slices * kSrSegment) * kSrSegment;
     int shift = 4;
-    while (((a.vocab - 1) >> shift) + 1 > kSrGroups) shift++;
-    const size_t smem = sizeof(SrShared) + (size_t)((a.vocab + kSrSegment - 1) / kSrSegment) * 8 +
-                        (size_t)(((a.vocab - 1) >> shift) + 1) * 4;
-    const cudaError_t e = allow_smem((const void *)sample_rows_kernel<T, NT>);
+    while (((len - 1) >> shift) + 1 > kSrGroups) shift++;
+    const size_t smem = sizeof(SrShared) + (size_t)(len / kSrSegment) * 8 + (size_t)(((len - 1) >> shift) + 1) * 4;
+    const cudaError_t e = allow_smem((const void *)sample_rows_kernel<T, CL>);
     if (e != cudaSuccess) return e;
-    return launch_pdl(sample_rows_kernel<T, NT>, dim3(std::min(a.rows, 1 << 20)), dim3(NT), smem, s, a, shift);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(std::min(a.rows, 1 << 20) * slices);
+    cfg.blockDim = dim3(kSrThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2]{};
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = slices;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CL ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, sample_rows_kernel<T, CL>, a, slices, shift);
 }
 
-cudaError_t sample_rows_launch(const SampleRowsArgs &a, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_sample<uint16_t, 512>(a, s) : launch_sample<float, 512>(a, s);
+cudaError_t sample_rows_launch(const SampleRowsArgs &a, bool bf16, int sms, cudaStream_t s) {
+    // Slices of 16,384 tokens and more: what an SM has to do is then cut finely enough to be even, and rows
+    // that wait for memory run beside rows that do not.  Of 4,096 and more while there is room for all rows.
+    int slices = 1;
+    while (slices < kSrCluster &&
+           (a.vocab / (2 * slices) >= 16384 ||
+            (a.vocab / (2 * slices) >= 4096 && (long long)a.rows * 2 * slices <= kSrResident * sms)))
+        slices *= 2;
+    if (slices > 1) return bf16 ? launch_sample<uint16_t, true>(a, slices, s) : launch_sample<float, true>(a, slices, s);
+    return bf16 ? launch_sample<uint16_t, false>(a, 1, s) : launch_sample<float, false>(a, 1, s);
 }
 
 }  // namespace slm
