@@ -102,7 +102,7 @@ struct SrShared {
         struct {
             uint32_t hist[kSrBins], merged[kSrBins];
         };
-        uint32_t by_index[kSrList];  // draw_list
+        uint32_t queue[kSrList];     // list_bins
     };
     u64 list[kSrList], sorted[kSrList];  // places in the order
 };
@@ -212,6 +212,24 @@ template <typename T, bool CL> struct SrRow {
         }
         return t;
     }
+    // The largest of both halves of v, each for itself.
+    __device__ __forceinline__ u64 both_most_of(u64 v) {
+        auto both = [](u64 a, u64 b) {
+            return (u64)max((uint32_t)(a >> 32), (uint32_t)(b >> 32)) << 32 | max((uint32_t)a, (uint32_t)b);
+        };
+        v = (u64)__reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32)) << 32 | __reduce_max_sync(0xffffffffu, (uint32_t)v);
+        __syncthreads();
+        if (lane == 0) S->warp[warp] = v;
+        __syncthreads();
+        u64 t = 0;
+#pragma unroll 8
+        for (int i = 0; i < NT / 32; i++) t = both(t, S->warp[i]);
+        if (CL) {
+            const int k = share(t);
+            for (int r = 0; r < slices; r++) t = both(t, S->slices[k][r]);
+        }
+        return t;
+    }
     __device__ __forceinline__ u64 most_of(u64 v) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -249,8 +267,9 @@ template <typename T, bool CL> struct SrRow {
     }
 
     // f(four logits, index) of the slice's tokens of those groups that pass(maximum), 512 tokens a warp at
-    // a time so that four loads are in flight; done(segment) after each segment's.  Behind the slice's
-    // end the logits are -infinity.
+    // a time so that four loads are in flight; done(segment) after each segment's.  In the place of tokens
+    // behind the slice's end, and of those of other groups, there is -infinity.  f's work has few
+    // branches, so that the 16 tokens of a thread are worked on side by side.
     template <typename P, typename F, typename D> __device__ __forceinline__ void each(P pass, F f, D done) const {
         for (int s0 = i0 + warp * kSrSegment; s0 < i1; s0 += NT / 32 * kSrSegment) {
 #pragma unroll 1
@@ -271,12 +290,10 @@ template <typename T, bool CL> struct SrRow {
                         v[q] = mine[q] ? sr_wide4(x, c + 128 * q + 4 * lane) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        if (mine[q]) v[q] = sr_load4(x, c + 128 * q + 4 * lane, i1, wide);
+                    for (int q = 0; q < 4; q++) v[q] = sr_load4(x, mine[q] ? c + 128 * q + 4 * lane : i1, i1, wide);
                 }
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    if (mine[q]) f(v[q], c + 128 * q + 4 * lane);
+                for (int q = 0; q < 4; q++) f(v[q], c + 128 * q + 4 * lane);
             }
             done((s0 - i0) / kSrSegment);
         }
@@ -336,12 +353,8 @@ template <typename T, bool CL> struct SrRow {
 
     // 256 bins of equal width between the largest logit and the groups' smallest maximum; the bin that
     // the k-th largest of all maxima is in.
-    __device__ __forceinline__ int kth_bin(int k, float &width) {
+    __device__ __forceinline__ int kth_bin(int k, float low, float &width) {
         const int n = groups();
-        uint32_t least = 0xffffffffu;
-        for (int g = tid; g < n; g += NT)
-            if (sr_value(gm[g]) > -INFINITY) least = min(least, gm[g]);
-        const float low = sr_value(0xffffffffu - (uint32_t)most_of(0xffffffffu - least));
         const float range = vmax - low;
         width = range > 1e-30f ? 255.0f / range : 0.0f;
         for (int b = tid; b < 256; b += NT) S->hist[b] = 0;
@@ -366,6 +379,40 @@ template <typename T, bool CL> struct SrRow {
         return (int)fminf((vmax - v) * width, 255.0f);
     }
 
+    // The list of the tokens in the bins up to `last`.  Groups that hold some are put in a queue first, so
+    // that the loads of all of them are in flight together.
+    __device__ __forceinline__ void list_bins(float width, int last) const {
+        const int n = groups();
+        if (tid == 0) S->lo = 0;
+        __syncthreads();
+        for (int g = tid; g < n; g += NT) {
+            const float v = sr_value(gm[g]);
+            if (v > -INFINITY && bin_of_value(v, width) <= last) {
+                const int at = atomicAdd(&S->lo, 1);
+                if (at < kSrList) S->queue[at] = (uint32_t)g;
+            }
+        }
+        __syncthreads();
+        const int queued = S->lo;
+        auto list = [&](float4 v, int i) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float f = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
+                // tokens of -infinity have no weight and come last in the order: never listed
+                if (f > -INFINITY && bin_of_value(f, width) <= last) append(place(sr_key(f), i + q));
+            }
+        };
+        if (queued > kSrList) {
+            each([&](float g) { return g > -INFINITY && bin_of_value(g, width) <= last; }, list, [](int) {});
+            return;
+        }
+        const int quads = queued << (shift - 2);  // of four tokens
+        for (int c = tid; c < quads; c += NT) {
+            const int i = i0 + (int)(S->queue[c >> (shift - 2)] << shift) + 4 * (c & ((1 << (shift - 2)) - 1));
+            if (i < i1) list(sr_load4(x, i, i1, wide), i);
+        }
+    }
+
     static __device__ __forceinline__ u64 target_of(float u, u64 M) {
         u = u >= 0.f ? fminf(u, 1.0f) : 0.f;
         return min((u64)((double)u * (double)M), M - 1);
@@ -377,31 +424,31 @@ template <typename T, bool CL> struct SrRow {
     // By slice 0: the list's tokens after top-k (k = 0: all of them), top-p and min-p; the draw.  The
     // list holds the first k tokens of the row at least.
     __device__ __forceinline__ void draw_list(int n, int k, float p, float u) const {
-        sort(S->list, n, [&](int rank, u64 at) { S->sorted[rank] = at; });
+        sort(S->list, n);
         // every cut keeps a prefix: adjacent tokens a thread, and the sum before each
         const int per = (n + NT - 1) / NT, c0 = min(n, tid * per), c1 = min(k > 0 ? min(n, k) : n, c0 + per);
         u64 mass = 0, M;
-        for (int c = c0; c < c1; c++) mass += whole(weight_at(S->sorted[c]));
+        for (int c = c0; c < c1; c++) mass += whole(weight_at(S->list[c]));
         u64 before = scan(mass, M) - mass;
         const u64 want = p < 1.0f ? share_of(p, M) : ~0ull;
         u64 left = 0;
         for (int c = c0; c < c1; c++) {
-            const float w = weight_at(S->sorted[c]);
+            const float w = weight_at(S->list[c]);
             left += before < want && !(w < minp);
             before += whole(w);
         }
         const int m = (int)cta_total(left);
-        for (int c = tid; c < m; c += NT) S->list[c] = S->sorted[c] << 32 | (uint32_t)c;  // complemented index first
+        for (int c = tid; c < m; c += NT) S->sorted[c] = S->list[c] << 32 | (uint32_t)c;  // complemented index first
         __syncthreads();
-        sort(S->list, m, [&](int rank, u64 at) { S->by_index[rank] = (uint32_t)at; });
+        sort(S->sorted, m);
         const int share = (m + NT - 1) / NT, d0 = min(m, tid * share), d1 = min(m, d0 + share);
         mass = 0;
-        for (int d = d0; d < d1; d++) mass += whole(weight_at(S->sorted[S->by_index[d]]));
+        for (int d = d0; d < d1; d++) mass += whole(weight_at(S->list[(uint32_t)S->sorted[d]]));
         const u64 upto = scan(mass, M), target = target_of(u, M);
         if (upto > target && upto - mass <= target) {
             u64 a = upto - mass;
             for (int d = d0; d < d1; d++) {
-                const u64 at = S->sorted[S->by_index[d]];
+                const u64 at = S->list[(uint32_t)S->sorted[d]];
                 a += whole(weight_at(at));
                 if (a > target) {
                     *out = (int)(0xffffffffu - (uint32_t)at);
@@ -410,46 +457,59 @@ template <typename T, bool CL> struct SrRow {
             }
         }
     }
-    // put(rank, value) of n different values, the largest first.  A warp sorts 64 at a time, two a lane (a
-    // bitonic network); a value's rank is its place there plus the larger ones of every other 64.
-    template <typename P> __device__ __forceinline__ void sort(u64 *a, int n, P put) const {
-        for (int c = 64 * warp; c < n; c += 64 * (NT / 32)) {
-            u64 x = c + lane < n ? a[c + lane] : 0, y = c + 32 + lane < n ? a[c + 32 + lane] : 0;
+    // a[0 .. n) in order, the largest first (a bitonic network over the next power of two, at least 64;
+    // the places behind n become 0).  Exchanges of up to 32 places apart stay within a warp's 64 values,
+    // two a lane.
+    __device__ __forceinline__ void sort(u64 *a, int n) const {
+        int m = 64;
+        while (m < n) m <<= 1;
+        for (int c = n + tid; c < m; c += NT) a[c] = 0;
+        __syncthreads();
+        auto within = [&](int c, int size, u64 &x, u64 &y) {  // exchanges 32 to 1 apart of the network's `size`
 #pragma unroll
-            for (int size = 2; size <= 64; size <<= 1)
+            for (int stride = 32; stride > 0; stride >>= 1) {
+                if (stride >= size) continue;
+                if (stride == 32) {
+                    const u64 hi = max(x, y), lo = min(x, y);
+                    const bool down = (c & size) == 0;
+                    x = down ? hi : lo;
+                    y = down ? lo : hi;
+                } else {
+                    const u64 u = __shfl_xor_sync(0xffffffffu, x, stride), v = __shfl_xor_sync(0xffffffffu, y, stride);
+                    const bool first = (lane & stride) == 0;
+                    x = first == (((c + lane) & size) == 0) ? max(x, u) : min(x, u);
+                    y = first == (((c + 32 + lane) & size) == 0) ? max(y, v) : min(y, v);
+                }
+            }
+        };
+        for (int c = 64 * warp; c < m; c += 64 * (NT / 32)) {
+            u64 x = a[c + lane], y = a[c + 32 + lane];
 #pragma unroll
-                for (int stride = size >> 1; stride > 0; stride >>= 1) {
-                    if (stride == 32) {
-                        const u64 hi = max(x, y);
-                        y = min(x, y);
-                        x = hi;
-                    } else {
-                        const u64 u = __shfl_xor_sync(0xffffffffu, x, stride), v = __shfl_xor_sync(0xffffffffu, y, stride);
-                        const bool first = (lane & stride) == 0;
-                        x = first == ((lane & size) == 0) ? max(x, u) : min(x, u);
-                        y = first == (((lane + 32) & size) == 0) ? max(y, v) : min(y, v);
+            for (int size = 2; size <= 64; size <<= 1) within(c, size, x, y);
+            a[c + lane] = x;
+            a[c + 32 + lane] = y;
+        }
+        __syncthreads();
+        for (int size = 128; size <= m; size <<= 1) {
+            for (int stride = size >> 1; stride >= 64; stride >>= 1) {
+                for (int i = tid; i < m / 2; i += NT) {
+                    const int c = 2 * i - (i & (stride - 1));
+                    const u64 x = a[c], y = a[c + stride];
+                    if ((x < y) == ((c & size) == 0)) {
+                        a[c] = y;
+                        a[c + stride] = x;
                     }
                 }
-            if (c + lane < n) a[c + lane] = x;
-            if (c + 32 + lane < n) a[c + 32 + lane] = y;
-        }
-        __syncthreads();
-        for (int i = tid; i < n; i += NT) {
-            const u64 me = a[i];
-            const int mine = i & ~63;
-            int rank = i & 63;
-#pragma unroll 4
-            for (int c = 0; c < n; c += 64) {
-                if (c == mine) continue;
-                int lo = 0;  // how many of the 64 are larger
-#pragma unroll
-                for (int step = 64; step; step >>= 1)
-                    if (lo + step <= 64 && c + lo + step <= n && a[c + lo + step - 1] > me) lo += step;
-                rank += lo;
+                __syncthreads();
             }
-            put(rank, me);
+            for (int c = 64 * warp; c < m; c += 64 * (NT / 32)) {
+                u64 x = a[c + lane], y = a[c + 32 + lane];
+                within(c, size, x, y);
+                a[c + lane] = x;
+                a[c + 32 + lane] = y;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 
     // The draw from the tokens from `least` on, by the segments' sums.
@@ -547,15 +607,20 @@ template <typename T, bool CL> struct SrRow {
         SrSum mass;
         each([&](float m) { return exponent(m) > -42.0f; },
              [&](float4 v, int) {
+                 int b[4];
+                 uint32_t t[4];
+                 bool some[4];
 #pragma unroll
                  for (int q = 0; q < 4; q++) {
                      const float e = exponent(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w), w = fast_exp2(e);
-                     if (e <= -41.0f) continue;
-                     mass.add(w);
-                     const int b = bin_of(e);  // w 2^floor(b / 32) is between 2^-1.01 and 2^0.02
-                     atomicAdd(&S->hist[b],
-                               __float2uint_rz(__uint_as_float(__float_as_uint(w) + ((uint32_t)(bits + (b >> 5)) << 23))));
+                     some[q] = e > -41.0f;
+                     mass.add(some[q] ? w : 0.0f);
+                     b[q] = bin_of(e);  // w 2^floor(b / 32) is between 2^-1.01 and 2^0.02
+                     t[q] = __float2uint_rz(__uint_as_float(__float_as_uint(w) + ((uint32_t)(bits + (b[q] >> 5)) << 23)));
                  }
+#pragma unroll
+                 for (int q = 0; q < 4; q++)
+                     if (some[q]) atomicAdd(&S->hist[b[q]], t[q]);
                  mass.flush();
              },
              [](int) {});
@@ -594,17 +659,20 @@ template <typename T, bool CL> struct SrRow {
         SrSum sum, cut_off;  // what min-p leaves, and takes, above the list
         each([&](float m) { return exponent(m) > -42.0f && bin_of(exponent(m)) <= b2; },
              [&](float4 v, int i) {
+                 bool in_list[4], any = false;
 #pragma unroll
                  for (int q = 0; q < 4; q++) {
-                     const float f = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w, e = exponent(f), w = fast_exp2(e);
-                     if (e <= -41.0f) continue;
+                     const float e = exponent(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w), w = fast_exp2(e);
                      const int b = bin_of(e);
-                     if (b < b1) {
-                         sum.add(w < minp ? 0.0f : w);
-                         if (minp > 0.0f) cut_off.add(w < minp ? w : 0.0f);
-                     } else if (b <= b2) {
-                         append(place(sr_key(f), i + q));
-                     }
+                     const bool up = b < b1;
+                     sum.add(up && !(w < minp) ? w : 0.0f);
+                     if (minp > 0.0f) cut_off.add(up && w < minp ? w : 0.0f);
+                     any |= in_list[q] = !up && b <= b2 && e > -41.0f;
+                 }
+                 if (any) {
+#pragma unroll
+                     for (int q = 0; q < 4; q++)
+                         if (in_list[q]) append(place(sr_key(q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w), i + q));
                  }
              },
              [&](int s) {
@@ -829,6 +897,7 @@ __global__ void __launch_bounds__(kSrThreads, kSrResident) sample_rows_kernel(co
         }
         // the largest logit of every 16 tokens (four lanes), four loads in flight
         float most = -INFINITY;
+        uint32_t least = 0xffffffffu;  // key of the smallest maximum that is a number
         for (int c = R.i0 + R.warp * 512; c < R.i1; c += NT / 32 * 512) {
             float4 v[4];
             if (R.wide && c + 512 <= R.i1) {
@@ -844,6 +913,7 @@ __global__ void __launch_bounds__(kSrThreads, kSrResident) sample_rows_kernel(co
                 g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
                 g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
                 most = fmaxf(most, g);
+                if (g > -INFINITY) least = min(least, sr_key(g));
                 const int i = c + 128 * q + 4 * lane;
                 if ((lane & 3) == 0 && i < R.i1) {
                     if (shift == 4)
@@ -854,7 +924,9 @@ __global__ void __launch_bounds__(kSrThreads, kSrResident) sample_rows_kernel(co
             }
         }
         if (tid == 0) S->n = 0;
-        R.vmax = sr_value((uint32_t)R.most_of(sr_key(most)));
+        const u64 ends = R.both_most_of((u64)sr_key(most) << 32 | (0xffffffffu - least));
+        R.vmax = sr_value((uint32_t)(ends >> 32));
+        const float low = sr_value(0xffffffffu - (uint32_t)ends);
         if (R.vmax == -INFINITY) {
             if (R.rank == 0 && tid == 0) *R.out = 0;
             continue;
@@ -867,18 +939,8 @@ __global__ void __launch_bounds__(kSrThreads, kSrResident) sample_rows_kernel(co
         if (R.vmax < INFINITY) {
             if (V <= kSrList / 2 || (k > 0 && k <= min((V + (1 << shift) - 1) >> shift, kSrList / 2))) {
                 float width = 0.0f;
-                const int last = V <= kSrList / 2 ? 255 : R.kth_bin(k, width);
-                // tokens of -infinity have no weight and come last in the order: never listed
-                R.each([&](float g) { return g > -INFINITY && R.bin_of_value(g, width) <= last; },
-                       [&](float4 v, int i) {
-#pragma unroll
-                           for (int q = 0; q < 4; q++) {
-                               const float f = q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w;
-                               if (f > -INFINITY && R.bin_of_value(f, width) <= last)
-                                   R.append(R.place(sr_key(f), i + q));
-                           }
-                       },
-                       [](int) {});
+                const int last = V <= kSrList / 2 ? 255 : R.kth_bin(k, low, width);
+                R.list_bins(width, last);
                 const int n = R.gather();
                 if (n <= kSrList) {
                     if (R.rank == 0) R.draw_list(n, k, p, u);
