@@ -383,17 +383,17 @@ template <typename T, bool CL> struct SrRow {
     // that the loads of all of them are in flight together.
     __device__ __forceinline__ void list_bins(float width, int last) const {
         const int n = groups();
-        if (tid == 0) S->lo = 0;
+        if (tid == 0) S->hi = 0;  // (S->lo may still be read: kth_bin)
         __syncthreads();
         for (int g = tid; g < n; g += NT) {
             const float v = sr_value(gm[g]);
             if (v > -INFINITY && bin_of_value(v, width) <= last) {
-                const int at = atomicAdd(&S->lo, 1);
+                const int at = atomicAdd(&S->hi, 1);
                 if (at < kSrList) S->queue[at] = (uint32_t)g;
             }
         }
         __syncthreads();
-        const int queued = S->lo;
+        const int queued = S->hi;
         auto list = [&](float4 v, int i) {
 #pragma unroll
             for (int q = 0; q < 4; q++) {
