@@ -61,10 +61,7 @@
 
 namespace slm {
 
-// Threads of a CTA: ten warps; scored calls twelve (two of them idle), so that their softmax groups can
-// take registers over from the other roles: 2 x 128 x 208 + 128 x 88 = 384 x 168, what such a CTA is
-// launched with.
-__host__ __device__ constexpr int tc_threads(int score) { return score ? 384 : 320; }
+constexpr int kTcThreads = 320;
 constexpr int kTcBlk = 128;                 // positions per block
 constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]
 constexpr int kTcCols = 512;                // tensor memory columns
@@ -161,6 +158,9 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r) {
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld1(uint32_t addr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_ld64(uint32_t addr, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -222,7 +222,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // Keys from `lim` on become -infinity.  `all` (at most any lane's lim): no lane's key before it does,
 // so groups of 16 below it are left alone (two instructions an element at half rate: a diagonal
 // block took twice as long as the others).
-template <int N> __device__ __forceinline__ void mask64(uint32_t (&s)[N], int lim, int all) {
+template <int N> __device__ __forceinline__ void mask_from(uint32_t (&s)[N], int lim, int all) {
 #pragma unroll
     for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 + 16 > all) {
@@ -232,7 +232,7 @@ template <int N> __device__ __forceinline__ void mask64(uint32_t (&s)[N], int li
         }
 }
 
-template <int N> __device__ __forceinline__ float max64(const uint32_t (&s)[N]) {
+template <int N> __device__ __forceinline__ float max_of(const uint32_t (&s)[N]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int k = 0; k < N; k += 8)
@@ -242,7 +242,7 @@ template <int N> __device__ __forceinline__ float max64(const uint32_t (&s)[N]) 
 }
 
 // Keys before `low` become -infinity.  `all`: at least any lane's low.
-template <int N> __device__ __forceinline__ void mask64_low(uint32_t (&s)[N], int low, int all) {
+template <int N> __device__ __forceinline__ void mask_to(uint32_t (&s)[N], int low, int all) {
 #pragma unroll
     for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 < all) {
@@ -252,7 +252,7 @@ template <int N> __device__ __forceinline__ void mask64_low(uint32_t (&s)[N], in
         }
 }
 
-template <int N> __device__ __forceinline__ float absmax64(const uint32_t (&s)[N]) {
+template <int N> __device__ __forceinline__ float absmax(const uint32_t (&s)[N]) {
     float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < N; k += 8)
@@ -345,25 +345,24 @@ __device__ __forceinline__ void scores(uint32_t (&s)[N], const RowsScores &sc, f
         tiers(std::false_type{});
 }
 
-// The most that a distance's term comes to in the 64 keys from d0 (their first position minus the row's) on.
+// The most that a distance's term comes to in the 32 keys from d0 (their first position minus the row's) on.
 __device__ __forceinline__ float bias_most(float sl, float d0) {
-    const float a = fabsf(d0), b = fabsf(d0 + 63.f), far = fmaxf(a, b);
-    const float near = d0 > 0.f || d0 < -63.f ? fminf(a, b) : 0.f;
+    const float a = fabsf(d0), b = fabsf(d0 + 31.f), far = fmaxf(a, b);
+    const float near = d0 > 0.f || d0 < -31.f ? fminf(a, b) : 0.f;
     return -sl * (sl > 0.f ? near : far);
 }
 
-// P = 2^S of 64 keys: added to the sums, and as bf16 pairs to tensor memory.
-__device__ __forceinline__ void exps64(const uint32_t (&s)[64], uint64_t (&sum)[2], uint32_t addr) {
+// P = 2^S (DONE) or 2^(S c - m c) of 32 keys: added to the sums, and as bf16 pairs.
+template <bool DONE>
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t c2, uint64_t mc2, uint64_t (&sum)[2], uint32_t (&pk)[16]) {
 #pragma unroll
-    for (int k0 = 0; k0 < 64; k0 += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-            const float a = fast_exp2(__uint_as_float(s[k0 + k])), b = fast_exp2(__uint_as_float(s[k0 + k + 1]));
-            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
-            pk[k / 2] = pack_bf16x2(a, b);
-        }
-        tmem_st16(addr + k0 / 2, pk);
+    for (int k = 0; k < 32; k += 2) {
+        float a = __uint_as_float(s[k]), b = __uint_as_float(s[k + 1]);
+        if (!DONE) unpack2(fma2(pack2(a, b), c2, mc2), a, b);
+        a = fast_exp2(a);
+        b = fast_exp2(b);
+        sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+        pk[k / 2] = pack_bf16x2(a, b);
     }
 }
 
@@ -463,7 +462,7 @@ __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool sp
 // ------------------------------------------------------------------ the kernel
 
 template <int HDP, bool PAGED, int SCORE>
-__global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
+__global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
     constexpr int NP = HDP / 64;  // 64-column panels of a [128][head_dim] operand
     // Tensor memory columns: S 128 i, O 256 + HDP i.  P (64 columns) has its own where O leaves
     // room, else the upper half of S, which the softmax holds in registers by then.
@@ -532,11 +531,11 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     Walk w;
     if constexpr (kSpans) {
         RowsStart *start = (RowsStart *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, start, (int *)ring, w, tid, tc_threads(SCORE));
+        masked_layout(A, seq, wstart, start, (int *)ring, w, tid, kTcThreads);
         const long long unit = range_units(wstart[A.nseq], A.P);
         w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), *start);
     } else {
-        rows_layout(A, seq, wstart, tid, tc_threads(SCORE));  // ends with a __syncthreads()
+        rows_layout(A, seq, wstart, tid, kTcThreads);  // ends with a __syncthreads()
     }
     // an item of at most 32 rows is split by keys over the four warps of a group, and worked on twice
     // over whatever its heads' width
@@ -570,7 +569,6 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     RowsPiece p;
 
     if (warp < 8) {
-        if constexpr (kSpans) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------------------------- softmax, a thread per row
         const int i = warp >> 2, r = tid & 127;                 // tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -603,6 +601,19 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
             }
             const bool sees = seen > p.kb0 * kTcBlk && (!kSpans || from < min(seen, p.kb1 * kTcBlk));  // some of the piece's
             const bool blind = kSpans && from >= seen;                                                // nothing at all
+            // over the warp's rows: the least and the most that they see, their first position
+            int seen_all = 0, seen_any = 0, from_all = 0, from_any = 0, pos_any = 0;
+            bool steep = false;
+            if constexpr (kSpans) {
+                seen_all = __reduce_min_sync(0xffffffffu, valid ? seen : 0x7fffffff);
+                seen_any = __reduce_max_sync(0xffffffffu, valid ? seen : 0);
+                from_all = __reduce_max_sync(0xffffffffu, valid ? from : 0);
+                from_any = __reduce_min_sync(0xffffffffu, valid ? from : 0x7fffffff);
+                if (kBias) {
+                    pos_any = __reduce_min_sync(0xffffffffu, valid ? pos : 0x7fffffff);
+                    steep = __any_sync(0xffffffffu, fabsf(sl) > 96.f / 31.f);
+                }
+            }
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             const uint32_t op0 = op;  // phases that this piece's O completes
@@ -624,88 +635,143 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
             for (int j = 0; j < v.n; j++) {
                 if (!(ok = tc_wait(&B->s_full[i], sp, A.status, stop))) break;
                 sp ^= 1;
-                if (kSpans && v.split) {
-                    // The four warps hold the same 32 rows, and each works on 32 keys of the block: their
-                    // maxima and, at the end, sums meet in shared memory, and so do their weights, which
-                    // the tensor core takes from there.
-                    tc_after();
-                    __syncwarp();
+                if constexpr (kSpans) {
+                    // Keys in quarters of 32, by loops whose bodies fit the instruction cache beside the other
+                    // roles': first for the maximum, then, the last quarter first (P of a quarter takes the place
+                    // of keys behind it), for the weights.  In a split item the four warps hold the same 32 rows,
+                    // and each has one quarter: their maxima and, at the end, sums meet in shared memory, and
+                    // their weights, which the tensor core takes from there.
+                    const int t0 = (v.first + j * v.step) * kTcBlk;
+                    const int qa = v.split ? wq : 0, qb = v.split ? wq : 3;
                     float *xs = split_x + 384 * i;
-                    const int t0 = (v.first + j * v.step) * kTcBlk + 32 * wq;
-                    uint32_t x[32];
-                    tmem_ld32(tS + 32 * wq, x);
-                    const int lim = seen - t0, low = from - t0;
+                    float mb = -INFINITY, most = 0.f;
                     int tier = 0;
-                    if (kCap) tier = cap_tier(A.sc, absmax64(x));
-                    if (kX) scores<SCORE>(x, A.sc, c, sl, (float)(t0 - pos), tier, kBias && pre > 0, 0.f);
-                    const int all = __reduce_min_sync(0xffffffffu, lim), low_all = __reduce_max_sync(0xffffffffu, low);
-                    if (all < 32) mask64(x, lim, all);
-                    if (low_all > 0) mask64_low(x, low, low_all);
-                    xs[(j & 1) * 128 + 32 * wq + lane] = max64(x);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&B->quarter[i]);
-                    if (!(ok = tc_wait(&B->quarter[i], hp, A.status, stop))) break;
-                    hp ^= 1;
-                    const float *xr = xs + (j & 1) * 128 + lane;
-                    const float mb = fmaxf(fmaxf(xr[0], xr[32]), fmaxf(xr[64], xr[96]));
-                    if (j == 0) {
-                        m = mb;
-                    } else {
-                        const bool grow = m == -INFINITY ? mb > m : (mb - m) * mu > kTcSlack;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? fast_exp2((m - mb) * mu) : 1.0f;
-                            if (grow) m = mb;
-                            l *= f;
-                            if (wq == 0) {
+                    // keys [lo, hi) of the quarter are those that the row sees; `some`: any row of the warp does
+                    auto mask = [&](uint32_t (&x)[32], int k0) {
+                        if (seen_all < k0 + 32) mask_from(x, seen - k0, seen_all - k0);
+                        if (from_all > k0) mask_to(x, from - k0, from_all - k0);
+                    };
+                    auto some = [&](int k0) { return seen_any > k0 && from_any < k0 + 32; };
+                    const bool both = kBias && pre > 0 && t0 + kTcBlk - 1 > pos_any;
+                    if (busy) {
+                        tc_after();
+                        __syncwarp();
 #pragma unroll 1
-                                for (int d = 0; d < HDP; d += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(tO + d, o);
-#pragma unroll
-                                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                    tmem_st32(tO + d, o);
-                                }
-                                tmem_wait_st();
+                        for (int q = qa; q <= qb; q++) {
+                            const int k0 = t0 + 32 * q;
+                            if (!some(k0)) continue;
+                            uint32_t x[32];
+                            tmem_ld32(tS + 32 * q, x);
+                            if (kCap) most = fmaxf(most, absmax(x));
+                            mask(x, k0);
+                            // Of the products, the largest: tanh is monotone, and a distance's term is at most
+                            // bias_most.  That bound of the maximum is at most 31 |sl| above it (96 where it is
+                            // taken, so that weights of 2^-24 of the largest stay normal numbers).
+                            float y = max_of(x);
+                            if (kX && y != -INFINITY) {
+                                y = kCap ? cap_any(A.sc, c, y) : y * c;
+                                if (kBias) y += bias_most(sl, (float)(k0 - pos));
+                            }
+                            mb = fmaxf(mb, y);
+                        }
+                        if (kCap) tier = cap_tier(A.sc, most);
+                        if (kBias && steep) {  // key by key
+                            mb = -INFINITY;
+#pragma unroll 1
+                            for (int k = 32 * qa; k < 32 * qb + 32; k++) {
+                                uint32_t x1;
+                                tmem_ld1(tS + k, x1);
+                                const float y = kCap ? cap_any(A.sc, c, __uint_as_float(x1)) : __uint_as_float(x1) * c;
+                                if (t0 + k < seen && t0 + k >= from) mb = fmaxf(mb, fmaf(-sl, fabsf((float)(t0 + k - pos)), y));
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * mu;
-                    const uint64_t c2 = pack2(mu, mu), mc2 = pack2(-mc, -mc);
-                    uint64_t sum[2] = {0, 0};
-                    // row `lane`, 16-byte chunk 4 (wq & 1) + q of its 128 bytes in panel wq >> 1
-                    const uint32_t dst = smem_addr(split_p) + kSplitP * i + 4096 * (wq >> 1) + 128 * lane;
-#pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            float a, b;
-                            unpack2(fma2(pack2(__uint_as_float(x[8 * q + k]), __uint_as_float(x[8 * q + k + 1])), c2, mc2), a, b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
-                            w[k / 2] = pack_bf16x2(a, b);
-                        }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((4 * (wq & 1) + q) ^ (lane & 7)) << 4)),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                     : "memory");
-                    }
-                    float a, b;
-                    unpack2(add2(sum[0], sum[1]), a, b);
-                    l += a + b;
-                    if (j == v.n - 1) {  // before the last weights go: then this memory may be the producer's
-                        xs[256 + 32 * wq + lane] = l;
+                    if (v.split) {
+                        xs[(j & 1) * 128 + 32 * wq + lane] = mb;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&B->quarter[i]);
                         if (!(ok = tc_wait(&B->quarter[i], hp, A.status, stop))) break;
                         hp ^= 1;
-                        l = (xs[256 + lane] + xs[288 + lane]) + (xs[320 + lane] + xs[352 + lane]);
+                        const float *xr = xs + (j & 1) * 128 + lane;
+                        mb = fmaxf(fmaxf(xr[0], xr[32]), fmaxf(xr[64], xr[96]));
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (busy) {
+                        if (j == 0) {
+                            m = mb;
+                        } else {
+                            const bool grow = m == -INFINITY ? mb > m : (mb - m) * mu > kTcSlack;
+                            if (__any_sync(0xffffffffu, grow)) {
+                                const float f = grow ? fast_exp2((m - mb) * mu) : 1.0f;
+                                if (grow) m = mb;
+                                l *= f;
+                                if (!v.split || wq == 0) {
+#pragma unroll 1
+                                    for (int d = 0; d < HDP; d += 32) {
+                                        uint32_t o[32];
+                                        tmem_ld32(tO + d, o);
+#pragma unroll
+                                        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                        tmem_st32(tO + d, o);
+                                    }
+                                    tmem_wait_st();
+                                }
+                            }
+                        }
+                        const float mc = m == -INFINITY ? 0.f : m * mu;
+                        uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+                        for (int q = qb; q >= qa; q--) {
+                            const int k0 = t0 + 32 * q;
+                            uint32_t x[32], pk[16];
+                            if (some(k0)) {
+                                tmem_ld32(tS + 32 * q, x);
+                                if (kX) scores<SCORE>(x, A.sc, c, sl, (float)(k0 - pos), tier, both, -mc);
+                                mask(x, k0);
+                                weights32<kX>(x, pack2(mu, mu), pack2(-mc, -mc), sum, pk);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 16; k++) pk[k] = 0;
+                            }
+                            if (v.split) {
+                                // row `lane`, 16-byte chunk 4 (wq & 1) + e of its 128 bytes in panel wq >> 1
+                                const uint32_t dst = smem_addr(split_p) + kSplitP * i + 4096 * (wq >> 1) + 128 * lane;
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (((4 * (wq & 1) + e) ^ (lane & 7)) << 4)),
+                                                 "r"(pk[4 * e]), "r"(pk[4 * e + 1]), "r"(pk[4 * e + 2]), "r"(pk[4 * e + 3])
+                                                 : "memory");
+                            } else {
+                                tmem_st16(tP + 16 * q, pk);
+                                if (q == 2) {  // keys 64-127: the tensor core can begin
+                                    tmem_wait_st();
+                                    tc_before();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(&B->p_half[i]);
+                                    __syncwarp();
+                                }
+                            }
+                        }
+                        float a, b;
+                        unpack2(add2(sum[0], sum[1]), a, b);
+                        l += a + b;
+                    }
+                    if (v.split) {
+                        if (j == v.n - 1) {  // before the last weights go: then this memory may be the producer's
+                            xs[256 + 32 * wq + lane] = l;
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&B->quarter[i]);
+                            if (!(ok = tc_wait(&B->quarter[i], hp, A.status, stop))) break;
+                            hp ^= 1;
+                            l = (xs[256 + lane] + xs[288 + lane]) + (xs[320 + lane] + xs[352 + lane]);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    } else if (busy) {
+                        tmem_wait_st();
+                    }
                     tc_before();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&B->p_half[i]);
+                        if (v.split || !busy) mbar_arrive(&B->p_half[i]);
                         mbar_arrive(&B->p_ready[i]);
                     }
                     continue;
@@ -718,77 +784,19 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                     const int lim = seen - (v.first + j * v.step) * kTcBlk;  // keys of the block that the row sees
                     const int all = __reduce_min_sync(0xffffffffu, lim);
                     const bool cut = all < kTcBlk;
-                    // the first keys of the block that the row does not see, and the most of a lane
-                    const int low = kSpans ? from - (v.first + j * v.step) * kTcBlk : 0;
-                    const int low_all = kSpans ? __reduce_max_sync(0xffffffffu, low) : 0;
-                    const bool cut_low = kSpans && low_all > 0;
                     uint32_t lo[64], hi[64];
-                    auto mask_lo = [&] {
-                        if (cut) mask64(lo, lim, all);
-                        if (cut_low) mask64_low(lo, low, low_all);
-                    };
-                    auto mask_hi = [&] {
-                        if (cut) mask64(hi, lim - 64, all - 64);
-                        if (cut_low) mask64_low(hi, low - 64, low_all - 64);
-                    };
-                    float mb;
-                    // the distance of the block's first key; whether keys may stand behind rows
-                    float d0 = 0.f;
-                    bool both = false;
-                    int tier = 0;
-                    if constexpr (kBias) {
-                        const int t0 = (v.first + j * v.step) * kTcBlk;
-                        d0 = (float)(t0 - pos);
-                        both = pre > 0 && __any_sync(0xffffffffu, t0 + kTcBlk - 1 > pos);
-                    }
-                    if constexpr (kX) {
-                        // Of the products, the largest: tanh is monotone, and a distance's term is at most
-                        // bias_most.  That bound of the maximum is at most 63 |sl| above it (96 where it is
-                        // taken, so that weights of 2^-24 of the largest stay normal numbers); steeper
-                        // slopes have their scores worked out for it.
-                        const bool steep = kBias && __any_sync(0xffffffffu, fabsf(sl) > 96.f / 63.f);
-                        float most = 0.f;
-                        auto largest = [&](uint32_t (&x)[64], float d) {
-                            float y = max64(x);
-                            if (y == -INFINITY) return y;
-                            y = kCap ? cap_any(A.sc, c, y) : y * c;
-                            return kBias ? y + bias_most(sl, d) : y;
-                        };
-                        tmem_ld64(tS, lo);
-                        if (kCap) most = absmax64(lo);
-                        mask_lo();
-                        mb = largest(lo, d0);
-                        tmem_ld64(tS + 64, hi);
-                        if (kCap) {
-                            most = fmaxf(most, absmax64(hi));
-                            tier = cap_tier(A.sc, most);
-                        }
-                        mask_hi();
-                        mb = fmaxf(mb, largest(hi, d0 + 64.f));
-                        if (steep) {
-                            scores<SCORE>(lo, A.sc, c, sl, d0, tier, both, 0.f);
-                            mask_lo();
-                            mb = max64(lo);
-                            tmem_ld64(tS + 64, lo);
-                            scores<SCORE>(lo, A.sc, c, sl, d0 + 64.f, tier, both, 0.f);
-                            if (cut) mask64(lo, lim - 64, all - 64);
-                            if (cut_low) mask64_low(lo, low - 64, low_all - 64);
-                            mb = fmaxf(mb, max64(lo));
-                        }
-                    } else {
-                        tmem_ld64(tS, lo);
-                        mask_lo();
-                        mb = max64(lo);
-                        tmem_ld64(tS + 64, hi);
-                        mask_hi();
-                        mb = fmaxf(mb, max64(hi));
-                    }
+                    tmem_ld64(tS, lo);
+                    if (cut) mask_from(lo, lim, all);
+                    float mb = max_of(lo);
+                    tmem_ld64(tS + 64, hi);
+                    if (cut) mask_from(hi, lim - 64, all - 64);
+                    mb = fmaxf(mb, max_of(hi));
                     if (j == 0) {
                         m = mb;
                     } else {
-                        const bool grow = m == -INFINITY ? mb > m : (mb - m) * mu > kTcSlack;
+                        const bool grow = m == -INFINITY ? mb > m : (mb - m) * c > kTcSlack;
                         if (__any_sync(0xffffffffu, grow)) {
-                            const float f = grow ? fast_exp2((m - mb) * mu) : 1.0f;
+                            const float f = grow ? fast_exp2((m - mb) * c) : 1.0f;
                             if (grow) m = mb;
                             l *= f;
 #pragma unroll 1
@@ -801,30 +809,18 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             }
                         }
                     }
-                    const float mc = m == -INFINITY ? 0.f : m * mu;
-                    const uint64_t c2 = pack2(mu, mu), mc2 = pack2(-mc, -mc);
+                    const float mc = m == -INFINITY ? 0.f : m * c;
+                    const uint64_t c2 = pack2(c, c), mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {0, 0};  // two packed pairs of fp32 zeros
-                    if constexpr (kX) {
-                        scores<SCORE>(hi, A.sc, c, sl, d0 + 64.f, tier, both, -mc);
-                        mask_hi();
-                        exps64(hi, sum, tP + 32);
-                    } else {
-                        weights64(hi, c2, mc2, sum, tP + 32);
-                    }
+                    weights64(hi, c2, mc2, sum, tP + 32);
                     tmem_wait_st();  // keys 64-127: the tensor core can begin
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&B->p_half[i]);
                     __syncwarp();
                     tmem_ld64(tS, lo);
-                    if constexpr (kX) {
-                        scores<SCORE>(lo, A.sc, c, sl, d0, tier, both, -mc);
-                        mask_lo();
-                        exps64(lo, sum, tP);
-                    } else {
-                        mask_lo();
-                        weights64(lo, c2, mc2, sum, tP);
-                    }
+                    if (cut) mask_from(lo, lim, all);
+                    weights64(lo, c2, mc2, sum, tP);
                     float a, b;
                     unpack2(add2(sum[0], sum[1]), a, b);
                     l += a + b;
@@ -937,10 +933,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
             if (both && lane == 0) mbar_arrive(&B->x_free);
         }
         if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
-    } else if (kSpans && warp >= 10) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     } else if (warp == 8) {
-        if constexpr (kSpans) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- tensor core
         constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
         const int ksteps = (A.hd + 15) / 16;
@@ -1120,7 +1113,6 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
         }
         __syncwarp();
     } else if (warp == 9) {
-        if constexpr (kSpans) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- TMA producer
         if constexpr (kSpans) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // masked_layout's scratch
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
@@ -1268,7 +1260,7 @@ template <int HDP, bool PAGED, int SCORE> static cudaError_t launch_tc(RowsTcArg
         if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 3, d, vs, b);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(tc_threads(SCORE)), smem, s, t);
+    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(kTcThreads), smem, s, t);
 }
 
 static RowsTcArgs tc_args(const RowsArgs &a, bool spans) {
