@@ -972,18 +972,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 mma_ss(tmem + kO + HDP * i, a + (k >> 2) * (4096 / 16) + (k & 3) * 2, b + k * 128, idO, !(first && k == 0));
         };
         // P_i V for one block of group i; `last`: O_i is complete
-        auto weigh = [&](int i, bool first, bool last, bool split) {
+        auto weigh = [&](int i, bool first, bool last) {
             if (!tc_wait(&B->p_half[i], pph >> i & 1, A.status, stop)) return false;
-            if (kSpans && split) {
-                if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
-                pph ^= 1u << i;
-                tc_after();
-                if (elect_one()) {
-                    issue_split_o(i, first);
-                    if (last) tc_commit(&B->o_full[i]);
-                }
-                return true;
-            }
             tc_after();
             if (elect_one()) issue_o(i, 1, first);
             if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
@@ -991,6 +981,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             tc_after();
             if (elect_one()) {
                 issue_o(i, 0, false);
+                if (last) tc_commit(&B->o_full[i]);
+            }
+            return true;
+        };
+        auto weigh_split = [&](int i, bool first, bool last) {
+            if (!tc_wait(&B->p_half[i], pph >> i & 1, A.status, stop)) return false;
+            if (!tc_wait(&B->p_ready[i], pph >> i & 1, A.status, stop)) return false;
+            pph ^= 1u << i;
+            tc_after();
+            if (elect_one()) {
+                issue_split_o(i, first);
                 if (last) tc_commit(&B->o_full[i]);
             }
             return true;
@@ -1056,7 +1057,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = score(0)) || (n > 1 && !(ok = score(1)))) break;
                 another = w.next(seq, A.nseq, A.geom, ahead);
                 for (int b = 0; b < n; b++) {
-                    if (!(ok = take_v(b == 0 ? head : 0, b == n - 1 ? tail : kTcBlk)) || !(ok = weigh(b & 1, b < 2, b + 2 >= n, v0.split))) break;
+                    if (!(ok = take_v(b == 0 ? head : 0, b == n - 1 ? tail : kTcBlk)) || !(ok = (kSpans && v0.split ? weigh_split(b & 1, b < 2, b + 2 >= n) : weigh(b & 1, b < 2, b + 2 >= n)))) break;
                     drop_v();
                     if (b + 2 < n && !(ok = score(b + 2))) break;
                 }
@@ -1086,7 +1087,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 const bool more = j + 1 < n;
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    if (j < nt[i] && !(ok = weigh(i, j == 0, j == nt[i] - 1, v0.split))) break;
+                    if (j < nt[i] && !(ok = weigh(i, j == 0, j == nt[i] - 1))) break;
                     if (i == 1) drop_v();
                     if (i == 0 && more) {
                         if (!(ok = tc_wait(&B->kv_full[ks], kph, A.status, stop))) break;
@@ -1101,7 +1102,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!ok) break;
                 if (more) drop_k();
             }
-            if (kSpans && ok && v0.split && elect_one()) tc_commit(&B->q_empty[1]);
         }
         // What was issued has run, and its commits have arrived, before the CTA gives up its tensor and
         // shared memory -- in an abandoned call too, whoever gives up and however late.
