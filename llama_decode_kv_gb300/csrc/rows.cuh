@@ -288,11 +288,15 @@ cudaError_t rows_simt_scored_launch(const RowsArgs &a, bool bf16, cudaStream_t s
 
 // Tensor-core attention: bf16, head_dim up to 128; items of two tiles of 128 / G tokens.
 cudaError_t rows_tc_launch(const RowsArgs &a, cudaStream_t s);
-cudaError_t rows_tc_scored_launch_64(const RowsArgs &a, cudaStream_t s);   // head_dim up to 64
-cudaError_t rows_tc_scored_launch_128(const RowsArgs &a, cudaStream_t s);  // from 72 to 128
+// head_dim up to 64, and from 72 to 128; `straight`: the same for long items.
+cudaError_t rows_tc_scored_64(const RowsArgs &a, cudaStream_t s);
+cudaError_t rows_tc_scored_128(const RowsArgs &a, cudaStream_t s);
+cudaError_t rows_tc_scored_straight_64(const RowsArgs &a, cudaStream_t s);
+cudaError_t rows_tc_scored_straight_128(const RowsArgs &a, cudaStream_t s);
 
 // What a kernel does beyond the plain causal scores, as bits of a template argument.
-constexpr int kMasked = 1, kCapped = 2, kBiased = 4;
+// kStraight: how, not what (rows_attention_tc.cuh).
+constexpr int kMasked = 1, kCapped = 2, kBiased = 4, kStraight = 8;
 
 struct AppendArgs {
     const int *row_start, *ctx_len;

@@ -61,7 +61,10 @@
 
 namespace slm {
 
-constexpr int kTcThreads = 320;
+// Threads of a CTA: ten warps; with kStraight twelve (two of them idle), so that the softmax groups can
+// take registers over from the other roles: 2 x 128 x 208 + 128 x 88 = 384 x 168, what such a CTA is
+// launched with.
+__host__ __device__ constexpr int tc_threads(int score) { return score & kStraight ? 384 : 320; }
 constexpr int kTcBlk = 128;                 // positions per block
 constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]
 constexpr int kTcCols = 512;                // tensor memory columns
@@ -345,10 +348,10 @@ __device__ __forceinline__ void scores(uint32_t (&s)[N], const RowsScores &sc, f
         tiers(std::false_type{});
 }
 
-// The most that a distance's term comes to in the 32 keys from d0 (their first position minus the row's) on.
-__device__ __forceinline__ float bias_most(float sl, float d0) {
-    const float a = fabsf(d0), b = fabsf(d0 + 31.f), far = fmaxf(a, b);
-    const float near = d0 > 0.f || d0 < -31.f ? fminf(a, b) : 0.f;
+// The most that a distance's term comes to in the N keys from d0 (their first position minus the row's) on.
+template <int N> __device__ __forceinline__ float bias_most(float sl, float d0) {
+    const float a = fabsf(d0), b = fabsf(d0 + (float)(N - 1)), far = fmaxf(a, b);
+    const float near = d0 > 0.f || d0 < (float)(1 - N) ? fminf(a, b) : 0.f;
     return -sl * (sl > 0.f ? near : far);
 }
 
@@ -363,6 +366,25 @@ __device__ __forceinline__ void weights32(const uint32_t (&s)[32], uint64_t c2, 
         b = fast_exp2(b);
         sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
         pk[k / 2] = pack_bf16x2(a, b);
+    }
+}
+
+// The same of 64 keys, the pairs to tensor memory.
+template <bool DONE>
+__device__ __forceinline__ void straight_weights(const uint32_t (&s)[64], uint64_t c2, uint64_t mc2, uint64_t (&sum)[2], uint32_t addr) {
+#pragma unroll
+    for (int k0 = 0; k0 < 64; k0 += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float a = __uint_as_float(s[k0 + k]), b = __uint_as_float(s[k0 + k + 1]);
+            if (!DONE) unpack2(fma2(pack2(a, b), c2, mc2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, b));
+            pk[k / 2] = pack_bf16x2(a, b);
+        }
+        tmem_st16(addr + k0 / 2, pk);
     }
 }
 
@@ -462,7 +484,7 @@ __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool sp
 // ------------------------------------------------------------------ the kernel
 
 template <int HDP, bool PAGED, int SCORE>
-__global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
+__global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __grid_constant__ RowsTcArgs T) {
     constexpr int NP = HDP / 64;  // 64-column panels of a [128][head_dim] operand
     // Tensor memory columns: S 128 i, O 256 + HDP i.  P (64 columns) has its own where O leaves
     // room, else the upper half of S, which the softmax holds in registers by then.
@@ -474,6 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     // Masked items have blocks of their own, rows see spans; capped or biased scores are worked out in
     // the log2 domain (kX), plain ones stay q . k and take their factor with the exponential.
     constexpr bool kSpans = SCORE != 0, kCap = (SCORE & kCapped) != 0, kBias = (SCORE & kBiased) != 0, kX = kCap || kBias;
+    constexpr bool kLong = (SCORE & kStraight) != 0;
     using Walk = std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk>;
     const RowsArgs &A = T.a;
     extern __shared__ uint8_t smem_raw[];
@@ -531,11 +554,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     Walk w;
     if constexpr (kSpans) {
         RowsStart *start = (RowsStart *)(((uintptr_t)(seq + A.nseq) + 15) & ~(uintptr_t)15);
-        masked_layout(A, seq, wstart, start, (int *)ring, w, tid, kTcThreads);
+        masked_layout(A, seq, wstart, start, (int *)ring, w, tid, tc_threads(SCORE));
         const long long unit = range_units(wstart[A.nseq], A.P);
         w.begin(seq, wstart[A.nseq], A.nseq, A.geom, unit * blockIdx.x, unit * (blockIdx.x + 1), *start);
     } else {
-        rows_layout(A, seq, wstart, tid, kTcThreads);  // ends with a __syncthreads()
+        rows_layout(A, seq, wstart, tid, tc_threads(SCORE));  // ends with a __syncthreads()
     }
     // an item of at most 32 rows is split by keys over the four warps of a group, and worked on twice
     // over whatever its heads' width
@@ -569,6 +592,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
     RowsPiece p;
 
     if (warp < 8) {
+        if constexpr (kLong) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---------------------------------------------------------------- softmax, a thread per row
         const int i = warp >> 2, r = tid & 127;                 // tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -611,7 +635,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 from_any = __reduce_min_sync(0xffffffffu, valid ? from : 0x7fffffff);
                 if (kBias) {
                     pos_any = __reduce_min_sync(0xffffffffu, valid ? pos : 0x7fffffff);
-                    steep = __any_sync(0xffffffffu, fabsf(sl) > 96.f / 31.f);
+                    steep = __any_sync(0xffffffffu, fabsf(sl) > 96.f / 63.f);
                 }
             }
             float m = -INFINITY, l = 0.f;
@@ -636,11 +660,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                 if (!(ok = tc_wait(&B->s_full[i], sp, A.status, stop))) break;
                 sp ^= 1;
                 if constexpr (kSpans) {
-                    // Keys in quarters of 32, by loops whose bodies fit the instruction cache beside the other
-                    // roles': first for the maximum, then, the last quarter first (P of a quarter takes the place
-                    // of keys behind it), for the weights.  In a split item the four warps hold the same 32 rows,
-                    // and each has one quarter: their maxima and, at the end, sums meet in shared memory, and
-                    // their weights, which the tensor core takes from there.
+                    // With kStraight, a block that all of the warp's rows see whole goes through straight code, keys
+                    // 0-63 for the maximum only, keys 64-127 to stay, then 0-63 once more: long items run faster
+                    // by it, short ones slower, whose instructions it pushes out of the cache (rows_scored_tc.cuh
+                    // has the figures).  The others go by quarters of 32 keys,
+                    // in loops whose bodies fit the instruction cache beside the other roles': first for the
+                    // maximum, then, the last quarter first (P of a quarter takes the place of keys behind it), for
+                    // the weights.  In a split item the four warps hold the same 32 rows, and each has one quarter:
+                    // their maxima and, at the end, sums meet in shared memory, and their weights, which the tensor
+                    // core takes from there.
                     const int t0 = (v.first + j * v.step) * kTcBlk;
                     const int qa = v.split ? wq : 0, qb = v.split ? wq : 3;
                     float *xs = split_x + 384 * i;
@@ -653,7 +681,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                     };
                     auto some = [&](int k0) { return seen_any > k0 && from_any < k0 + 32; };
                     const bool both = kBias && pre > 0 && t0 + kTcBlk - 1 > pos_any;
-                    if (busy) {
+                    const bool clear = kLong && busy && !v.split && seen_all >= t0 + kTcBlk && from_all <= t0 && !steep;
+                    // The running maximum after a block's; O and l follow it where it grew by too much.
+                    auto follow = [&](float top) {
+                        if (j == 0) {
+                            m = top;
+                            return;
+                        }
+                        const bool grow = m == -INFINITY ? top > m : (top - m) * mu > kTcSlack;
+                        if (!__any_sync(0xffffffffu, grow)) return;
+                        const float f = grow ? fast_exp2((m - top) * mu) : 1.0f;
+                        if (grow) m = top;
+                        l *= f;
+                        if (v.split && wq > 0) return;
+#pragma unroll 1
+                        for (int d = 0; d < HDP; d += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + d, o);
+#pragma unroll
+                            for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st32(tO + d, o);
+                        }
+                        tmem_wait_st();
+                    };
+                    bool straight = false;  // the block is done
+                    if (kLong && clear) {
+                        tc_after();
+                        __syncwarp();
+                        // The largest score is the largest product's: tanh is monotone, and a distance's term is at
+                        // most bias_most, a bound at most 63 |sl| above (`steep` has no more than 96, so that
+                        // weights of 2^-24 of the largest stay normal numbers).
+                        auto largest = [&](uint32_t (&x)[64], int k0) {
+                            if (kCap) most = fmaxf(most, absmax(x));
+                            float y = max_of(x);
+                            if (kX) y = kCap ? cap_any(A.sc, c, y) : y * c;
+                            if (kBias) y += bias_most<64>(sl, (float)(k0 - pos));
+                            return y;
+                        };
+                        uint32_t lo[64], hi[64];
+                        tmem_ld64(tS, lo);
+                        mb = largest(lo, t0);
+                        tmem_ld64(tS + 64, hi);
+                        mb = fmaxf(mb, largest(hi, t0 + 64));
+                        if (kCap) tier = cap_tier(A.sc, most);
+                        straight = tier == 0 && !both;
+                        if (straight) {
+                            follow(mb);
+                            const float mc = m == -INFINITY ? 0.f : m * mu;
+                            const uint64_t c2 = pack2(mu, mu), mc2 = pack2(-mc, -mc);
+                            uint64_t sum[2] = {0, 0};
+                            if (kX) score_pairs<SCORE, 0, false>(hi, A.sc, c, sl, (float)(t0 + 64 - pos), -mc);
+                            straight_weights<kX>(hi, c2, mc2, sum, tP + 32);
+                            tmem_wait_st();  // keys 64-127: the tensor core can begin
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&B->p_half[i]);
+                            __syncwarp();
+                            tmem_ld64(tS, lo);
+                            if (kX) score_pairs<SCORE, 0, false>(lo, A.sc, c, sl, (float)(t0 - pos), -mc);
+                            straight_weights<kX>(lo, c2, mc2, sum, tP);
+                            float a, b;
+                            unpack2(add2(sum[0], sum[1]), a, b);
+                            l += a + b;
+                        }
+                    } else if (busy) {
                         tc_after();
                         __syncwarp();
 #pragma unroll 1
@@ -670,7 +761,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                             float y = max_of(x);
                             if (kX && y != -INFINITY) {
                                 y = kCap ? cap_any(A.sc, c, y) : y * c;
-                                if (kBias) y += bias_most(sl, (float)(k0 - pos));
+                                if (kBias) y += bias_most<32>(sl, (float)(k0 - pos));
                             }
                             mb = fmaxf(mb, y);
                         }
@@ -695,28 +786,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
                         const float *xr = xs + (j & 1) * 128 + lane;
                         mb = fmaxf(fmaxf(xr[0], xr[32]), fmaxf(xr[64], xr[96]));
                     }
-                    if (busy) {
-                        if (j == 0) {
-                            m = mb;
-                        } else {
-                            const bool grow = m == -INFINITY ? mb > m : (mb - m) * mu > kTcSlack;
-                            if (__any_sync(0xffffffffu, grow)) {
-                                const float f = grow ? fast_exp2((m - mb) * mu) : 1.0f;
-                                if (grow) m = mb;
-                                l *= f;
-                                if (!v.split || wq == 0) {
-#pragma unroll 1
-                                    for (int d = 0; d < HDP; d += 32) {
-                                        uint32_t o[32];
-                                        tmem_ld32(tO + d, o);
-#pragma unroll
-                                        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                        tmem_st32(tO + d, o);
-                                    }
-                                    tmem_wait_st();
-                                }
-                            }
-                        }
+                    if (busy && !straight) {
+                        follow(mb);
                         const float mc = m == -INFINITY ? 0.f : m * mu;
                         uint64_t sum[2] = {0, 0};
 #pragma unroll 1
@@ -933,7 +1004,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
             if (both && lane == 0) mbar_arrive(&B->x_free);
         }
         if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
+    } else if (kLong && warp >= 10) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     } else if (warp == 8) {
+        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- tensor core
         constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
         const int ksteps = (A.hd + 15) / 16;
@@ -1113,6 +1187,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) rows_tc_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp == 9) {
+        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         // ---------------------------------------------------------------- TMA producer
         if constexpr (kSpans) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // masked_layout's scratch
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
@@ -1260,7 +1335,7 @@ template <int HDP, bool PAGED, int SCORE> static cudaError_t launch_tc(RowsTcArg
         if (e == cudaSuccess) e = make_bf16_map_nd(&t.v, a.kv.v, 3, d, vs, b);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(kTcThreads), smem, s, t);
+    return launch_pdl(rows_tc_kernel<HDP, PAGED, SCORE>, dim3(a.P), dim3(tc_threads(SCORE)), smem, s, t);
 }
 
 static RowsTcArgs tc_args(const RowsArgs &a, bool spans) {

@@ -241,13 +241,22 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
         a.q_ld = a.out_ld = (long long)a.H * a.hd;
         a.kv.k_ld = a.kv.v_ld = (long long)a.KV * a.hd;
     }
+    // Items of many blocks, as far as the sizes tell (a window and the table, or the average prompt;
+    // documents, and items of one split tile, are short).  Straight / looped, us, 32 / 8 heads of 128, cap
+    // 30: a prompt of 8,192 588 / 818, of 2,048 73 / 78, 16 of 512 117 / 101, 64 of 128 72 / 55; chunks of
+    // up to 512 over 16,000 positions with a window of 4,096 113 / 129; documents of up to 1,500 in
+    // prompts of up to 6,000 220 / 202; a step of 64 sequences, window 4,096, 172 / 163.
+    const long long reach = std::min(longest, a.kv.table ? longest : (long long)a.rows / a.nseq);
+    const bool long_items = sc && reach >= 2048 && !sc->first && (long long)a.rows * a.G > 32LL * a.nseq;
     cudaError_t e;
     if (!sc)
         e = on_tensor_cores(dtype, a.hd) ? rows_tc_launch(a, s) : rows_simt_launch(a, bf16, s);
-    else if (on_tensor_cores(dtype, a.hd))
-        e = a.hd <= 64 ? rows_tc_scored_launch_64(a, s) : rows_tc_scored_launch_128(a, s);
-    else
+    else if (!on_tensor_cores(dtype, a.hd))
         e = rows_simt_scored_launch(a, bf16, s);
+    else if (long_items)
+        e = a.hd <= 64 ? rows_tc_scored_straight_64(a, s) : rows_tc_scored_straight_128(a, s);
+    else
+        e = a.hd <= 64 ? rows_tc_scored_64(a, s) : rows_tc_scored_128(a, s);
     if (e == cudaSuccess && a.geom.split) e = rows_join_launch(a, bf16, s);
     if (e != cudaSuccess) return launch_fail("attention", e);
     return SLM_OK;

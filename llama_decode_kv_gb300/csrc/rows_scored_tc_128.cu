@@ -1,18 +1,8 @@
-// rows_scored_tc_128.cu -- the tensor-core attention of packed rows (rows_attention_tc.cuh) for scored
-// rows with heads of 72 to 128.
-#include "rows_attention_tc.cuh"
+// rows_scored_tc_128.cu -- scored rows on the tensor cores, heads of 72 to 128.
+#include "rows_scored_tc.cuh"
 
 namespace slm {
 
-template <bool PAGED> static cudaError_t launch(RowsTcArgs &t, cudaStream_t s) {
-    const bool cap = t.a.sc.cap_log2 > 0.f;
-    if (t.a.sc.slopes) return cap ? launch_tc<128, PAGED, kMasked | kCapped | kBiased>(t, s) : launch_tc<128, PAGED, kMasked | kBiased>(t, s);
-    return cap ? launch_tc<128, PAGED, kMasked | kCapped>(t, s) : launch_tc<128, PAGED, kMasked>(t, s);
-}
-
-cudaError_t rows_tc_scored_launch_128(const RowsArgs &a, cudaStream_t s) {
-    RowsTcArgs t = tc_args(a, true);
-    return a.kv.table ? launch<true>(t, s) : launch<false>(t, s);
-}
+cudaError_t rows_tc_scored_128(const RowsArgs &a, cudaStream_t s) { return scored<128, 0>(a, s); }
 
 }  // namespace slm

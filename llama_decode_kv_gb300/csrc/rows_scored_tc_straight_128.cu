@@ -1,0 +1,8 @@
+// rows_scored_tc_straight_128.cu -- scored rows on the tensor cores, heads of 72 to 128, long items.
+#include "rows_scored_tc.cuh"
+
+namespace slm {
+
+cudaError_t rows_tc_scored_straight_128(const RowsArgs &a, cudaStream_t s) { return scored<128, kStraight>(a, s); }
+
+}  // namespace slm
