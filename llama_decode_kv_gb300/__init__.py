@@ -221,6 +221,13 @@ def _ints(x, name: str, *shape):
     return x.data_ptr()
 
 
+def _list(x, name: str, n: int):
+    """_ints of one dimension."""
+    if x.dtype is not _INT or x.numel() != n or x.dim() != 1 or not x.is_contiguous():
+        raise ValueError(f"{name}: {tuple(x.shape)} {x.dtype}, expected contiguous int32 ({n},)")
+    return x.data_ptr()
+
+
 def _cache(k_cache, v_cache, page_table, kv: int, hd: int, what: str) -> bytes:
     """The slm_kv_cache of a cache of kv heads (0: any number) of hd."""
     shape, dt = k_cache.shape, k_cache.dtype
@@ -294,7 +301,8 @@ def kv_append_axes(k, v, k_cache, v_cache, page_table, row_start, ctx_len, statu
                    q_out=None, stream=None) -> None:
     """slm_kv_append_axes over torch tensors of the current device: kv_append whose pair j of a row
     turns by rope[positions[axis_of_pair[j]][row]][j].  positions: int32 [axes][rows], rows of it at
-    any stride; axis_of_pair: head_dim / 2 whole numbers, -1 for a pair that is not turned.
+    any stride; axis_of_pair: head_dim / 2 whole numbers, -1 for a pair that is not turned
+    (or them as bytes, two's complement).
     Raises SlmError / ValueError."""
     if rope is None:
         raise ValueError("rope is needed")
@@ -304,10 +312,13 @@ def kv_append_axes(k, v, k_cache, v_cache, page_table, row_start, ctx_len, statu
     if positions.dtype is not _INT or rows != k.shape[0] or (one != 1 and rows > 1):
         raise ValueError(f"positions: {tuple(positions.shape)} {positions.dtype} (strides {positions.stride()}), expected int32 "
                          f"[axes][{k.shape[0]}], adjacent in a row")
+    half = k.shape[2] // 2
     try:
-        pairs = struct.pack(f"{k.shape[2] // 2}b", *axis_of_pair)
+        pairs = axis_of_pair if type(axis_of_pair) is bytes else struct.pack("%db" % half, *axis_of_pair)
+        if len(pairs) != half:
+            raise struct.error(f"{len(pairs)} given")
     except struct.error as e:
-        raise ValueError(f"axis_of_pair: {k.shape[2] // 2} axes expected ({e})") from None
+        raise ValueError(f"axis_of_pair: {half} axes expected ({e})") from None
     rc = slm_kv_append_axes(*a, axes, pairs, positions.data_ptr(), ld if axes > 1 else rows, *b, _ints(status, "status", 1),
                             _rows_stream(stream, k))
     if rc:
@@ -329,12 +340,12 @@ def rows_plan(new_len, seq_len, page_table, page_size, free_pages, free_count, r
     if slots.dtype is not _I64T or slots.shape != (rows,) or not slots.is_contiguous():
         raise ValueError(f"slots: {tuple(slots.shape)} {slots.dtype}, expected contiguous int64 ({rows},)")
     n_pages = free_pages.shape[0]
-    pool = _PACK_POOL(_ints(page_table, "page_table", nseq, ld), _ints(free_pages, "free_pages", n_pages),
-                      _ints(free_count, "free_count", 1), _ints(seq_len, "seq_len", nseq), nseq, ld, n_pages, page_size)
-    rc = slm_rows_plan(pool, _ints(new_len, "new_len", nseq), rows, _ints(row_start, "row_start", nseq + 1),
-                       _ints(ctx_len, "ctx_len", nseq), _ints(positions, "positions", rows), slots.data_ptr(),
-                       _ints(seq_len_out, "seq_len_out", nseq), _ints(free_count_out, "free_count_out", 1),
-                       _ints(status, "status", 1), _rows_stream(stream, new_len))
+    pool = _PACK_POOL(_ints(page_table, "page_table", nseq, ld), _list(free_pages, "free_pages", n_pages),
+                      _list(free_count, "free_count", 1), _list(seq_len, "seq_len", nseq), nseq, ld, n_pages, page_size)
+    rc = slm_rows_plan(pool, _list(new_len, "new_len", nseq), rows, _list(row_start, "row_start", nseq + 1),
+                       _list(ctx_len, "ctx_len", nseq), _list(positions, "positions", rows), slots.data_ptr(),
+                       _list(seq_len_out, "seq_len_out", nseq), _list(free_count_out, "free_count_out", 1),
+                       _list(status, "status", 1), _rows_stream(stream, new_len))
     if rc:
         raise SlmError(rc, "slm_rows_plan", slm_last_error(None).decode())
 
@@ -345,8 +356,11 @@ def attention_rows_workspace_bytes(dtype, rows: int, nseq: int, n_heads: int, n_
     return int(slm_attention_rows_workspace_bytes(_dtype_code(dtype), rows, nseq, n_heads, n_kv_heads, head_dim))
 
 
-def _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream):
-    """(cache, rows), what follows them in a paged attention call, and the sequences."""
+def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream=None) -> None:
+    """slm_attention_paged over torch tensors of the current device: out[row][h] = attention of
+    the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
+    already holds the rows' own keys and values).  workspace: uint8 tensor of
+    attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
     shape, dt = q.shape, k_cache.dtype
     rows, heads, hd = shape
     nseq = page_table.shape[0]
@@ -356,40 +370,8 @@ def _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, worksp
     r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
                    0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
     q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
-    return (c, r), (heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace), _ints(status, "status", 1),
-                    _rows_stream(stream, q)), nseq
-
-
-def _prompt_args(q, k, v, row_start, out, workspace, status, stream):
-    """rows, what follows them in a prompt attention call, and the sequences."""
-    shape, ks, dt = q.shape, k.shape, q.dtype
-    rows, heads, hd = shape
-    if ks[0] != rows or ks[2] != hd:
-        raise ValueError(f"k: {tuple(ks)}, expected ({rows}, kv heads, {hd})")
-    code, nseq = _dtype_code(dt), row_start.shape[0] - 1
-    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1), 0, nseq, rows)
-    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
-    k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
-    return r, (code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(), o_ld,
-               *_workspace(workspace), _ints(status, "status", 1), _rows_stream(stream, q)), nseq
-
-
-def _scores(scale, cap, slopes, window, prefix_len, first, rows: int, heads: int, nseq: int) -> bytes:
-    """The slm_scores of a call."""
-    if slopes is not None and (slopes.dtype is not _F32 or slopes.shape != (heads,) or not slopes.is_contiguous()):
-        raise ValueError(f"slopes: {tuple(slopes.shape)} {slopes.dtype}, expected contiguous float32 ({heads},)")
-    return _PACK_SCORES(scale, cap, 0 if slopes is None else slopes.data_ptr(),
-                        0 if prefix_len is None else _ints(prefix_len, "prefix_len", nseq),
-                        0 if first is None else _ints(first, "first", rows), window)
-
-
-def attention_paged(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream=None) -> None:
-    """slm_attention_paged over torch tensors of the current device: out[row][h] = attention of
-    the packed rows q [rows][heads][head_dim] over positions 0..p of the paged cache (which
-    already holds the rows' own keys and values).  workspace: uint8 tensor of
-    attention_rows_workspace_bytes bytes.  Raises SlmError / ValueError."""
-    a, b, _ = _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream)
-    rc = slm_attention_paged(*a, *b)
+    rc = slm_attention_paged(c, r, heads, q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace),
+                             _ints(status, "status", 1), _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_paged", slm_last_error(None).decode())
 
@@ -398,31 +380,70 @@ def attention_prompt(q, k, v, row_start, out, workspace, status, stream=None) ->
     """slm_attention_prompt over torch tensors of the current device: causal attention of the
     packed prompts q [rows][heads][head_dim], k, v [rows][kv heads][head_dim] into out.
     Raises SlmError / ValueError."""
-    r, b, _ = _prompt_args(q, k, v, row_start, out, workspace, status, stream)
-    rc = slm_attention_prompt(r, *b)
+    shape, ks, dt = q.shape, k.shape, q.dtype
+    rows, heads, hd = shape
+    if ks[0] != rows or ks[2] != hd:
+        raise ValueError(f"k: {tuple(ks)}, expected ({rows}, kv heads, {hd})")
+    code, nseq = _dtype_code(dt), row_start.shape[0] - 1
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1), 0, nseq, rows)
+    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
+    k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
+    rc = slm_attention_prompt(r, code, heads, ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+                              out.data_ptr(), o_ld, *_workspace(workspace), _ints(status, "status", 1),
+                              _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_prompt", slm_last_error(None).decode())
 
 
-def attention_paged_scored(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, *, scale=0.0,
+def _scores(scale, cap, slopes, window, prefix_len, first, rows: int, heads: int, nseq: int) -> bytes:
+    """The slm_scores of a call."""
+    sl = 0
+    if slopes is not None:
+        if slopes.dtype is not _F32 or slopes.shape != (heads,) or not slopes.is_contiguous():
+            raise ValueError(f"slopes: {tuple(slopes.shape)} {slopes.dtype}, expected contiguous float32 ({heads},)")
+        sl = slopes.data_ptr()
+    return _PACK_SCORES(scale, cap, sl, 0 if prefix_len is None else _ints(prefix_len, "prefix_len", nseq),
+                        0 if first is None else _ints(first, "first", rows), window)
+
+
+def attention_paged_scored(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, scale=0.0,
                            cap=0.0, slopes=None, window=0, prefix_len=None, first=None, stream=None) -> None:
     """slm_attention_paged_scored over torch tensors of the current device: attention_paged with
     scores cap tanh(scale q.k / cap) - slopes[h] |p - t| over the positions from max(first[row],
     p + 1 - window) on, up to p or prefix_len[s] - 1, whichever is later (scale 0: 1 / sqrt(head_dim);
     cap 0, window 0, None: without).  slopes: float32 [heads]; prefix_len: int32 [sequences]; first:
     int32 [rows].  Rows that see nothing get zeros.  Raises SlmError / ValueError."""
-    a, b, nseq = _paged_args(q, k_cache, v_cache, page_table, row_start, ctx_len, out, workspace, status, stream)
-    rc = slm_attention_paged_scored(*a, _scores(scale, cap, slopes, window, prefix_len, first, q.shape[0], b[0], nseq), *b)
+    shape, dt = q.shape, k_cache.dtype
+    rows, heads, hd = shape
+    nseq = page_table.shape[0]
+    if _INT is None:
+        _torch_names()
+    c = _cache(k_cache, v_cache, page_table, 0, hd, "q")
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1),
+                   0 if ctx_len is None else _ints(ctx_len, "ctx_len", nseq), nseq, rows)
+    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
+    rc = slm_attention_paged_scored(c, r, _scores(scale, cap, slopes, window, prefix_len, first, rows, heads, nseq), heads,
+                                    q.data_ptr(), q_ld, out.data_ptr(), o_ld, *_workspace(workspace),
+                                    _ints(status, "status", 1), _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_paged_scored", slm_last_error(None).decode())
 
 
-def attention_prompt_scored(q, k, v, row_start, out, workspace, status, *, scale=0.0, cap=0.0, slopes=None, window=0,
+def attention_prompt_scored(q, k, v, row_start, out, workspace, status, scale=0.0, cap=0.0, slopes=None, window=0,
                             prefix_len=None, first=None, stream=None) -> None:
     """slm_attention_prompt_scored over torch tensors of the current device: attention_prompt with
     the scores and masks of attention_paged_scored.  Raises SlmError / ValueError."""
-    r, b, nseq = _prompt_args(q, k, v, row_start, out, workspace, status, stream)
-    rc = slm_attention_prompt_scored(r, _scores(scale, cap, slopes, window, prefix_len, first, q.shape[0], b[1], nseq), *b)
+    shape, ks, dt = q.shape, k.shape, q.dtype
+    rows, heads, hd = shape
+    if ks[0] != rows or ks[2] != hd:
+        raise ValueError(f"k: {tuple(ks)}, expected ({rows}, kv heads, {hd})")
+    code, nseq = _dtype_code(dt), row_start.shape[0] - 1
+    r = _PACK_ROWS(_ints(row_start, "row_start", nseq + 1), 0, nseq, rows)
+    q_ld, o_ld = _heads(q, "q", shape, dt), _heads(out, "out", shape, dt)
+    k_ld, v_ld = _heads(k, "k", ks, dt), _heads(v, "v", ks, dt)
+    rc = slm_attention_prompt_scored(r, _scores(scale, cap, slopes, window, prefix_len, first, rows, heads, nseq), code, heads,
+                                     ks[1], hd, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld, out.data_ptr(),
+                                     o_ld, *_workspace(workspace), _ints(status, "status", 1), _rows_stream(stream, q))
     if rc:
         raise SlmError(rc, "slm_attention_prompt_scored", slm_last_error(None).decode())
 

@@ -97,7 +97,7 @@ def check(b, out, keys, values, m, kw, dtype):
             X, B = x.abs().masked_fill(hd, 0).amax(-1, keepdim=True), 0.0
             if m.get("slopes"):
                 bias = kw["slopes"][h].double() * (p - t).abs()[~blind]
-                B = bias.masked_fill(hd, 0).amax(-1, keepdim=True)
+                B = bias.abs().masked_fill(hd, 0).amax(-1, keepdim=True)
                 x = x - bias
             w = torch.softmax(x.masked_fill(hd, -math.inf), dim=-1)
             want, mean = w @ vv, w @ vv.abs()
@@ -191,6 +191,42 @@ def test_prompt(slm, dtype, H, KV, hd, name):  # noqa: F811
     keys = [b.k[a:a + n] for a, n in zip(b.starts, new)]
     values = [b.v[a:a + n] for a, n in zip(b.starts, new)]
     check(b, out, keys, values, m, kw, dtype)
+
+
+@pytest.mark.parametrize("name", MASKS)
+@pytest.mark.parametrize("H,KV,hd", [(9, 3, 64), (32, 8, 128), (64, 1, 64), (12, 4, 80)])
+def test_wide_table(slm, H, KV, hd, name):  # noqa: F811
+    """A table for many more positions than there are: the code for long items, and divided ones."""
+    b = Batch(BF16, H, KV, hd, *CHUNKS, 16, seed=hd + H, lead=2, pad=3)
+    b.page_table = torch.cat([b.page_table, torch.full((len(b.new), 200), -1, dtype=torch.int32, device="cuda")], 1)
+    m = masks(b, name)
+    out, keys, values, kw = paged(slm, b, m)
+    check(b, out, keys, values, m, kw, BF16)
+
+
+@pytest.mark.parametrize("name", ["plain", "cap", "small_cap", "slopes", "window", "prefix", "all_prefix"])
+@pytest.mark.parametrize("H,KV,hd", [(4, 2, 64), (8, 2, 128)])
+def test_long_prompt(slm, H, KV, hd, name):  # noqa: F811
+    new = [2600, 1700]
+    b = Batch(BF16, H, KV, hd, new, seed=hd, pad=5)
+    m = masks(b, name)
+    kw, out = arguments(b, m), b.out()
+    slm.attention_prompt_scored(b.q, b.k, b.v, b.row_start, out, b.workspace(slm), b.status, **kw)
+    check(b, out, [b.k[:2600], b.k[2600:4300]], [b.v[:2600], b.v[2600:4300]], m, kw, BF16)
+
+
+@pytest.mark.parametrize("slope", [-0.3, 1.2, 40.0, -3.0])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_steep_and_negative_slopes(slm, hd, slope):  # noqa: F811
+    """Distances that outweigh the products, or draw a row to its farthest positions."""
+    for new, ctx in (([70, 1], [300, 900]), ([1, 1], [5000, 130])):
+        b = Batch(BF16, 4, 2, hd, new, ctx, 16, seed=6)
+        m = dict(slopes=True)
+        b.fill([n + c for n, c in zip(b.new, b.ctx)])
+        kw, out = dict(slopes=torch.tensor([slope, 0.0, slope / 7, slope], device="cuda")), b.out()
+        slm.attention_paged_scored(b.q, b.k_cache, b.v_cache, b.page_table, b.row_start, b.ctx_len, out, b.workspace(slm),
+                                   b.status, **kw)
+        check(b, out, b.seq_k, b.seq_v, m, kw, BF16)
 
 
 @pytest.mark.parametrize("page", [16, 64, 256])
