@@ -222,16 +222,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Keys from `lim` on become -infinity.  `all` (at most any lane's lim): no lane's key before it does,
-// so groups of 16 below it are left alone (two instructions an element at half rate: a diagonal
+// Keys from `lim` on become -infinity (or `hidden`).  `all` (at most any lane's lim): no lane's key before
+// it does, so groups of 16 below it are left alone (two instructions an element at half rate: a diagonal
 // block took twice as long as the others).
-template <int N> __device__ __forceinline__ void mask_from(uint32_t (&s)[N], int lim, int all) {
+constexpr uint32_t kHidden = 0xff800000u, kIgnored = 0x7fffffffu;  // -infinity; a NaN, which a maximum passes over
+template <int N> __device__ __forceinline__ void mask_from(uint32_t (&s)[N], int lim, int all, uint32_t hidden = kHidden) {
 #pragma unroll
     for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 + 16 > all) {
 #pragma unroll
             for (int k = k0; k < k0 + 16; k++)
-                if (k >= lim) s[k] = 0xff800000u;
+                if (k >= lim) s[k] = hidden;
         }
 }
 
@@ -244,14 +245,14 @@ template <int N> __device__ __forceinline__ float max_of(const uint32_t (&s)[N])
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// Keys before `low` become -infinity.  `all`: at least any lane's low.
-template <int N> __device__ __forceinline__ void mask_to(uint32_t (&s)[N], int low, int all) {
+// Keys before `low` do.  `all`: at least any lane's low.
+template <int N> __device__ __forceinline__ void mask_to(uint32_t (&s)[N], int low, int all, uint32_t hidden = kHidden) {
 #pragma unroll
     for (int k0 = 0; k0 < N; k0 += 16)
         if (k0 < all) {
 #pragma unroll
             for (int k = k0; k < k0 + 16; k++)
-                if (k < low) s[k] = 0xff800000u;
+                if (k < low) s[k] = hidden;
         }
 }
 
@@ -275,7 +276,9 @@ __device__ __forceinline__ float tanh_large(float y) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return copysignf(fmaf(-2.0f, r, 1.0f), y);
 }
-// 0: every |s| of the warp is below half the cap (in its units), 1: below it, 2: some are above.
+// 0: every |s| of the warp is below half the cap (in its units), 1: below it, 2: some are above.  `most`
+// counts products of the batch's rows with keys that they see and no others: what lies behind a
+// sequence's last key or row differs from call to call, and the bits of a call must not.
 __device__ __forceinline__ int cap_tier(const RowsScores &sc, float most) {
     return __all_sync(0xffffffffu, most <= sc.half_cap) ? 0 : __all_sync(0xffffffffu, most <= sc.one_cap) ? 1 : 2;
 }
@@ -675,9 +678,9 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                     float mb = -INFINITY, most = 0.f;
                     int tier = 0;
                     // keys [lo, hi) of the quarter are those that the row sees; `some`: any row of the warp does
-                    auto mask = [&](uint32_t (&x)[32], int k0) {
-                        if (seen_all < k0 + 32) mask_from(x, seen - k0, seen_all - k0);
-                        if (from_all > k0) mask_to(x, from - k0, from_all - k0);
+                    auto mask = [&](uint32_t (&x)[32], int k0, uint32_t hidden) {
+                        if (seen_all < k0 + 32) mask_from(x, seen - k0, seen_all - k0, hidden);
+                        if (from_all > k0) mask_to(x, from - k0, from_all - k0, hidden);
                     };
                     auto some = [&](int k0) { return seen_any > k0 && from_any < k0 + 32; };
                     const bool both = kBias && pre > 0 && t0 + kTcBlk - 1 > pos_any;
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                         mb = largest(lo, t0);
                         tmem_ld64(tS + 64, hi);
                         mb = fmaxf(mb, largest(hi, t0 + 64));
-                        if (kCap) tier = cap_tier(A.sc, most);
+                        if (kCap) tier = cap_tier(A.sc, valid ? most : 0.f);
                         straight = tier == 0 && !both;
                         if (straight) {
                             follow(mb);
@@ -753,8 +756,8 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             if (!some(k0)) continue;
                             uint32_t x[32];
                             tmem_ld32(tS + 32 * q, x);
+                            mask(x, k0, kIgnored);
                             if (kCap) most = fmaxf(most, absmax(x));
-                            mask(x, k0);
                             // Of the products, the largest: tanh is monotone, and a distance's term is at most
                             // bias_most.  That bound of the maximum is at most 31 |sl| above it (96 where it is
                             // taken, so that weights of 2^-24 of the largest stay normal numbers).
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             }
                             mb = fmaxf(mb, y);
                         }
-                        if (kCap) tier = cap_tier(A.sc, most);
+                        if (kCap) tier = cap_tier(A.sc, valid ? most : 0.f);
                         if (kBias && steep) {  // key by key
                             mb = -INFINITY;
 #pragma unroll 1
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             if (some(k0)) {
                                 tmem_ld32(tS + 32 * q, x);
                                 if (kX) scores<SCORE>(x, A.sc, c, sl, (float)(k0 - pos), tier, both, -mc);
-                                mask(x, k0);
+                                mask(x, k0, kHidden);
                                 weights32<kX>(x, pack2(mu, mu), pack2(-mc, -mc), sum, pk);
                             } else {
 #pragma unroll
