@@ -14,6 +14,10 @@
 // the keys of a block instead of multiplying rows that do not exist.  Seven prompts of up to 701
 // tokens, 9 / 3 heads of 64: 76 us = 18 TFLOP/s of useful work, 30% of the FMA pipe's issue slots (a
 // CTA has five blocks, and half of a diagonal block is masked).
+//
+// Scored rows are the same kernels with SCORED: a row's span (row_span) in place of [0, p], and simt_score
+// on every product.  The prefixes make blocks above the diagonal count, which is why seven prompts
+// of up to 700 tokens with prefixes and slopes take 141 us for twice the pairs.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -24,6 +24,29 @@
 // Heads of 72 to 112 run as 128-wide ones in P V and in shared memory (their S leaves the missing
 // columns out), so up to 44% of their P V and of their ring is padding.
 //
+// Scored rows (SCORE):  x_t = scale q . k_t,  cap tanh(x_t / cap),  - slope_h |p - t|,  over the t that
+// the row sees, [from, to) by row_span (window, document, prefix); a row that sees none is 0.  An item
+// walks the blocks that some row of it sees (MaskedWalk), and its softmax groups mask where a block
+// holds a key that some row of the warp does not see.  What is different from plain rows, and why:
+//   * Both heads' widths work on one-tile items twice over, and items of up to 32 rows (a decode
+//     step) are split: their queries stand in the tile four times, 32 rows for each warp of a group, so
+//     the four warps take 32 of a block's keys each in place of one warp all 128.  With one warp at work
+//     a capped block cost more than its bytes took to come (64 sequences, 32 / 8 heads of 128, window
+//     4,096, cap 30: 334 us; split 182, with quarters in loops 163 = 5.8 TB/s, 86% of the copy rate).
+//   * A quarter of 32 keys is the body of a loop.  The scored softmax as straight code pushes the other
+//     roles' instructions out of the cache (no_instruction was the first stall by far), and these
+//     then feed the tensor core late: documents of up to 1,500 in prompts of up to 6,000, 250 us as
+//     straight code, 196 in quarters.  Long items get over it, so they have a variant with straight code
+//     for blocks without masks (kStraight; the rule and its figures stand in rows_op.cu).
+//   * tanh is a polynomial while |x| is at most the cap, its degree by the warp's largest |x|
+//     (cap_tier), the branch outside the loops: inside, the compiler computes both sides for every key
+//     (64 sequences as above 992 us, outside 334).
+//   * The maximum is the score of the largest product plus a bound of the distance's term, so that one
+//     pass over a quarter finds it; slopes too steep for that take it key by key.
+// What bounds them now: decode steps HBM; prompts and chunks with masks the same chain of hand-offs as
+// plain rows, its softmax part longer by the cap's five to seven instructions for two keys (a prompt of
+// 8,192: 588 us with a cap, 430 without, plain 356), and items' ends where documents are short.
+//
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
 //                   causal mask where the block needs one, the running maximum, P = 2^(S - m) as
 //                   bf16 back into tensor memory, the sum in fp32; at the end O / l to global
@@ -665,9 +688,8 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                 if constexpr (kSpans) {
                     // With kStraight, a block that all of the warp's rows see whole goes through straight code, keys
                     // 0-63 for the maximum only, keys 64-127 to stay, then 0-63 once more: long items run faster
-                    // by it, short ones slower, whose instructions it pushes out of the cache (rows_scored_tc.cuh
-                    // has the figures).  The others go by quarters of 32 keys,
-                    // in loops whose bodies fit the instruction cache beside the other roles': first for the
+                    // by it, short ones slower, whose instructions it pushes out of the cache (rows_op.cu has
+                    // the figures).  The others go by quarters of 32 keys, in loops whose bodies fit the instruction cache beside the other roles': first for the
                     // maximum, then, the last quarter first (P of a quarter takes the place of keys behind it), for
                     // the weights.  In a split item the four warps hold the same 32 rows, and each has one quarter:
                     // their maxima and, at the end, sums meet in shared memory, and their weights, which the tensor

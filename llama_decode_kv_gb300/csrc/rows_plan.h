@@ -11,6 +11,10 @@
 // lengths are, and an item that a cut divides is joined afterwards from the partial states of
 // its pieces.  Where every item is short (split = 0), a CTA takes the items that begin in its
 // range whole, and nothing has to be joined.
+//
+// With masks (MaskedWalk) an item walks only the blocks [b0, b1) that some token of it sees (item_span),
+// and counts those; the units of a sequence are added up item by item (masked_layout in rows.cuh), as no
+// formula holds for documents.
 #pragma once
 
 #include <math.h>
