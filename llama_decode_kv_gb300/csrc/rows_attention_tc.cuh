@@ -1219,33 +1219,33 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
         uint32_t qn[2] = {0, 0};              // query tiles loaded so far
         bool ok = true;
         const int shift = A.kv.page_shift, box = T.box;
-        const int per = kTcBlk / box;         // boxes of a block
+        const int bshift = 31 - __clz(box);   // a box is the power of two that a page is, or a block
+        const int per = kTcBlk >> bshift;     // boxes of a block
         while (ok && w.next(seq, A.nseq, A.geom, p)) {
             const SeqRows sr = seq[p.s];
             const int L = item_to(sr, p), from = item_from(sr, p), pre = prefix_of(p.s);
-            // the page (lane: box) of a block; a bad id becomes page 0
+            // the page (lane: box) of a block, read a block ahead and not looked at before it is used
             auto page_of = [&](int kb) {
-                const int pos = kb * kTcBlk + lane * box;
-                if (!PAGED || lane >= per || pos >= L || kb >= p.kb1 || (kSpans && pos + box <= from)) return -1;
-                int pg = __ldg(A.kv.table + (size_t)p.s * A.kv.table_ld + (pos >> shift));
-                if (pg < 0 || pg >= A.kv.n_pages) {
-                    atomicOr(A.status, SLM_ROWS_PAGE);
-                    pg = 0;
-                }
-                return pg;
+                const int pos = kb * kTcBlk + (lane << bshift);
+                if (!PAGED || lane >= per || pos >= L || kb >= p.kb1 || (kSpans && pos + box <= from)) return 0;
+                return __ldg(A.kv.table + (size_t)p.s * A.kv.table_ld + (pos >> shift));
             };
             int page = page_of(p.kb0);
             for (int kb = p.kb0; kb < p.kb1 && ok; kb++) {
                 const int after = page_of(kb + 1);
                 const int pos0 = kb * kTcBlk;
-                const int nbox = PAGED ? min(per, (L - pos0 + box - 1) / box) : 1;
-                const int box0 = kSpans && PAGED ? max(0, (from - pos0) / box) : 0;  // boxes that no row sees a position of
+                const int nbox = PAGED ? min(per, (L - pos0 + box - 1) >> bshift) : 1;
+                const int box0 = kSpans && PAGED ? max(0, from - pos0) >> bshift : 0;  // boxes that no row sees a position of
+                if (PAGED && lane < nbox && lane >= box0 && (page < 0 || page >= A.kv.n_pages)) {  // becomes page 0
+                    atomicOr(A.status, SLM_ROWS_PAGE);
+                    page = 0;
+                }
                 for (int is_v = 0; is_v < 2; is_v++) {
                     if (issued >= (uint32_t)T.stages && !(ok = tc_wait(&B->kv_empty[st], ph ^ 1, A.status, stop))) break;
                     uint64_t *bar = &B->kv_full[st];
                     uint8_t *dst = ring + (size_t)st * NP * kPanel;
                     const CUtensorMap *map = is_v ? &T.v : &T.k;
-                    if (lane == 0) mbar_expect_tx(bar, (uint32_t)((nbox - box0) * box * 128 * NP));
+                    if (lane == 0) mbar_expect_tx(bar, (uint32_t)((nbox - box0) << bshift) * (128 * NP));
                     __syncwarp();
                     if (lane < nbox && lane >= box0)
 #pragma unroll

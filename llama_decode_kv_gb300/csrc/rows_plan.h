@@ -232,7 +232,7 @@ SLM_HD int piece_slot(int cta, const RowsPiece &p) { return 2 * cta + (p.begins(
 // hi = max(p + 1, prefix).  first does not descend within a sequence, so an item's span begins at
 // its first row's lo and ends at its last row's hi, and has blocks [b0, b0 + nb) of its own (none
 // where the span is empty: such an item still counts its `cost` units, and writes its rows).  There
-// is no closed form for their sum: the units of all items are added up one by one (masked_start).
+// is no closed form for their sum: the units of all items are added up one by one (masked_layout in rows.cuh).
 
 // The mask of one sequence: its first packed row's entry of `first` (null: none), its prefix cut to
 // [0, ctx + n], the window (0: none).
