@@ -91,6 +91,7 @@ __host__ __device__ constexpr int tc_threads(int score) { return score & kStraig
 constexpr int kTcBlk = 128;                 // positions per block
 constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]
 constexpr int kTcCols = 512;                // tensor memory columns
+constexpr float kNear = 40.0f;              // log2 scores this near 0 take a bound for their maximum
 constexpr float kTcSlack = 8.0f;            // log2 growth of a maximum that O is not rescaled for
 
 struct RowsTcArgs {
@@ -522,6 +523,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     // Masked items have blocks of their own, rows see spans; capped or biased scores are worked out in
     // the log2 domain (kX), plain ones stay q . k and take their factor with the exponential.
     constexpr bool kSpans = SCORE != 0, kCap = (SCORE & kCapped) != 0, kBias = (SCORE & kBiased) != 0, kX = kCap || kBias;
+    constexpr bool kAbs = kCap && !kBias;  // the largest |product| may stand for the maximum
     constexpr bool kLong = (SCORE & kStraight) != 0;
     using Walk = std::conditional_t<kSpans, RowsMaskedWalk, RowsWalk>;
     const RowsArgs &A = T.a;
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     RowsPiece p;
 
     if (warp < 8) {
-        if constexpr (kLong) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if constexpr (kLong) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---------------------------------------------------------------- softmax, a thread per row
         const int i = warp >> 2, r = tid & 127;                 // tile, row
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -729,7 +731,16 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                         }
                         tmem_wait_st();
                     };
+                    // The largest |product| is wanted for the cap's tier.  Without distances it serves for the maximum
+                    // too, where no score can be far from 0: the cap of it is then a bound, at most 2 kNear above the
+                    // largest score, and weights of 2^-24 of the largest stay normal numbers.
+                    auto bound = [&] {
+                        if (!__all_sync(0xffffffffu, !valid || fminf(most * c, A.sc.cap_log2) <= kNear)) return false;
+                        mb = cap_any(A.sc, c, most);
+                        return true;
+                    };
                     bool straight = false;  // the block is done
+                    bool have = false;      // mb is
                     if (kLong && clear) {
                         tc_after();
                         __syncwarp();
@@ -738,6 +749,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                         // weights of 2^-24 of the largest stay normal numbers).
                         auto largest = [&](uint32_t (&x)[64], int k0) {
                             if (kCap) most = fmaxf(most, absmax(x));
+                            if (kAbs) return -INFINITY;
                             float y = max_of(x);
                             if (kX) y = kCap ? cap_any(A.sc, c, y) : y * c;
                             if (kBias) y += bias_most<64>(sl, (float)(k0 - pos));
@@ -749,7 +761,8 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                         tmem_ld64(tS + 64, hi);
                         mb = fmaxf(mb, largest(hi, t0 + 64));
                         if (kCap) tier = cap_tier(A.sc, valid ? most : 0.f);
-                        straight = tier == 0 && !both;
+                        have = !kAbs || bound();
+                        straight = have && tier == 0 && !both;
                         if (straight) {
                             follow(mb);
                             const float mc = m == -INFINITY ? 0.f : m * mu;
@@ -772,6 +785,21 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                     } else if (busy) {
                         tc_after();
                         __syncwarp();
+                        if constexpr (kAbs) {
+#pragma unroll 1
+                            for (int q = qa; q <= qb; q++) {
+                                const int k0 = t0 + 32 * q;
+                                if (!some(k0)) continue;
+                                uint32_t x[32];
+                                tmem_ld32(tS + 32 * q, x);
+                                mask(x, k0, kIgnored);
+                                most = fmaxf(most, absmax(x));
+                            }
+                            tier = cap_tier(A.sc, valid ? most : 0.f);
+                            have = bound();
+                        }
+                    }
+                    if (busy && !have) {
 #pragma unroll 1
                         for (int q = qa; q <= qb; q++) {
                             const int k0 = t0 + 32 * q;
@@ -779,7 +807,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             uint32_t x[32];
                             tmem_ld32(tS + 32 * q, x);
                             mask(x, k0, kIgnored);
-                            if (kCap) most = fmaxf(most, absmax(x));
+                            if (kCap && !kAbs) most = fmaxf(most, absmax(x));
                             // Of the products, the largest: tanh is monotone, and a distance's term is at most
                             // bias_most.  That bound of the maximum is at most 31 |sl| above it (96 where it is
                             // taken, so that weights of 2^-24 of the largest stay normal numbers).
@@ -790,7 +818,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                             }
                             mb = fmaxf(mb, y);
                         }
-                        if (kCap) tier = cap_tier(A.sc, valid ? most : 0.f);
+                        if (kCap && !kAbs) tier = cap_tier(A.sc, valid ? most : 0.f);
                         if (kBias && steep) {  // key by key
                             mb = -INFINITY;
 #pragma unroll 1
@@ -1030,9 +1058,9 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
         }
         if (!joined && tid == 0) write_join(A, blockIdx.x, seq, unit, nullptr);
     } else if (kLong && warp >= 10) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else if (warp == 8) {
-        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------------------------------------------------------- tensor core
         constexpr uint32_t idS = tc_idesc(128, kTcBlk, 0), idO = tc_idesc(128, HDP, 1);
         const int ksteps = (A.hd + 15) / 16;
@@ -1212,7 +1240,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
         }
         __syncwarp();
     } else if (warp == 9) {
-        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if constexpr (kLong) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------------------------------------------------------- TMA producer
         if constexpr (kSpans) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // masked_layout's scratch
         uint32_t st = 0, ph = 0, issued = 0;  // ring position; stages filled so far
