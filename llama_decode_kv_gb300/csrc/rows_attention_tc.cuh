@@ -36,16 +36,18 @@
 //   * A quarter of 32 keys is the body of a loop.  The scored softmax as straight code pushes the other
 //     roles' instructions out of the cache (no_instruction was the first stall by far), and these
 //     then feed the tensor core late: documents of up to 1,500 in prompts of up to 6,000, 250 us as
-//     straight code, 196 in quarters.  Long items get over it, so they have a variant with straight code
+//     straight code, 205 in quarters (183 now).  Long items get over it, so they have a variant with straight code
 //     for blocks without masks (kStraight; the rule and its figures stand in rows_op.cu).
 //   * tanh is a polynomial while |x| is at most the cap, its degree by the warp's largest |x|
 //     (cap_tier), the branch outside the loops: inside, the compiler computes both sides for every key
 //     (64 sequences as above 992 us, outside 334).
 //   * The maximum is the score of the largest product plus a bound of the distance's term, so that one
-//     pass over a quarter finds it; slopes too steep for that take it key by key.
+//     pass over a quarter finds it; slopes too steep for that take it key by key.  Without distances the
+//     cap of the largest |product|, which cap_tier needs anyhow, serves where it is small (documents 193 us
+//     -> 183, a prompt of 8,192 588 -> 548).
 // What bounds them now: decode steps HBM; prompts and chunks with masks the same chain of hand-offs as
 // plain rows, its softmax part longer by the cap's five to seven instructions for two keys (a prompt of
-// 8,192: 588 us with a cap, 430 without, plain 356), and items' ends where documents are short.
+// 8,192: 536 us with a cap, 430 without, plain 356), and items' ends where documents are short.
 //
 //   warps 0-3, 4-7  softmax of tile 0 and of tile 1, a thread per row: S from tensor memory, the
 //                   causal mask where the block needs one, the running maximum, P = 2^(S - m) as
@@ -85,8 +87,8 @@
 namespace slm {
 
 // Threads of a CTA: ten warps; with kStraight twelve (two of them idle), so that the softmax groups can
-// take registers over from the other roles: 2 x 128 x 208 + 128 x 88 = 384 x 168, what such a CTA is
-// launched with.
+// take registers over from the other roles: 2 x 128 x 216 + 128 x 72 = 384 x 168, what such a CTA is
+// launched with (a prompt of 8,192 with a cap 535 us; with 224 / 56 549, 208 / 88 548, 192 / 120 578).
 __host__ __device__ constexpr int tc_threads(int score) { return score & kStraight ? 384 : 320; }
 constexpr int kTcBlk = 128;                 // positions per block
 constexpr int kPanel = 128 * 128;           // bytes of [128 rows][64 bf16]

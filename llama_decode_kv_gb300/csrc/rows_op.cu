@@ -243,9 +243,9 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     }
     // Items of many blocks, as far as the sizes tell (a window and the table, or the average prompt;
     // documents, and items of one split tile, are short).  Straight / looped, us, 32 / 8 heads of 128, cap
-    // 30: a prompt of 8,192 588 / 818, of 2,048 73 / 78, 16 of 512 117 / 101, 64 of 128 72 / 55; chunks of
-    // up to 512 over 16,000 positions with a window of 4,096 113 / 129; documents of up to 1,500 in
-    // prompts of up to 6,000 220 / 202; a step of 64 sequences, window 4,096, 172 / 163.
+    // 30: a prompt of 8,192 537 / 707, of 2,048 71 / 71, 16 of 512 116 / 97, 64 of 128 70 / 53; chunks of
+    // up to 512 over 16,000 positions with a window of 4,096 106 / 117; documents of up to 1,500 in
+    // prompts of up to 6,000 215 / 183; a step of 64 sequences, window 4,096, 174 / 162.
     const long long reach = std::min(longest, a.kv.table ? longest : (long long)a.rows / a.nseq);
     const bool long_items = sc && reach >= 2048 && !sc->first && (long long)a.rows * a.G > 32LL * a.nseq;
     cudaError_t e;

@@ -27,7 +27,7 @@
 // 256 rows of 128,256 fp32 logits with every kind of cut take 90 us, of which HBM needs 19; the rest is the
 // latency of a row's steps, one barrier behind the other, which three CTAs per SM hide in part (a CTA a row,
 // lists ranked by comparing all pairs, 252; in slices, lists sorted, 140; loops without branches 90; the
-// general way for all 3,479).  One row of 49,152 with top-p takes 21 us on eight SMs (61, 28 and 23).
+// general way for all 3,479).  One row of 49,152 with top-p takes 21 to 24 us on eight SMs (61, 28 before).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
