@@ -507,7 +507,7 @@ inline size_t tc_lengths_bytes(int nseq, bool spans) {
 
 __host__ __device__ constexpr size_t tc_fixed_bytes(int HDP, int stages, bool spans) {
     return 1024 + (size_t)(2 + stages) * (HDP / 64) * kPanel + (sizeof(TcBars) + 15) / 16 * 16 +
-           (HDP == 64 ? 1024 + (spans ? 3072 : 0) : spans ? 256 : 0);
+           (HDP == 64 ? 1024 + (spans ? 2 * 384 * sizeof(float) : 0) : spans ? 256 : 0);
 }
 
 // ------------------------------------------------------------------ the kernel
