@@ -735,10 +735,11 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
                     };
                     // The largest |product| is wanted for the cap's tier.  Without distances it serves for the maximum
                     // too, where no score can be far from 0: the cap of it is then a bound, at most 2 kNear above the
-                    // largest score, and weights of 2^-24 of the largest stay normal numbers.
+                    // largest score, and weights of 2^-24 of the largest stay normal numbers.  That holds for a row
+                    // that sees some of these keys; of one that does not, `most` says nothing and there is no maximum.
                     auto bound = [&] {
                         if (!__all_sync(0xffffffffu, !valid || fminf(most * c, A.sc.cap_log2) <= kNear)) return false;
-                        mb = cap_any(A.sc, c, most);
+                        if (max(from, t0 + 32 * qa) < min(seen, t0 + 32 * qb + 32)) mb = cap_any(A.sc, c, most);
                         return true;
                     };
                     bool straight = false;  // the block is done
