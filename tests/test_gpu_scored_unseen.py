@@ -74,7 +74,9 @@ def test_masks(slm, dtype, H, KV, hd, size, cap, masks, new, ctx):  # noqa: F811
 def test_two_levels(slm, H, KV, hd, cap):  # noqa: F811
     """Documents in turns of scores near 20 and near -100: rows of one warp take their maximum from a bound
     that holds for one document and not for the other."""
-    b = low(BF16, H, KV, hd, [400, 20], [44, 700], 100.0)  # a warp has the positions 380 to 387, a document ends at 383
+    # A warp has the positions 380 to 387, and a document ends at 383, with a block.  Tables of up to 512
+    # positions leave items whole.
+    b = low(BF16, H, KV, hd, [400, 20], [44, 100], 100.0)
     first = []
     for s, keys in enumerate(b.seq_k):
         L = keys.shape[0]
