@@ -541,10 +541,12 @@ int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, i
  *
  * Free pages are a stack: free_pages[0 .. free_count - 1], the top last.  The pages of ended
  * sequences (page_table[s][0 .. ceil(seq_len[s] / page_size) - 1]) are put on it in the order
- * (sequence, block); then the pages of the new blocks of positions, ceil(seq_len / page_size) to
- * ceil((seq_len + new_len) / page_size) - 1 of every other sequence, are taken from its top in the
- * same order and written into page_table.  Every page belongs to one sequence.  No other entry of
- * page_table is written, an ended sequence's neither.
+ * (sequence, block).  Pages that the caller gave back before, such as those that a window has left
+ * behind, are not theirs any more: a caller that does so makes their entries negative, in front of a
+ * sequence's others, and they are passed over.  Then the pages of the new blocks of positions,
+ * ceil(seq_len / page_size) to ceil((seq_len + new_len) / page_size) - 1 of every other sequence, are
+ * taken from its top in the same order and written into page_table.  Every page belongs to one
+ * sequence.  No other entry of page_table is written, an ended sequence's neither.
  *
  *   row_start [nseq + 1], ctx_len [nseq]   what slm_rows takes: row_start from 0, ctx_len = seq_len
  *                                          (0 where the sequence ends)
@@ -561,7 +563,8 @@ int slm_attention_prompt(const slm_rows *rows, int32_t dtype, int32_t n_heads, i
  * status says why: SLM_ROWS_POOL (too few free pages, or more than n_pages of them), SLM_ROWS_LENGTH
  * (a seq_len is negative, a sequence outgrows its page table or 2^31 - 256 positions, or there are
  * more rows than `rows`).
- * A page id outside [0, n_pages) sets SLM_ROWS_PAGE, is passed on as it is, and its slots are -1.
+ * Any other page id outside [0, n_pages) that is put on the stack, taken from it or looked up for a
+ * slot sets SLM_ROWS_PAGE, is passed on as it is, and its slots are -1.
  * nseq in [1, 1024], rows in [0, 2^30], table_ld and n_pages at least 1, page_size a power of two in
  * [16, 2^20].
  */
@@ -610,7 +613,8 @@ int slm_kv_append_axes(const slm_kv_cache *cache, const slm_rows *rows, int32_t 
  *   window: positions that a row sees at most, its own the last of them.
  * Where row_start descends (SLM_ROWS_LENGTH), the results of the whole call are meaningless.
  * Positions before the smallest `from` of a sequence's rows are not read, nor are their page-table
- * entries: their pages may have been given back.  The other arguments, the requirements, the
+ * entries: their pages may have been given back (with negative entries in their place, where
+ * slm_rows_plan is to end the sequence).  The other arguments, the requirements, the
  * workspace and the rounding are those of slm_attention_paged and slm_attention_prompt; non-finite
  * values at positions that some rows of a sequence see may reach its other rows that see something.
  * The scores stay fp32, the cap's tanh included.

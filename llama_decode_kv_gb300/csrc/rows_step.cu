@@ -8,6 +8,10 @@
 // given back and is looked up in its sequence's table row, so nobody reads what another thread
 // writes and one launch does.
 //
+// A sequence under a window may have lost its first pages before it ends: its table row begins with
+// negative entries then, and as those stand in front of the others, a binary search of the row counts
+// them.  The row's first entry, which says whether there is one to count, is read beside the lengths.
+//
 // Latency bounds it: the lengths, three running sums over at most 1,024 sequences (one per thread),
 // then for every row a search of its sequence, its page and two stores.  Up to eight CTAs, each with
 // the sums of its own, share the rows; they are a cluster, so that all have read the counters before
@@ -29,9 +33,10 @@ constexpr int kStepThreads = 1024;
 static_assert(kStepThreads >= kRowsMaxSeqs, "a thread per sequence");
 constexpr int kStepCtas = 8;
 
-// What stands in shared memory: running sums before each sequence, and its length.
+// What stands in shared memory: running sums before each sequence, its length, and its pages that were
+// given back before it ends.
 struct StepShared {
-    int row[kRowsMaxSeqs + 1], need[kRowsMaxSeqs + 1], back[kRowsMaxSeqs + 1], len[kRowsMaxSeqs];
+    int row[kRowsMaxSeqs + 1], need[kRowsMaxSeqs + 1], back[kRowsMaxSeqs + 1], len[kRowsMaxSeqs], gone[kRowsMaxSeqs];
     long long warp[3][32];
 };
 
@@ -77,15 +82,29 @@ __device__ __forceinline__ void scan3(long long (&v)[3], long long (*warp)[32]) 
     }
 }
 
+// How many of a table row's n entries, of which the first is negative, are: they stand in front.
+__device__ __forceinline__ int negative_entries(const int *row, int n) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (row[mid] < 0)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return hi;
+}
+
 __global__ void __launch_bounds__(kStepThreads) rows_step_kernel(const __grid_constant__ StepArgs A) {
     __shared__ StepShared S;
     const int tid = threadIdx.x, cta = blockIdx.x, ctas = gridDim.x, shift = A.page_shift;
     pdl_wait();
     pdl_trigger();
     const int F = *A.free_count;
-    int n = 0, c = 0;
+    int n = 0, c = 0, first = 0;
     bool ends = false, bad = false;
     if (tid < A.nseq) {
+        first = A.page_table[(size_t)tid * A.table_ld];
         n = A.new_len[tid];
         c = A.seq_len[tid];
         ends = n < 0;
@@ -95,7 +114,8 @@ __global__ void __launch_bounds__(kStepThreads) rows_step_kernel(const __grid_co
     const int c0 = bad ? 0 : c, n0 = bad ? 0 : n;  // inside the table, so that no sum overflows
     const int held = (int)(((long long)c0 + (1 << shift) - 1) >> shift);
     const int all = (int)(((long long)c0 + n0 + (1 << shift) - 1) >> shift);
-    const int need = ends ? 0 : all - held, back = ends ? held : 0;
+    const int gone = ends && held > 0 && first < 0 ? negative_entries(A.page_table + (size_t)tid * A.table_ld, held) : 0;
+    const int need = ends ? 0 : all - held, back = ends ? held - gone : 0;
     long long v[3] = {n0, need, back};
     scan3(v, S.warp);
     const long long rows = S.warp[0][31], T = S.warp[1][31], R = S.warp[2][31];
@@ -105,6 +125,7 @@ __global__ void __launch_bounds__(kStepThreads) rows_step_kernel(const __grid_co
         S.need[tid] = (int)(v[1] - need);
         S.back[tid] = (int)(v[2] - back);
         S.len[tid] = c;
+        S.gone[tid] = gone;
     }
     const bool length = __syncthreads_or(bad) || rows > A.rows;
     const bool pool = F < 0 || F > A.n_pages || (long long)F + R > A.n_pages || T > (long long)F + R;
@@ -136,13 +157,17 @@ __global__ void __launch_bounds__(kStepThreads) rows_step_kernel(const __grid_co
     // the k-th page given back, and page j of the step
     auto given = [&](int k) {
         const int s = owner_of(S.back, A.nseq, k);
-        return A.page_table[(size_t)s * A.table_ld + (k - S.back[s])];
+        return A.page_table[(size_t)s * A.table_ld + S.gone[s] + (k - S.back[s])];
     };
     auto taken = [&](int j) {
         const long long e = F + R - 1 - j;
         return e >= F ? given((int)(e - F)) : A.free_pages[e];
     };
-    for (int k = t0; k < R; k += step) A.free_pages[F + k] = given(k);
+    for (int k = t0; k < R; k += step) {
+        const int page = given(k);
+        if (page < 0 || page >= A.n_pages) atomicOr(A.status, SLM_ROWS_PAGE);
+        A.free_pages[F + k] = page;
+    }
     for (int j = t0; j < T; j += step) {
         const int s = owner_of(S.need, A.nseq, j), page = taken(j);
         if (page < 0 || page >= A.n_pages) atomicOr(A.status, SLM_ROWS_PAGE);
