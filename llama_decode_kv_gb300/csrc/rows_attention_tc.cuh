@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(tc_threads(SCORE), 1) rows_tc_kernel(const __g
     // an item of at most 32 rows is split by keys over the four warps of a group, and worked on twice
     // over whatever its heads' width
     auto view = [&](const SeqRows &sr, const RowsPiece &p, int i, int prefix) {
-        const bool split = kSpans && (sr.n - p.t * PT) * G <= 32;
+        const bool split = kSpans && fits_rows(sr.n - p.t * PT, G, 32);
         TileView v = tile_view(sr, p, TT, PT, i, prefix, kTwin || split);
         v.split = split;
         return v;

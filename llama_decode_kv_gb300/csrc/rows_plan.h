@@ -99,6 +99,9 @@ struct RowsGeom {
 
 SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
 
+// Whether `left` tokens of G heads are at most `rows` rows (a sequence's rows may be more than 2^31).
+SLM_HD bool fits_rows(int left, int G, int rows) { return left <= rows / G; }
+
 SLM_HD int item_blocks(const RowsGeom &g, int ctx, int n, int t) {
     const int left = n - t * g.PT, end = left < g.PT ? n : n - left + g.PT;
     return (int)(((unsigned)ctx + (unsigned)end + (1u << g.shift) - 1) >> g.shift);
