@@ -205,8 +205,8 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     // 21.2.  `longest` is what the caller's table (for prompts: the packed rows) could hold, since the
     // lengths are not known here: a short context under a wide table is cut all the same (one token
     // over 250 positions, table for 32,768: 9.1 us).
-    // A window bounds what an item sees besides.
-    if (sc && sc->window) longest = std::min(longest, (long long)sc->window + t.geom.PT);
+    // A window bounds what an item sees besides; prefixes may reach to a sequence's last row all the same.
+    if (sc) longest = most_seen(longest, sc->window, sc->prefix_len != nullptr, t.geom.PT, a.rows);
     a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
     a.lost = g_lost.load(std::memory_order_relaxed);

@@ -266,6 +266,14 @@ SLM_HD RowsSpan item_span(const RowsGeom &g, const SeqRows &r, const RowsMask &m
     return s;
 }
 
+// Positions that an item can see at most, of sequences of at most `longest` positions in a call of `rows`
+// rows.  Behind a window an item's span begins at most window - 1 positions before its first row and ends
+// with its last row, or with the prefix, which ends with the sequence's last row at the latest.
+SLM_HD long long most_seen(long long longest, int window, bool prefixes, int PT, int rows) {
+    const long long most = (long long)window + (prefixes ? rows : PT);
+    return window && most < longest ? most : longest;
+}
+
 // The item that holds a unit of the line.
 struct RowsStart {
     int s, g, t;
