@@ -326,24 +326,32 @@ def kv_append_axes(k, v, k_cache, v_cache, page_table, row_start, ctx_len, statu
 
 
 def rows_plan(new_len, seq_len, page_table, page_size, free_pages, free_count, row_start, ctx_len, positions, slots,
-              seq_len_out, free_count_out, status, stream=None) -> None:
+              seq_len_out, free_count_out, status, stream=None, rows=None) -> None:
     """slm_rows_plan over torch tensors of the current device: row_start [sequences + 1], ctx_len,
     positions [rows], slots [rows] (int64) of a step that brings new_len[s] rows after seq_len[s]
     positions (negative: the sequence ends), page_table [sequences][entries] with the new pages,
     taken from the stack free_pages [pages] of free_count[0] entries; seq_len_out and
     free_count_out after the step (they may be seq_len and free_count).  All int32 but slots.
+    positions and slots may be None; where both are, `rows` says how many rows the step may have.
     Raises SlmError / ValueError."""
     if _INT is None:
         _torch_names()
     nseq, ld = page_table.shape
-    rows = positions.shape[0]
-    if slots.dtype is not _I64T or slots.shape != (rows,) or not slots.is_contiguous():
-        raise ValueError(f"slots: {tuple(slots.shape)} {slots.dtype}, expected contiguous int64 ({rows},)")
+    if rows is None:
+        if positions is None and slots is None:
+            raise ValueError("rows is needed without positions and slots")
+        rows = (slots if positions is None else positions).shape[0]
+    slots_ptr = None
+    if slots is not None:
+        if slots.dtype is not _I64T or slots.shape != (rows,) or not slots.is_contiguous():
+            raise ValueError(f"slots: {tuple(slots.shape)} {slots.dtype}, expected contiguous int64 ({rows},)")
+        slots_ptr = slots.data_ptr()
     n_pages = free_pages.shape[0]
     pool = _PACK_POOL(_ints(page_table, "page_table", nseq, ld), _list(free_pages, "free_pages", n_pages),
                       _list(free_count, "free_count", 1), _list(seq_len, "seq_len", nseq), nseq, ld, n_pages, page_size)
     rc = slm_rows_plan(pool, _list(new_len, "new_len", nseq), rows, _list(row_start, "row_start", nseq + 1),
-                       _list(ctx_len, "ctx_len", nseq), _list(positions, "positions", rows), slots.data_ptr(),
+                       _list(ctx_len, "ctx_len", nseq), None if positions is None else _list(positions, "positions", rows),
+                       slots_ptr,
                        _list(seq_len_out, "seq_len_out", nseq), _list(free_count_out, "free_count_out", 1),
                        _list(status, "status", 1), _rows_stream(stream, new_len))
     if rc:
