@@ -205,8 +205,12 @@ static int run_attention(RowsArgs &a, const RowsTiling &t, int dtype, long long 
     // 21.2.  `longest` is what the caller's table (for prompts: the packed rows) could hold, since the
     // lengths are not known here: a short context under a wide table is cut all the same (one token
     // over 250 positions, table for 32,768: 9.1 us).
-    // A window bounds what an item sees besides; prefixes may reach to a sequence's last row all the same.
-    if (sc) longest = most_seen(longest, sc->window, sc->prefix_len != nullptr, t.geom.PT, a.rows);
+    // A window bounds what an item sees besides.  Prefixes may reach to a sequence's last row all the same,
+    // and are as unknown here as the lengths: they count where that may be 2,048 positions.  Whole / cut, 32
+    // / 8 heads of 128, a window of 400 and a prefix of 30 positions, half the rows and all: 8,000 rows 101 /
+    // 138 us, 250 / 241 and 635 / 484, 2,000 rows 36 / 48, 48 / 55 and 82 / 72; 8 heads on one, 8,000 rows,
+    // 34 / 47, 94 / 75 and 263 / 137; three chunks of 300 behind 16,000 positions, up to 100, 21 / 30.
+    if (sc) longest = most_seen(longest, sc->window, sc->prefix_len && (long long)sc->window + a.rows >= 2048, t.geom.PT, a.rows);
     a.geom.split = longest > (long long)(on_tensor_cores(dtype, a.hd) ? 4 : 2) << t.geom.shift;
     a.G = a.H / a.KV;
     a.lost = g_lost.load(std::memory_order_relaxed);
