@@ -100,8 +100,8 @@ struct RowsGeom {
 SLM_HD int item_count(const RowsGeom &g, int n) { return (n + g.PT - 1) / g.PT; }
 
 // Whether `left` tokens of G heads are at most `rows` rows (all of a sequence's may be more than 2^31, so
-// the tokens are compared first).
-SLM_HD bool fits_rows(int left, int G, int rows) { return left <= rows && left * G <= rows; }
+// the tokens are cut first).
+SLM_HD bool fits_rows(int left, int G, int rows) { return (left <= rows ? left : rows + 1) * G <= rows; }
 
 SLM_HD int item_blocks(const RowsGeom &g, int ctx, int n, int t) {
     const int left = n - t * g.PT, end = left < g.PT ? n : n - left + g.PT;
