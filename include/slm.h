@@ -655,6 +655,8 @@ int slm_attention_prompt_scored(const slm_rows *rows, const slm_scores *scores, 
  *     [rows].
  *   Probabilities are added up as whole numbers of 2^-40 of the largest, so the result does not
  *   depend on the order of the additions.  rows = 0 does nothing.
+ *   A top_k above 1,024 or about vocab / 16 (and below vocab) takes several times as long as others; so
+ *   may a top_k where logits are masked out by a large negative number and not by -infinity.
  */
 int slm_sample_rows(int32_t rows, int32_t vocab, int32_t dtype, const void *logits, int64_t ld, const float *temperature,
                     const int32_t *top_k, const float *top_p, const float *min_p, const float *uniforms,

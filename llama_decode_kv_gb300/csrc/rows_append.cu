@@ -18,7 +18,8 @@
 // 8,000 rows of 48 heads of 64, fp32 to bf16: 30.7 us = 6.0 TB/s, 88% of the copy rate, in a captured
 // graph, 31.5 us through the binding; one row 2.5 us, which is the chain of lookups.  With positions of
 // three axes (16 prompts of up to 1,024 rows, the same heads and types, through the binding) 30.5 us,
-// 73% of the copy rate: a row's positions are one more dependent load before its rotation can be looked up.
+// 73% of the copy rate: a row's positions are one more dependent load in front of the barrier behind which
+// all of its units are loaded, the values too, although their addresses do not depend on it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -15,10 +15,11 @@
 // Latency bounds it: the lengths, three running sums over at most 1,024 sequences (one per thread),
 // then for every row a search of its sequence, its page and two stores.  Up to eight CTAs, each with
 // the sums of its own, share the rows; they are a cluster, so that all have read the counters before
-// one of them writes them (they may be overwritten in place).  256 sequences with a row each take 3.7 us in a
-// captured graph and 8.9 through the binding (the call on the host); 96 sequences with 41,500 rows 9.8 both
-// ways.  Searching four rows at a time (11.4), giving a warp adjacent rows that keep the last owner (10.3) and
-// reading the written table instead of finding a page twice (10.1) did not make that shorter.
+// one of them writes them (they may be overwritten in place).  256 sequences with a row each take 3.8 us in a
+// captured graph and 9.1 through the binding (the call on the host); 96 sequences with 41,500 rows 10.1 and
+// 10.3.  Where that stood at 9.8, searching four rows at a time (11.4), giving a warp adjacent rows that keep
+// the last owner (10.3) and reading the written table instead of finding a page twice (10.1) did not make it
+// shorter.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
